@@ -59,6 +59,17 @@ extern "C" {
 /* ---- dtype codes and flags ---------------------------------------------- */
 #define GALE_F16 1
 #define GALE_F32 2
+#define GALE_BF16 3               /* only where an entry point says so */
+
+/* Element formats of MX (microscaled) numbers, see gale_mx_quantize. */
+#define GALE_MX_E2M1 1            /* 4 bits: sign, 2 exponent bits, 1 mantissa bit; largest 6 */
+#define GALE_MX_E4M3 2            /* 8 bits: sign, 4 exponent bits, 3 mantissa bits; largest 448 */
+
+/* Scores and group values of gale_route_scored. */
+#define GALE_SCORE_SOFTMAX 1
+#define GALE_SCORE_SIGMOID 2
+#define GALE_GROUP_MAX  1         /* a group is worth its best expert */
+#define GALE_GROUP_TOP2 2         /* a group is worth the sum of its two best experts */
 
 #define GALE_X_ROTATED    0x1u   /* x is already H.x (fp32 or fp16); skip the rotation */
 #define GALE_X_PREPARED   0x2u   /* gale_expert_gemv: x holds records from gale_prepare_activations */
@@ -98,6 +109,10 @@ extern "C" {
 #define GALE_MAX_TOPK         8
 #define GALE_MAX_EXPERTS    512
 #define GALE_MAX_DECODE_TOKENS 64 /* gale_moe_layer_fwd decode path limit */
+#define GALE_MX_BLOCK        32   /* columns per MX scale */
+#define GALE_MX_GROUP       128   /* MX rows are stored padded to whole groups of this many columns */
+#define GALE_MX_MAX_COLS  65536   /* columns of an MX row */
+#define GALE_MAX_GROUPS      64   /* expert groups of gale_route_scored */
 
 /*
  * Device layout of one packed matrix (produced by gale_pack_*), rows % 16 == 0,
@@ -383,6 +398,98 @@ size_t gale_route_workspace_bytes(int32_t n_tok, int32_t n_experts);
 int gale_route_topk(const float* logits, int32_t n_tok, int32_t n_experts, int32_t top_k,
                     int32_t* topk_idx, float* topk_w, int32_t* offsets, int32_t* perm,
                     void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* ---- around the routed layer: norm, scored routing, MX linear layers -------------- */
+
+/* The routed layer of gale_moe_layer_fwd_routed with each token's experts AND their weights given
+ * (the outputs of gale_route_scored, or any other router): y[t] = sum over slots j, in order, of
+ * topk_w[t][j] * FFN_{topk_idx[t][j]}(x[t]).  topk_idx: int32 [n_tok][top_k]; topk_w: fp32
+ * [n_tok][top_k].  A slot with no expert has index -1 and weight 0 (an index outside
+ * [0, n_experts) is clamped into it, so such a slot still computes an expert and adds 0 times its
+ * output).  Same workspace, paths and flags as gale_moe_layer_fwd; fp16 x and y. */
+int gale_moe_layer_fwd_given(int32_t hidden, int32_t inter, const gale_expert* experts_dev,
+                             int32_t n_experts, const int32_t* topk_idx, const float* topk_w, int32_t top_k,
+                             const void* x, int32_t n_tok, void* y, void* ws, size_t ws_bytes, uint32_t flags,
+                             hipStream_t stream);
+
+/* Expert choice from scores.  For each token, with its logits l[0..n_experts):
+ *   s[e] = softmax(l)[e] or sigmoid(l[e])  (score),   c[e] = s[e] + bias[e]  (bias: fp32
+ *          [n_experts], or NULL for none; it moves the choice, never the weights);
+ *   the experts form n_groups groups of n_experts / n_groups consecutive ones; the keep_groups
+ *          groups of the largest value (group_rule: the largest c of the group, or the sum of its
+ *          two largest) stay, ties to the lower group;
+ *   the top_k experts of these groups by (c descending, index ascending) fill the slots in
+ *          that order, with weights w = scale * s, divided by the sum of the token's chosen s
+ *          when renormalize != 0 (all 0 if that sum is 0).
+ * An expert whose logit is NaN or -infinity, or whose bias is, is never chosen and has score 0;
+ * a group of only such experts never stays.  Slots left without an expert get index -1 and
+ * weight 0.  +infinity logits count as the largest finite fp32 number.  Without a bias the
+ * order of c is taken from the logits themselves (the scores have the same order), otherwise
+ * scores, sums and group values are computed and compared in 64 bits, so that the choice does
+ * not hang on a rounding; equal values are ties.
+ * logits: [n_tok] rows of n_experts values of logits_dtype (GALE_F32, GALE_F16 or GALE_BF16),
+ * logits_stride elements apart.  topk_idx: int32 [n_tok][top_k]; topk_w: fp32 [n_tok][top_k].
+ * n_experts <= GALE_MAX_EXPERTS and a multiple of n_groups <= GALE_MAX_GROUPS, 1 <= keep_groups <=
+ * n_groups, 1 <= top_k <= GALE_MAX_TOPK and top_k <= keep_groups * (n_experts / n_groups).
+ * n_tok may be 0 (nothing is enqueued). */
+int gale_route_scored(const void* logits, int32_t logits_dtype, int64_t logits_stride, int32_t n_tok,
+                      int32_t n_experts, const float* bias, int32_t score, int32_t n_groups, int32_t keep_groups,
+                      int32_t group_rule, int32_t top_k, int32_t renormalize, float scale, int32_t* topk_idx,
+                      float* topk_w, hipStream_t stream);
+
+/* MX numbers (microscaling): a row of cols numbers is cut into blocks of GALE_MX_BLOCK = 32 columns;
+ * column k is element[k] * 2^(scale[k / 32] - 127), elements of fmt GALE_MX_E2M1 (two per byte, the
+ * even column in the low nibble) or GALE_MX_E4M3, one scale byte per block (255: the block is NaN).
+ * Rows are stored back to back, padded to whole groups of GALE_MX_GROUP = 128 columns: codes
+ * [rows][gale_mx_code_bytes(fmt, cols)], scales [rows][gale_mx_scale_bytes(cols)].  Codes and scales
+ * behind column cols are zero bytes: every writer below stores them, and gale_mx_gemm relies on it.
+ * codes are 16-byte, scales 4-byte aligned. */
+size_t gale_mx_code_bytes(int32_t fmt, int32_t cols);    /* bytes of a row of codes (0: bad arguments) */
+size_t gale_mx_scale_bytes(int32_t cols);                /* bytes of a row of scales */
+
+/* x -> MX.  The scale of a block is the smallest power of two (at least 2^-127) that the block's
+ * largest magnitude divided by it does not pass the format's largest number, so nothing
+ * saturates; elements are rounded to nearest even.  A block that holds an infinity or a NaN becomes
+ * a NaN block (scale 255, codes 0).  x: [rows] rows of cols values of x_dtype (GALE_F16, GALE_BF16,
+ * GALE_F32), x_stride elements apart.  rows may be 0. */
+int gale_mx_quantize(const void* x, int32_t x_dtype, int64_t x_stride, int64_t rows, int32_t cols, int32_t fmt,
+                     uint8_t* codes, uint8_t* scales, hipStream_t stream);
+
+/* The same of silu(g) * u, computed in fp32 and rounded only to the element: rows of x hold g in
+ * columns [0, cols) and u in [cols, 2 cols) (the output of one product with gate and up rows
+ * stacked). */
+int gale_mx_swiglu_quantize(const void* x, int32_t x_dtype, int64_t x_stride, int64_t rows, int32_t cols,
+                            int32_t fmt, uint8_t* codes, uint8_t* scales, hipStream_t stream);
+
+/* MX -> the numbers, rounded once to y_dtype (exact in fp32).  y: [rows] rows of cols values,
+ * y_stride elements apart. */
+int gale_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t fmt, int64_t rows, int32_t cols,
+                       void* y, int32_t y_dtype, int64_t y_stride, hipStream_t stream);
+
+/* y = A . W^T (+ add): y[i][j] = sum_k A[i][k] W[j][k] (+ add[i][j]), products of MX numbers
+ * exact, sums in fp32, one rounding to y_dtype.  A: m MX rows of k columns of a_fmt (activations); W:
+ * n MX rows of k columns of GALE_MX_E2M1 (a weight matrix [out, in]).  y: [m] rows of n values of
+ * y_dtype (GALE_F16, GALE_BF16, GALE_F32), y_stride elements apart; add: the same type, add_stride apart,
+ * or NULL; add may be y itself with the same stride.  A NaN block makes every y that reads it
+ * NaN.  m <= GALE_MAX_ROWS (0: nothing is enqueued), 1 <= n <= GALE_MAX_ROWS,
+ * 1 <= k <= GALE_MX_MAX_COLS.  A row of y hangs on its own row of A only, and equal calls give
+ * equal bits; the order of the fp32 sums depends on m, n and k. */
+int gale_mx_gemm(int32_t m, int32_t n, int32_t k, const uint8_t* a_codes, const uint8_t* a_scales, int32_t a_fmt,
+                 const uint8_t* w_codes, const uint8_t* w_scales, const void* add, int64_t add_stride, void* y,
+                 int32_t y_dtype, int64_t y_stride, hipStream_t stream);
+
+/* Residual addition and root-mean-square norm of rows of cols values:
+ *   s = x + residual, rounded once to dtype (s = x without a residual);
+ *   y = s / sqrt(mean(s^2) + eps) * weight, in fp32 from the rounded s (what later layers read).
+ * Outputs, each optional but at least one of y and codes: sum_out = s (dtype); y rounded to y_dtype;
+ * codes and scales = the MX numbers of the unrounded y in mx_fmt (as gale_mx_quantize makes them).
+ * x, residual: [rows] rows of dtype (GALE_F16, GALE_BF16, GALE_F32), x_stride and residual_stride elements
+ * apart; weight: [cols] of weight_dtype, or NULL for ones; sum_out and y: rows back to back.
+ * sum_out may be x or residual itself when that is stored back to back.  1 <= cols <= GALE_MAX_COLS,
+ * eps >= 0; rows may be 0. */
+int gale_add_rms_norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride, int32_t dtype,
+                      int64_t rows, int32_t cols, const void* weight, int32_t weight_dtype, float eps, void* sum_out,
+                      void* y, int32_t y_dtype, int32_t mx_fmt, uint8_t* codes, uint8_t* scales, hipStream_t stream);
 
 /* Diagnostic, not a step of the method: reads `bytes` bytes at device pointer src (16-byte
  * aligned, a positive multiple of 16) once with a plain streaming kernel, 16 bytes per lane per

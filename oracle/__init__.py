@@ -3,6 +3,7 @@
 TEST INFRASTRUCTURE ONLY: imported by the tests, the smoke check and the CPU
 baseline leg of the benchmark, never by the GPU library or its Python binding.
 """
+from . import block_oracle  # noqa: F401
 from .gale_oracle import *  # noqa: F401,F403
 from .gale_oracle import (  # noqa: F401
     hadamard, rotate, unpack_signs, decode_int4, outlier_triplets, dequantize, gemv,

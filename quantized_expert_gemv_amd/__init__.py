@@ -13,5 +13,8 @@ from .binding import (  # noqa: F401
     moe_workspace_bytes, gale_tiles_flag, gale_layer_tiles_flag, GALE_OUTLIER_STAGE_SHIFT, gale_outlier_stage_flag,
     GALE_SYNC_NO_WAIT, GALE_SYNC_BYTES, GALE_ERR_SYNC, moe_workspace, sync_init, sync_status,
     decode_stack_workspace_bytes, layer_table, moe_decode_stack,
+    GALE_BF16, GALE_MX_E2M1, GALE_MX_E4M3, GALE_MX_BLOCK, GALE_MX_GROUP, GALE_SCORE_SOFTMAX, GALE_SCORE_SIGMOID,
+    GALE_GROUP_MAX, GALE_GROUP_TOP2, MXTensor, mx_quantize, mx_swiglu_quantize, mx_dequantize, mx_gemm, add_rms_norm,
+    route_scored, moe_layer_fwd_given,
 )
 from .pack_files import Pack, PackWriter, LoadedStack, load_stack, read_manifest  # noqa: F401,E402

@@ -18,7 +18,11 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgale.so")
 
 GALE_OK = 0
-GALE_F16, GALE_F32 = 1, 2
+GALE_F16, GALE_F32, GALE_BF16 = 1, 2, 3
+GALE_MX_E2M1, GALE_MX_E4M3 = 1, 2
+GALE_MX_BLOCK, GALE_MX_GROUP = 32, 128
+GALE_SCORE_SOFTMAX, GALE_SCORE_SIGMOID = 1, 2
+GALE_GROUP_MAX, GALE_GROUP_TOP2 = 1, 2
 GALE_X_ROTATED = 0x1
 GALE_X_PREPARED = 0x2
 GALE_PATH_DECODE = 0x10
@@ -118,6 +122,17 @@ _SIGS = {
                                          _P]),
     "gale_route_workspace_bytes": (_SZ, [_I32, _I32]),
     "gale_route_topk": (_I32, [_P, _I32, _I32, _I32, _P, _P, _P, _P, _P, _SZ, _P]),
+    "gale_moe_layer_fwd_given": (_I32, [_I32, _I32, _P, _I32, _P, _P, _I32, _P, _I32, _P, _P, _SZ, _U32, _P]),
+    "gale_route_scored": (_I32, [_P, _I32, _I64, _I32, _I32, _P, _I32, _I32, _I32, _I32, _I32, _I32, ctypes.c_float,
+                                 _P, _P, _P]),
+    "gale_mx_code_bytes": (_SZ, [_I32, _I32]),
+    "gale_mx_scale_bytes": (_SZ, [_I32]),
+    "gale_mx_quantize": (_I32, [_P, _I32, _I64, _I64, _I32, _I32, _P, _P, _P]),
+    "gale_mx_swiglu_quantize": (_I32, [_P, _I32, _I64, _I64, _I32, _I32, _P, _P, _P]),
+    "gale_mx_dequantize": (_I32, [_P, _P, _I32, _I64, _I32, _P, _I32, _I64, _P]),
+    "gale_mx_gemm": (_I32, [_I32, _I32, _I32, _P, _P, _I32, _P, _P, _P, _I64, _P, _I32, _I64, _P]),
+    "gale_add_rms_norm": (_I32, [_P, _I64, _P, _I64, _I32, _I64, _I32, _P, _I32, ctypes.c_float, _P, _P, _I32, _I32,
+                                 _P, _P, _P]),
     "gale_decode_stack_workspace_bytes": (_SZ, [_I32, _I32, _I32]),
     "gale_moe_decode_stack": (_I32, [_I32, _I32, _I32, _I32, _I32, _P, _P, _SZ, _U32, _P]),
     "gale_moe_decode_stack_static": (_I32, [_I32, _I32, _I32, _I32, _I32, _P, _U32, _P]),
@@ -552,3 +567,257 @@ def moe_decode_stack(hidden: int, inter: int, n_experts: int, top_k: int, layers
                                                                  layers.ptr(), ws.data_ptr(), ws.numel(), flags,
                                                                  _stream()))
     return ws
+
+
+# ----------------------------------------------------------------------------
+# around the routed layer: norm, scored routing, MX linear layers
+# ----------------------------------------------------------------------------
+_DT3 = {torch.float16: GALE_F16, torch.float32: GALE_F32, torch.bfloat16: GALE_BF16}
+
+
+def _dt3(t: torch.Tensor) -> int:
+    code = _DT3.get(t.dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {t.dtype}")
+    return code
+
+
+def _enqueue(fn: str, dev: int, *args) -> None:
+    """Call fn on the current stream of device dev, made current for the launch where it is not."""
+    if dev < 0:
+        raise ValueError("libgale compute calls take device (cuda) tensors")
+    f = getattr(_lib or lib(), fn)
+    if dev == torch.cuda.current_device():
+        st = f(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if st != GALE_OK:
+        _check(fn, st)
+
+
+def _same_device(dev: int, *ts: Optional[torch.Tensor]) -> None:
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("all tensors of a call must be on the same device")
+
+
+def _as_rows(x: torch.Tensor):
+    """(x as rows of its last dimension, rows, row stride in elements): x itself where its rows are whole and apart,
+    else a copy."""
+    if x.dim() != 2:
+        if x.dim() == 0:
+            raise ValueError("a tensor of at least one dimension is needed")
+        x = x.reshape(-1, x.shape[-1]) if x.shape[-1] else x.reshape(0, 0)
+    rows, cols = x.shape
+    if cols > 1 and x.stride(1) != 1 or rows > 1 and x.stride(0) < cols:
+        x = x.contiguous()
+    return x, rows, x.stride(0) if rows > 1 else cols
+
+
+def _out_rows(out: torch.Tensor, rows: int, cols: int) -> int:
+    """Row stride of a caller's output, which is written in place: [rows, cols], whole rows that do not overlap."""
+    if tuple(out.shape) != (rows, cols) or (cols > 1 and out.stride(1) != 1) or (rows > 1 and out.stride(0) < cols):
+        raise ValueError(f"out must be [{rows}, {cols}] with whole rows")
+    return out.stride(0) if rows > 1 else cols
+
+
+def _out_packed(out: torch.Tensor, like: torch.Tensor) -> None:
+    if out.shape != like.shape or not out.is_contiguous():
+        raise ValueError(f"an output must be contiguous and shaped {tuple(like.shape)}")
+
+
+class MXTensor:
+    """MX numbers of one matrix: rows of `cols` columns in format `fmt` (GALE_MX_E2M1 or GALE_MX_E4M3).
+
+    codes (uint8 [rows, code bytes]) and scales (uint8 [rows, scale bytes]) are laid out as gale_mx_quantize
+    writes them: rows padded with zero bytes to whole groups of 128 columns."""
+    __slots__ = ("codes", "scales", "cols", "fmt")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int, fmt: int):
+        if fmt not in (GALE_MX_E2M1, GALE_MX_E4M3):
+            raise ValueError(f"unknown MX format {fmt}")
+        g = -(-cols // GALE_MX_GROUP)
+        if cols < 1 or codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or codes.dim() != 2 or \
+                codes.shape[1] != g * (64 if fmt == GALE_MX_E2M1 else 128) or \
+                tuple(scales.shape) != (codes.shape[0], g * 4) or not codes.is_contiguous() or \
+                not scales.is_contiguous() or codes.get_device() != scales.get_device():
+            raise ValueError(f"codes and scales do not hold MX rows of {cols} columns")
+        self.codes, self.scales, self.cols, self.fmt = codes, scales, cols, fmt
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, fmt: int, device) -> "MXTensor":
+        if fmt not in (GALE_MX_E2M1, GALE_MX_E4M3):
+            raise ValueError(f"unknown MX format {fmt}")
+        g = -(-cols // GALE_MX_GROUP)
+        return cls(torch.empty(rows, g * (64 if fmt == GALE_MX_E2M1 else 128), dtype=torch.uint8, device=device),
+                   torch.empty(rows, g * 4, dtype=torch.uint8, device=device), cols, fmt)
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[0]
+
+    def dequantize(self, dtype=torch.float32) -> torch.Tensor:
+        return mx_dequantize(self, dtype)
+
+
+def _mx_out(out: Optional[MXTensor], rows: int, cols: int, fmt: int, device) -> MXTensor:
+    if out is None:
+        return MXTensor.empty(rows, cols, fmt, device)
+    if out.rows != rows or out.cols != cols or out.fmt != fmt:
+        raise ValueError(f"out must hold {rows} rows of {cols} columns in format {fmt}")
+    return out
+
+
+def mx_quantize(x: torch.Tensor, fmt: int = GALE_MX_E2M1, out: Optional[MXTensor] = None) -> MXTensor:
+    """The rows of x [..., cols] (fp16, bf16 or fp32) as MX numbers; leading dimensions become rows."""
+    x, rows, stride = _as_rows(x)
+    dev, cols = x.get_device(), x.shape[1]
+    out = _mx_out(out, rows, cols, fmt, x.device)
+    _same_device(dev, out.codes)
+    _enqueue("gale_mx_quantize", dev, x.data_ptr(), _dt3(x), stride, rows, cols, fmt, out.codes.data_ptr(),
+             out.scales.data_ptr())
+    return out
+
+
+def mx_swiglu_quantize(x: torch.Tensor, fmt: int = GALE_MX_E4M3, out: Optional[MXTensor] = None) -> MXTensor:
+    """silu(g) * u as MX numbers, g the first and u the second half of the last dimension of x [..., 2 cols]."""
+    x, rows, stride = _as_rows(x)
+    if x.shape[1] % 2:
+        raise ValueError("the last dimension holds gate and up halves of one size")
+    dev, cols = x.get_device(), x.shape[1] // 2
+    out = _mx_out(out, rows, cols, fmt, x.device)
+    _same_device(dev, out.codes)
+    _enqueue("gale_mx_swiglu_quantize", dev, x.data_ptr(), _dt3(x), stride, rows, cols, fmt, out.codes.data_ptr(),
+             out.scales.data_ptr())
+    return out
+
+
+def mx_dequantize(mx: MXTensor, dtype=torch.float32, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The numbers that MX rows stand for [rows, cols] (exact in fp32)."""
+    if out is None:
+        out = torch.empty(mx.rows, mx.cols, dtype=dtype, device=mx.codes.device)
+    dev = mx.codes.get_device()
+    _same_device(dev, out)
+    _enqueue("gale_mx_dequantize", dev, mx.codes.data_ptr(), mx.scales.data_ptr(), mx.fmt, mx.rows, mx.cols,
+             out.data_ptr(), _dt3(out), _out_rows(out, mx.rows, mx.cols))
+    return out
+
+
+def mx_gemm(a: MXTensor, w: MXTensor, add: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+            out_dtype=torch.float16) -> torch.Tensor:
+    """a . w^T (+ add): a [m, k] in either format, w [n, k] in GALE_MX_E2M1; y [m, n] of out's or add's dtype, else
+    out_dtype.  add [m, n] has y's dtype and may be out itself."""
+    if w.fmt != GALE_MX_E2M1 or w.cols != a.cols:
+        raise ValueError("w must be GALE_MX_E2M1 rows of a's columns")
+    dev = a.codes.get_device()
+    m, n = a.rows, w.rows
+    if out is None:
+        out = torch.empty(m, n, dtype=out_dtype if add is None else add.dtype, device=a.codes.device)
+    stride = _out_rows(out, m, n)
+    add_ptr, add_stride = None, 0
+    if add is not None:
+        if tuple(add.shape) != (m, n) or add.dtype != out.dtype:
+            raise ValueError(f"add must be [{m}, {n}] of y's dtype")
+        add, _, add_stride = _as_rows(add)
+        add_ptr = add.data_ptr()
+    _same_device(dev, w.codes, out, add)
+    _enqueue("gale_mx_gemm", dev, m, n, a.cols, a.codes.data_ptr(), a.scales.data_ptr(), a.fmt, w.codes.data_ptr(),
+             w.scales.data_ptr(), add_ptr, add_stride, out.data_ptr(), _dt3(out), stride)
+    return out
+
+
+def add_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor], residual: Optional[torch.Tensor] = None,
+                 eps: float = 1e-6, out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                 sum_out: Optional[torch.Tensor] = None, mx_fmt: Optional[int] = None,
+                 mx_out: Optional[MXTensor] = None):
+    """(y, s, mx): s = x + residual rounded to x's dtype (x itself without a residual), y = s / rms(s) * weight in
+    out_dtype (default: x's), mx = y as MX numbers when mx_fmt or mx_out asks for them, else None."""
+    shape = x.shape
+    dev = x.get_device()
+    rx, rows, xs = _as_rows(x)
+    cols = rx.shape[1]
+    r_ptr, rs = None, 0
+    if residual is not None:
+        if residual.shape != shape or residual.dtype != x.dtype:
+            raise ValueError("residual must have x's shape and dtype")
+        rr, _, rs = _as_rows(residual)
+        r_ptr = rr.data_ptr()
+    if weight is not None and (tuple(weight.shape) != (cols,) or not weight.is_contiguous()):
+        raise ValueError(f"weight must be contiguous with {cols} entries")
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype or x.dtype, device=x.device)
+    else:
+        _out_packed(out, x)
+    if sum_out is not None:
+        _out_packed(sum_out, x)
+        if sum_out.dtype != x.dtype:
+            raise ValueError("sum_out must have x's dtype")
+    elif residual is not None:
+        sum_out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    if mx_out is not None or mx_fmt is not None:
+        mx_out = _mx_out(mx_out, rows, cols, mx_fmt if mx_fmt is not None else mx_out.fmt, x.device)
+    _same_device(dev, residual, weight, out, sum_out, mx_out.codes if mx_out is not None else None)
+    _enqueue("gale_add_rms_norm", dev, rx.data_ptr(), xs, r_ptr, rs, _dt3(x), rows, cols, _ptr(weight),
+             GALE_F32 if weight is None else _dt3(weight), eps, _ptr(sum_out), out.data_ptr(), _dt3(out),
+             0 if mx_out is None else mx_out.fmt, None if mx_out is None else mx_out.codes.data_ptr(),
+             None if mx_out is None else mx_out.scales.data_ptr())
+    return out, x if sum_out is None else sum_out, mx_out
+
+
+_SCORES = {"softmax": GALE_SCORE_SOFTMAX, "sigmoid": GALE_SCORE_SIGMOID}
+_GROUP_RULES = {"max": GALE_GROUP_MAX, "top2": GALE_GROUP_TOP2}
+
+
+def route_scored(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: Optional[torch.Tensor] = None,
+                 n_groups: int = 1, keep_groups: int = 1, group_score: str = "top2", renormalize: bool = True,
+                 scale: float = 1.0, out=None):
+    """(topk_idx int32 [T, top_k], topk_w fp32 [T, top_k]) of logits [T, E] (fp32, fp16 or bf16): softmax or sigmoid
+    scores, an fp32 selection bias [E], the keep_groups best of n_groups expert groups, weights renormalised over
+    the chosen and scaled.  Both feed moe_layer_fwd_given.  out: the two outputs' tensors."""
+    if score not in _SCORES or group_score not in _GROUP_RULES:
+        raise ValueError(f"score is one of {list(_SCORES)}, group_score one of {list(_GROUP_RULES)}")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [n_tok, n_experts]")
+    logits, T, stride = _as_rows(logits)
+    E, dev = logits.shape[1], logits.get_device()
+    if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (E,) or not bias.is_contiguous()):
+        raise ValueError("bias must be a contiguous fp32 tensor of n_experts entries")
+    if out is None:
+        idx = torch.empty(T, top_k, dtype=torch.int32, device=logits.device)
+        w = torch.empty(T, top_k, dtype=torch.float32, device=logits.device)
+    else:
+        idx, w = out
+        if idx.dtype != torch.int32 or w.dtype != torch.float32 or tuple(idx.shape) != (T, top_k) or \
+                w.shape != idx.shape or not idx.is_contiguous() or not w.is_contiguous():
+            raise ValueError("out must be contiguous int32 and fp32 tensors [n_tok, top_k]")
+    _same_device(dev, bias, idx, w)
+    _enqueue("gale_route_scored", dev, logits.data_ptr(), _dt3(logits), stride, T, E, _ptr(bias), _SCORES[score],
+             n_groups, keep_groups, _GROUP_RULES[group_score], top_k, int(bool(renormalize)), scale, idx.data_ptr(),
+             w.data_ptr())
+    return idx, w
+
+
+def moe_layer_fwd_given(table: DescriptorTable, hidden: int, inter: int, topk_idx: torch.Tensor,
+                        topk_w: torch.Tensor, x: torch.Tensor, flags: int = 0, y: Optional[torch.Tensor] = None,
+                        ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One routed-expert layer over x fp16 [T, hidden] with each token's experts (int32 [T, top_k], -1: none) and
+    their weights (fp32) given, as route_scored returns them."""
+    n_tok, top_k = topk_idx.shape
+    dev = x.get_device()
+    if topk_idx.dtype != torch.int32 or topk_w.dtype != torch.float32 or topk_w.shape != topk_idx.shape or \
+            not topk_idx.is_contiguous() or not topk_w.is_contiguous():
+        raise ValueError("topk_idx and topk_w must be contiguous int32 and fp32 tensors [n_tok, top_k]")
+    if x.dtype != torch.float16 or tuple(x.shape) != (n_tok, hidden) or not x.is_contiguous():
+        raise ValueError("x must be a contiguous fp16 tensor [n_tok, hidden]")
+    if y is None:
+        y = torch.empty(n_tok, hidden, dtype=torch.float16, device=x.device)
+    elif y.dtype != torch.float16 or y.shape != x.shape or not y.is_contiguous():
+        raise ValueError("y must be a contiguous fp16 tensor [n_tok, hidden]")
+    if ws is None:
+        ws = moe_workspace(moe_workspace_bytes(n_tok, table.count, top_k, hidden, inter, flags), x.device)
+    _same_device(dev, topk_idx, topk_w, y, ws)
+    _enqueue("gale_moe_layer_fwd_given", dev, hidden, inter, table.ptr(), table.count, topk_idx.data_ptr(),
+             topk_w.data_ptr(), top_k, x.data_ptr(), n_tok, y.data_ptr(), ws.data_ptr(), ws.numel(),
+             _with_stage(flags, table))
+    return y

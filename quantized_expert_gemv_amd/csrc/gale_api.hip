@@ -7,6 +7,7 @@
 #include <cstring>
 
 #include "gale_internal.h"
+#include "gale_mx.h"
 
 namespace gale {
 
@@ -534,7 +535,7 @@ extern "C" size_t gale_moe_workspace_bytes(int32_t n_tok, int32_t n_experts, int
 
 static int moe_layer(const char* fn, int32_t hidden, int32_t inter, const gale_expert* experts_dev,
                      int32_t n_experts, const float* logits, const float* select_bias, const int32_t* fixed_idx,
-                     int32_t top_k, const void* x, int32_t n_tok, void* y, int32_t* topk_idx, float* topk_w,
+                     const float* fixed_w, int32_t top_k, const void* x, int32_t n_tok, void* y, int32_t* topk_idx, float* topk_w,
                      void* ws, size_t ws_bytes, uint32_t flags, hipStream_t stream) {
   int st = check_matrix_shape(fn, inter, hidden);
   if (st) return st;
@@ -549,14 +550,15 @@ static int moe_layer(const char* fn, int32_t hidden, int32_t inter, const gale_e
     return GALE_ERR_SHAPE;
   }
   if (n_tok < 1) { set_error("%s: n_tok=%d", fn, n_tok); return GALE_ERR_SHAPE; }
-  if (!experts_dev || !logits || !x || !y || !ws) { set_error("%s: NULL pointer", fn); return GALE_ERR_NULL; }
+  // with given weights the logits are not read
+  if (!experts_dev || (!logits && !fixed_w) || !x || !y || !ws) { set_error("%s: NULL pointer", fn); return GALE_ERR_NULL; }
   if (!aligned(x, 16) || !aligned(ws, 256) || !aligned(y, 2) || !aligned(logits, 4) || !aligned(select_bias, 4) ||
-      !aligned(fixed_idx, 4)) {
+      !aligned(fixed_idx, 4) || !aligned(fixed_w, 4)) {
     set_error("%s: misaligned pointer", fn);
     return GALE_ERR_ALIGN;
   }
   if (select_bias && fixed_idx) { set_error("%s: a selection bias and fixed experts exclude each other", fn); return GALE_ERR_SHAPE; }
-  const RouteIn rin = {logits, select_bias, fixed_idx};
+  const RouteIn rin = {logits, select_bias, fixed_idx, fixed_w};
   if ((flags & GALE_PATH_DECODE) && (flags & GALE_PATH_GROUPED)) { set_error("%s: both paths forced", fn); return GALE_ERR_SHAPE; }
   const MoePath path = moe_path(n_tok, flags);
   if (path == kDecode && n_tok > GALE_MAX_DECODE_TOKENS) {
@@ -618,7 +620,7 @@ static int moe_layer(const char* fn, int32_t hidden, int32_t inter, const gale_e
     const int forced = (int)((flags >> GALE_TILES_SHIFT) & 0xF);
     return hip_status(fn, launch_decode_stack(io, nullptr, 1, n_experts, top_k, hidden, inter, h, ra_h,
                                               reinterpret_cast<uint64_t*>(base + W.sync), forced,
-                                              decode_wait_ticks(flags), stream));
+                                              decode_wait_ticks(flags), stream, fixed_w));
   }
   // decode items of one vector: each GEMV phase rotates and splits its input itself (same bits)
   const bool raw_up = path == kDecode && slots == 1 && raw_x_ok(hidden, 1, flags, hidden);
@@ -677,8 +679,8 @@ extern "C" int gale_moe_layer_fwd(int32_t hidden, int32_t inter, const gale_expe
                                   int32_t n_experts, const float* logits, int32_t top_k, const void* x,
                                   int32_t n_tok, void* y, int32_t* topk_idx, float* topk_w, void* ws,
                                   size_t ws_bytes, uint32_t flags, hipStream_t stream) {
-  return moe_layer("gale_moe_layer_fwd", hidden, inter, experts_dev, n_experts, logits, nullptr, nullptr, top_k, x,
-                   n_tok, y, topk_idx, topk_w, ws, ws_bytes, flags, stream);
+  return moe_layer("gale_moe_layer_fwd", hidden, inter, experts_dev, n_experts, logits, nullptr, nullptr, nullptr,
+                   top_k, x, n_tok, y, topk_idx, topk_w, ws, ws_bytes, flags, stream);
 }
 
 extern "C" int gale_moe_layer_fwd_routed(int32_t hidden, int32_t inter, const gale_expert* experts_dev,
@@ -687,7 +689,17 @@ extern "C" int gale_moe_layer_fwd_routed(int32_t hidden, int32_t inter, const ga
                                          void* y, int32_t* topk_idx, float* topk_w, void* ws, size_t ws_bytes,
                                          uint32_t flags, hipStream_t stream) {
   return moe_layer("gale_moe_layer_fwd_routed", hidden, inter, experts_dev, n_experts, logits, select_bias, fixed_idx,
-                   top_k, x, n_tok, y, topk_idx, topk_w, ws, ws_bytes, flags, stream);
+                   nullptr, top_k, x, n_tok, y, topk_idx, topk_w, ws, ws_bytes, flags, stream);
+}
+
+extern "C" int gale_moe_layer_fwd_given(int32_t hidden, int32_t inter, const gale_expert* experts_dev,
+                                        int32_t n_experts, const int32_t* topk_idx, const float* topk_w, int32_t top_k,
+                                        const void* x, int32_t n_tok, void* y, void* ws, size_t ws_bytes,
+                                        uint32_t flags, hipStream_t stream) {
+  const char* fn = "gale_moe_layer_fwd_given";
+  if (!topk_idx || !topk_w) { set_error("%s: NULL pointer", fn); return GALE_ERR_NULL; }
+  return moe_layer(fn, hidden, inter, experts_dev, n_experts, nullptr, nullptr, topk_idx, topk_w, top_k, x, n_tok, y,
+                   nullptr, nullptr, ws, ws_bytes, flags, stream);
 }
 
 extern "C" size_t gale_route_workspace_bytes(int32_t n_tok, int32_t n_experts) {
@@ -825,4 +837,155 @@ extern "C" int gale_moe_decode_stack_static(int32_t hidden, int32_t inter, int32
   return hip_status(fn, launch_decode_stack(none, layers_dev, n_layers, n_experts, top_k, hidden, inter, h, rec,
                                             reinterpret_cast<uint64_t*>(base), forced, decode_wait_ticks(flags),
                                             stream));
+}
+
+// ============================================================================
+// around the routed layer: norm, scored routing, MX linear layers
+// ============================================================================
+static inline bool dtype3_ok(int d) { return dtype_ok(d) || d == GALE_BF16; }
+static inline int dsize3(int d) { return d == GALE_F32 ? 4 : 2; }
+static inline bool mx_fmt_ok(int f) { return f == GALE_MX_E2M1 || f == GALE_MX_E4M3; }
+
+extern "C" int gale_route_scored(const void* logits, int32_t logits_dtype, int64_t logits_stride, int32_t n_tok,
+                                 int32_t n_experts, const float* bias, int32_t score, int32_t n_groups,
+                                 int32_t keep_groups, int32_t group_rule, int32_t top_k, int32_t renormalize,
+                                 float scale, int32_t* topk_idx, float* topk_w, hipStream_t stream) {
+  const char* fn = "gale_route_scored";
+  if (!dtype3_ok(logits_dtype)) { set_error("%s: bad dtype", fn); return GALE_ERR_DTYPE; }
+  if (n_tok < 0 || n_experts < 1 || n_experts > GALE_MAX_EXPERTS || logits_stride < n_experts) {
+    set_error("%s: bad sizes n_tok=%d n_experts=%d logits_stride=%lld", fn, n_tok, n_experts, (long long)logits_stride);
+    return GALE_ERR_SHAPE;
+  }
+  if (score != GALE_SCORE_SOFTMAX && score != GALE_SCORE_SIGMOID) { set_error("%s: unknown score %d", fn, score); return GALE_ERR_UNSUPPORTED; }
+  if (group_rule != GALE_GROUP_MAX && group_rule != GALE_GROUP_TOP2) { set_error("%s: unknown group rule %d", fn, group_rule); return GALE_ERR_UNSUPPORTED; }
+  if (n_groups < 1 || n_groups > GALE_MAX_GROUPS || n_experts % n_groups || keep_groups < 1 || keep_groups > n_groups) {
+    set_error("%s: n_groups=%d keep_groups=%d for %d experts", fn, n_groups, keep_groups, n_experts);
+    return GALE_ERR_SHAPE;
+  }
+  if (top_k < 1 || top_k > GALE_MAX_TOPK || top_k > keep_groups * (n_experts / n_groups)) {
+    set_error("%s: top_k=%d out of range", fn, top_k);
+    return GALE_ERR_SHAPE;
+  }
+  if (n_tok == 0) return GALE_OK;
+  if (!logits || !topk_idx || !topk_w) { set_error("%s: NULL pointer", fn); return GALE_ERR_NULL; }
+  if (!aligned(logits, dsize3(logits_dtype)) || !aligned(bias, 4) || !aligned(topk_idx, 4) || !aligned(topk_w, 4)) {
+    set_error("%s: misaligned pointer", fn);
+    return GALE_ERR_ALIGN;
+  }
+  return hip_status(fn, launch_route_scored(logits, logits_dtype, logits_stride, n_tok, n_experts, bias, score, n_groups,
+                                            keep_groups, group_rule, top_k, renormalize ? 1 : 0, scale, topk_idx, topk_w,
+                                            stream));
+}
+
+static inline bool mx_cols_ok(int cols) { return cols >= 1 && cols <= GALE_MX_MAX_COLS; }
+
+extern "C" size_t gale_mx_code_bytes(int32_t fmt, int32_t cols) {
+  return mx_fmt_ok(fmt) && mx_cols_ok(cols) ? (size_t)mx_code_row(fmt, cols) : 0;
+}
+
+extern "C" size_t gale_mx_scale_bytes(int32_t cols) { return mx_cols_ok(cols) ? (size_t)mx_scale_row(cols) : 0; }
+
+// What the MX calls have in common: the format, the sizes, the alignment of codes and scales and of rows of dtype.
+static int mx_check(const char* fn, int32_t fmt, int32_t dtype, int64_t stride, int64_t min_stride, int64_t rows,
+                    int32_t cols) {
+  if (!mx_fmt_ok(fmt)) { set_error("%s: unknown MX format %d", fn, fmt); return GALE_ERR_DTYPE; }
+  if (!dtype3_ok(dtype)) { set_error("%s: bad dtype", fn); return GALE_ERR_DTYPE; }
+  if (!mx_cols_ok(cols) || rows < 0 || rows > INT32_MAX || stride < min_stride) {
+    set_error("%s: rows=%lld cols=%d stride=%lld", fn, (long long)rows, cols, (long long)stride);
+    return GALE_ERR_SHAPE;
+  }
+  return GALE_OK;
+}
+
+static int mx_pointers(const char* fn, const void* rows, int32_t dtype, const uint8_t* codes, const uint8_t* scales) {
+  if (!rows || !codes || !scales) { set_error("%s: NULL pointer", fn); return GALE_ERR_NULL; }
+  if (!aligned(rows, dsize3(dtype)) || !aligned(codes, 16) || !aligned(scales, 4)) {
+    set_error("%s: rows need their element's, codes 16-byte, scales 4-byte alignment", fn);
+    return GALE_ERR_ALIGN;
+  }
+  return GALE_OK;
+}
+
+static int mx_quantize(const char* fn, const void* x, int32_t x_dtype, int64_t x_stride, int64_t rows, int32_t cols,
+                       int32_t fmt, bool swiglu, uint8_t* codes, uint8_t* scales, hipStream_t stream) {
+  int st = mx_check(fn, fmt, x_dtype, x_stride, (swiglu ? 2 : 1) * (int64_t)cols, rows, cols);
+  if (st || rows == 0) return st;
+  st = mx_pointers(fn, x, x_dtype, codes, scales);
+  if (st) return st;
+  return hip_status(fn, launch_mx_quantize(x, x_dtype, x_stride, rows, cols, fmt, swiglu, codes, scales, stream));
+}
+
+extern "C" int gale_mx_quantize(const void* x, int32_t x_dtype, int64_t x_stride, int64_t rows, int32_t cols,
+                                int32_t fmt, uint8_t* codes, uint8_t* scales, hipStream_t stream) {
+  return mx_quantize("gale_mx_quantize", x, x_dtype, x_stride, rows, cols, fmt, false, codes, scales, stream);
+}
+
+extern "C" int gale_mx_swiglu_quantize(const void* x, int32_t x_dtype, int64_t x_stride, int64_t rows, int32_t cols,
+                                       int32_t fmt, uint8_t* codes, uint8_t* scales, hipStream_t stream) {
+  return mx_quantize("gale_mx_swiglu_quantize", x, x_dtype, x_stride, rows, cols, fmt, true, codes, scales, stream);
+}
+
+extern "C" int gale_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t fmt, int64_t rows, int32_t cols,
+                                  void* y, int32_t y_dtype, int64_t y_stride, hipStream_t stream) {
+  const char* fn = "gale_mx_dequantize";
+  int st = mx_check(fn, fmt, y_dtype, y_stride, cols, rows, cols);
+  if (st || rows == 0) return st;
+  st = mx_pointers(fn, y, y_dtype, codes, scales);
+  if (st) return st;
+  return hip_status(fn, launch_mx_dequantize(codes, scales, fmt, rows, cols, y, y_dtype, y_stride, stream));
+}
+
+extern "C" int gale_mx_gemm(int32_t m, int32_t n, int32_t k, const uint8_t* a_codes, const uint8_t* a_scales,
+                            int32_t a_fmt, const uint8_t* w_codes, const uint8_t* w_scales, const void* add,
+                            int64_t add_stride, void* y, int32_t y_dtype, int64_t y_stride, hipStream_t stream) {
+  const char* fn = "gale_mx_gemm";
+  int st = mx_check(fn, a_fmt, y_dtype, y_stride, n, m, k);
+  if (st) return st;
+  if (m > GALE_MAX_ROWS || n < 1 || n > GALE_MAX_ROWS || (add && add_stride < n)) {
+    set_error("%s: m=%d n=%d add_stride=%lld", fn, m, n, (long long)add_stride);
+    return GALE_ERR_SHAPE;
+  }
+  if (add == y && add && add_stride != y_stride) { set_error("%s: add in place needs y's stride", fn); return GALE_ERR_SHAPE; }
+  if (m == 0) return GALE_OK;
+  st = mx_pointers(fn, y, y_dtype, a_codes, a_scales);
+  if (st) return st;
+  st = mx_pointers(fn, y, y_dtype, w_codes, w_scales);
+  if (st) return st;
+  if (!aligned(add, dsize3(y_dtype))) { set_error("%s: misaligned add", fn); return GALE_ERR_ALIGN; }
+  return hip_status(fn, launch_mx_gemm(m, n, k, a_codes, a_scales, a_fmt, w_codes, w_scales, add, add_stride, y, y_dtype,
+                                       y_stride, stream));
+}
+
+extern "C" int gale_add_rms_norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                                 int32_t dtype, int64_t rows, int32_t cols, const void* weight, int32_t weight_dtype,
+                                 float eps, void* sum_out, void* y, int32_t y_dtype, int32_t mx_fmt, uint8_t* codes,
+                                 uint8_t* scales, hipStream_t stream) {
+  const char* fn = "gale_add_rms_norm";
+  if (!dtype3_ok(dtype) || (weight && !dtype3_ok(weight_dtype)) || (y && !dtype3_ok(y_dtype)) ||
+      (codes && !mx_fmt_ok(mx_fmt))) {
+    set_error("%s: bad dtype", fn);
+    return GALE_ERR_DTYPE;
+  }
+  if (rows < 0 || rows > INT32_MAX || cols < 1 || cols > GALE_MAX_COLS || x_stride < cols ||
+      (residual && residual_stride < cols)) {
+    set_error("%s: rows=%lld cols=%d strides %lld, %lld", fn, (long long)rows, cols, (long long)x_stride,
+              (long long)residual_stride);
+    return GALE_ERR_SHAPE;
+  }
+  if (!(eps >= 0.f)) { set_error("%s: eps must not be negative", fn); return GALE_ERR_SHAPE; }
+  if ((codes == nullptr) != (scales == nullptr)) { set_error("%s: codes and scales go together", fn); return GALE_ERR_NULL; }
+  if (rows == 0) return GALE_OK;
+  if (!x || (!y && !codes)) { set_error("%s: NULL pointer", fn); return GALE_ERR_NULL; }
+  if ((sum_out == x && x_stride != cols) || (sum_out && sum_out == residual && residual_stride != cols)) {
+    set_error("%s: sum_out in place needs rows stored back to back", fn);
+    return GALE_ERR_SHAPE;
+  }
+  const int es = dsize3(dtype);
+  if (!aligned(x, es) || !aligned(residual, es) || !aligned(sum_out, es) || !aligned(weight, dsize3(weight_dtype)) ||
+      !aligned(y, dsize3(y_dtype)) || !aligned(codes, 16) || !aligned(scales, 4)) {
+    set_error("%s: rows need their element's, codes 16-byte, scales 4-byte alignment", fn);
+    return GALE_ERR_ALIGN;
+  }
+  return hip_status(fn, launch_add_rms_norm(x, x_stride, residual, residual_stride, dtype, rows, cols, weight,
+                                            weight_dtype, eps, sum_out, y, y_dtype, mx_fmt, codes, scales, stream));
 }

@@ -145,6 +145,7 @@ struct StackParams {
   uint8_t* rec;                    // [k] activation records of the rotated h (ra_bytes(I) each)
   uint64_t* sync;                  // kDecodeSyncBytes of synchronisation words
   int64_t wait_ticks;              // give-up time of a barrier wait (100 MHz ticks)
+  const float* weights0;           // the given weights of a one-layer call with given experts, or NULL
 };
 
 __device__ __forceinline__ gale_layer_io layer_io(const StackParams& P, int l) {
@@ -684,7 +685,7 @@ __global__ void __launch_bounds__(512) decode_stack_kernel(const StackParams P) 
       if (l > 0 && io.select_bias == nullptr && io.fixed_idx == nullptr && P.E <= 256)
         topk_wave_vals(lgv, P.E, Pk, lane, s_exp, s_w, s_exp);
       else
-        topk_wave(RouteIn{io.logits, io.select_bias, io.fixed_idx}, 0, P.E, Pk, lane, s_exp, s_w, s_exp);
+        topk_wave(RouteIn{io.logits, io.select_bias, io.fixed_idx, P.weights0}, 0, P.E, Pk, lane, s_exp, s_w, s_exp);
       __builtin_amdgcn_s_setprio(0);
     }
     if (wave == W - 1 && l == 0) warm_table(table, P.E, lane, s_hdr + 3);
@@ -1010,7 +1011,7 @@ static hipError_t launch_stack_t(StackParams P, int nt, int no, hipStream_t s) {
 
 hipError_t launch_decode_stack(const gale_layer_io& io0, const gale_layer_io* layers_dev, int L, int E, int k,
                                int hidden, int inter, float* h, uint8_t* rec, uint64_t* sync, int tiles,
-                               int64_t wait_ticks, hipStream_t s) {
+                               int64_t wait_ticks, hipStream_t s, const float* weights0) {
   StackParams P;
   P.io0 = io0;
   P.layers = layers_dev;
@@ -1023,6 +1024,7 @@ hipError_t launch_decode_stack(const gale_layer_io& io0, const gale_layer_io* la
   P.rec = rec;
   P.sync = sync;
   P.wait_ticks = wait_ticks;
+  P.weights0 = weights0;
   const int C_H = hidden >> 10;
   int R = tiles >= 1 && tiles <= 3 ? tiles : 3;   // gate/up tiles per unit; 2 R wavefronts serve the outliers
   R = R <= C_H ? R : C_H;

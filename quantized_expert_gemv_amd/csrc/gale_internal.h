@@ -157,6 +157,7 @@ struct RouteIn {
   const float* logits;
   const float* bias;      // NULL: none
   const int32_t* fixed;   // NULL: top-k
+  const float* weights = nullptr;   // with fixed: the k weights are given too [T][k], logits are not read
 };
 
 hipError_t launch_route_small(const RouteIn& rin, int n_tok, int n_exp, int k, int32_t* idx, float* w,
@@ -193,6 +194,21 @@ hipError_t launch_grouped_gemm(const gale_matrix* table, int gateup, int rows, i
                                const int32_t* perm, int top_k, const GemmTile* tiles, const int32_t* n_tiles,
                                int max_tiles, const uint16_t* A, float* out, int out_stride, hipStream_t s);
 
+// around the routed layer: MX numbers, their products, the residual norm, scored routing
+hipError_t launch_mx_quantize(const void* x, int x_dtype, int64_t x_stride, int64_t rows, int cols, int fmt,
+                              bool swiglu, uint8_t* codes, uint8_t* scales, hipStream_t s);
+hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int fmt, int64_t rows, int cols, void* y,
+                                int y_dtype, int64_t y_stride, hipStream_t s);
+hipError_t launch_mx_gemm(int m, int n, int k, const uint8_t* a, const uint8_t* as, int a_fmt, const uint8_t* w,
+                          const uint8_t* ws, const void* add, int64_t add_stride, void* y, int y_dtype,
+                          int64_t y_stride, hipStream_t s);
+hipError_t launch_add_rms_norm(const void* x, int64_t x_stride, const void* res, int64_t res_stride, int dtype,
+                               int64_t rows, int cols, const void* w, int w_dtype, float eps, void* sum, void* y,
+                               int y_dtype, int fmt, uint8_t* codes, uint8_t* scales, hipStream_t s);
+hipError_t launch_route_scored(const void* logits, int dtype, int64_t stride, int n_tok, int E, const float* bias,
+                               int score, int G, int keep, int rule, int k, int renorm, float scale, int32_t* idx,
+                               float* w, hipStream_t s);
+
 // one-launch decode of one token through one MoE layer or a stack of layers (route, gate/up +
 // SwiGLU, rotate h, down, combine per layer); sync: kDecodeSyncBytes of synchronisation words
 // (zero-filled before the first call), h: decode_stack_h_bytes(inter, top_k) of fp32 h,
@@ -203,7 +219,7 @@ size_t decode_stack_h_bytes(int inter, int top_k);
 size_t decode_stack_rec_bytes(int inter, int top_k);
 hipError_t launch_decode_stack(const gale_layer_io& io0, const gale_layer_io* layers_dev, int L, int E, int k,
                                int hidden, int inter, float* h, uint8_t* rec, uint64_t* sync, int tiles,
-                               int64_t wait_ticks, hipStream_t s);
+                               int64_t wait_ticks, hipStream_t s, const float* weights0 = nullptr);
 hipError_t launch_sync_init(void* sync, hipStream_t s);
 // 0: valid and no error; 1: the words were never zeroed; 2: a barrier wait gave up
 int sync_words_state(const uint64_t words[3]);

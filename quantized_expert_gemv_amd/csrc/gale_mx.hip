@@ -1,0 +1,142 @@
+// MX (microscaled) numbers: quantisation, its SwiGLU form, and the numbers that MX rows stand for.
+//
+// A thread takes units of eight columns, so a block of 32 is a quad of lanes and its amax two DPP steps.
+// All three kernels are bound by HBM: 2 + 17/32 bytes per fp16 number to 4 bits.
+#include "gale_mx.h"
+
+namespace gale {
+
+// g sigmoid(g) with z = e^-|g| <= 1, which neither overflows nor loses a small sigmoid to 1 / infinity.
+__device__ __forceinline__ float silu(float g) {
+  const float z = expf(-fabsf(g));
+  return g * ((g < 0.f ? z : 1.0f) / (1.0f + z));
+}
+
+// Units (8 columns, padded rows) of a launch are numbered row by row; the host keeps their count below 2^31.
+template <typename T, int FMT, bool SWIGLU>
+__global__ void __launch_bounds__(256) mx_quantize_kernel(const typename T::bits* __restrict__ x, int64_t x_stride,
+                                                          uint32_t n_units, int cols, int row_units, bool wide,
+                                                          uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+  if (i >= n_units) return;      // n_units is a multiple of 16: no quad is split
+  const uint32_t row = i / (uint32_t)row_units;
+  const int u = (int)(i - row * (uint32_t)row_units);
+  const typename T::bits* xr = x + (int64_t)row * x_stride;
+  float v[8];
+  load8<T>(xr, 8 * u, cols, wide, v);
+  if constexpr (SWIGLU) {
+    float up[8];
+    load8<T>(xr + cols, 8 * u, cols, wide, up);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = silu(v[j]) * up[j];
+  }
+  uint32_t words[2];
+  const uint32_t s = mx_encode8<FMT>(v, words);
+  mx_store8<FMT>(codes + (size_t)row * row_units * (FMT == GALE_MX_E2M1 ? 4 : 8),
+                 scales + (size_t)row * (row_units >> 2), u, s, words);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) mx_dequantize_kernel(const uint8_t* __restrict__ codes,
+                                                            const uint8_t* __restrict__ scales, int fmt,
+                                                            uint32_t n_units, int cols, int row_units, bool wide,
+                                                            typename T::bits* __restrict__ y, int64_t y_stride) {
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+  if (i >= n_units) return;
+  const uint32_t row = i / (uint32_t)row_units;
+  const int u = (int)(i - row * (uint32_t)row_units);
+  const uint32_t s = scales[(size_t)row * (row_units >> 2) + (u >> 2)];
+  // 2^(s - 127): s = 0 is the subnormal 2^-127, 255 NaN
+  const float scale = s == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(s ? s << 23 : 0x400000u);
+  float v[8];
+  if (fmt == GALE_MX_E2M1) {
+    const uint32_t w = reinterpret_cast<const uint32_t*>(codes)[(size_t)i];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t c = (w >> (4 * j)) & 15u;
+      // magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6: exponent c / 2, mantissa bit c % 2, subnormal below 2
+      const uint32_t e = (c >> 1) & 3u, m = c & 1u;
+      const float a = e == 0 ? 0.5f * (float)m : __uint_as_float(((e + 126u) << 23) | (m << 22));
+      v[j] = (c & 8u ? -a : a) * scale;
+    }
+  } else {
+    const mx_u32x2 w = reinterpret_cast<const mx_u32x2*>(codes)[(size_t)i];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      v[4 * j + 0] = __builtin_amdgcn_cvt_f32_fp8((int)w[j], 0) * scale;
+      v[4 * j + 1] = __builtin_amdgcn_cvt_f32_fp8((int)w[j], 1) * scale;
+      v[4 * j + 2] = __builtin_amdgcn_cvt_f32_fp8((int)w[j], 2) * scale;
+      v[4 * j + 3] = __builtin_amdgcn_cvt_f32_fp8((int)w[j], 3) * scale;
+    }
+  }
+  if (8 * u < cols) store8<T>(y + (int64_t)row * y_stride, 8 * u, cols, wide, v);
+}
+
+static bool wide_rows(const void* p, int64_t stride, int es) { return ((uintptr_t)p & 15) == 0 && stride * es % 16 == 0; }
+
+// Rows of one launch: their units stay below 2^31.
+static int64_t slab_rows(int row_units) { return std::max<int64_t>(1, ((int64_t)1 << 31) / row_units - 1); }
+
+template <typename T, int FMT, bool SWIGLU>
+static hipError_t quantize_t(const void* x, int64_t x_stride, int64_t rows, int cols, uint8_t* codes, uint8_t* scales,
+                             hipStream_t s) {
+  const int ru = mx_groups(cols) * (GALE_MX_GROUP / 8);
+  constexpr int es = sizeof(typename T::bits);
+  // the up half starts at column cols: its units are wide only when cols keeps the alignment
+  const bool wide = wide_rows(x, x_stride, es) && (!SWIGLU || cols * es % 16 == 0);
+  const int64_t slab = slab_rows(ru);
+  for (int64_t r = 0; r < rows; r += slab) {
+    const int64_t n = std::min(slab, rows - r);
+    const uint32_t units = (uint32_t)(n * ru);
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(mx_quantize_kernel<T, FMT, SWIGLU>), dim3((units + 255) / 256), dim3(256), 0, s,
+                       (const typename T::bits*)x + r * x_stride, x_stride, units, cols, ru, wide,
+                       codes + (size_t)r * mx_code_row(FMT, cols), scales + (size_t)r * mx_scale_row(cols));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+template <typename T>
+static hipError_t quantize_d(const void* x, int64_t x_stride, int64_t rows, int cols, int fmt, bool swiglu,
+                             uint8_t* codes, uint8_t* scales, hipStream_t s) {
+  if (fmt == GALE_MX_E2M1)
+    return swiglu ? quantize_t<T, GALE_MX_E2M1, true>(x, x_stride, rows, cols, codes, scales, s)
+                  : quantize_t<T, GALE_MX_E2M1, false>(x, x_stride, rows, cols, codes, scales, s);
+  return swiglu ? quantize_t<T, GALE_MX_E4M3, true>(x, x_stride, rows, cols, codes, scales, s)
+                : quantize_t<T, GALE_MX_E4M3, false>(x, x_stride, rows, cols, codes, scales, s);
+}
+
+hipError_t launch_mx_quantize(const void* x, int x_dtype, int64_t x_stride, int64_t rows, int cols, int fmt,
+                              bool swiglu, uint8_t* codes, uint8_t* scales, hipStream_t s) {
+  if (x_dtype == GALE_F16) return quantize_d<F16>(x, x_stride, rows, cols, fmt, swiglu, codes, scales, s);
+  if (x_dtype == GALE_BF16) return quantize_d<BF16>(x, x_stride, rows, cols, fmt, swiglu, codes, scales, s);
+  return quantize_d<F32>(x, x_stride, rows, cols, fmt, swiglu, codes, scales, s);
+}
+
+template <typename T>
+static hipError_t dequantize_t(const uint8_t* codes, const uint8_t* scales, int fmt, int64_t rows, int cols, void* y,
+                               int64_t y_stride, hipStream_t s) {
+  const int ru = mx_groups(cols) * (GALE_MX_GROUP / 8);
+  const bool wide = wide_rows(y, y_stride, sizeof(typename T::bits));
+  const int64_t slab = slab_rows(ru);
+  for (int64_t r = 0; r < rows; r += slab) {
+    const int64_t n = std::min(slab, rows - r);
+    const uint32_t units = (uint32_t)(n * ru);
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(mx_dequantize_kernel<T>), dim3((units + 255) / 256), dim3(256), 0, s,
+                       codes + (size_t)r * mx_code_row(fmt, cols), scales + (size_t)r * mx_scale_row(cols), fmt, units,
+                       cols, ru, wide, (typename T::bits*)y + r * y_stride, y_stride);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int fmt, int64_t rows, int cols, void* y,
+                                int y_dtype, int64_t y_stride, hipStream_t s) {
+  if (y_dtype == GALE_F16) return dequantize_t<F16>(codes, scales, fmt, rows, cols, y, y_stride, s);
+  if (y_dtype == GALE_BF16) return dequantize_t<BF16>(codes, scales, fmt, rows, cols, y, y_stride, s);
+  return dequantize_t<F32>(codes, scales, fmt, rows, cols, y, y_stride, s);
+}
+
+}  // namespace gale

@@ -1,0 +1,157 @@
+// Residual addition and RMS norm, with an optional MX output.
+//
+// s = x + r (rounded to the rows' type), y = s / sqrt(mean(s^2) + eps) * w.  One pass over memory: a workgroup
+// holds its row in registers between the sum of squares and the outputs.
+#include "gale_mx.h"
+#include "gale_lanes.h"
+
+namespace gale {
+
+struct NormParams {
+  const void* x;
+  const void* res;           // NULL: none
+  int64_t x_stride, res_stride;
+  const void* w;             // NULL: ones
+  int w_dtype;
+  int cols, row_units;       // row_units: 8-column units, whole 128-column groups when MX is written
+  float eps;
+  void* sum;                 // NULL: not wanted
+  void* y;                   // NULL: not wanted
+  int y_dtype;
+  uint8_t* codes;
+  uint8_t* scales;
+  bool wide_x, wide_res, wide_w, wide_sum, wide_y;
+};
+
+// Sum over the workgroup, in an order fixed by its size: lanes first, then wavefronts.
+__device__ __forceinline__ float block_sum(float v, float* s_wave) {
+  v += lane_xor<1>(v);
+  v += lane_xor<2>(v);
+  v += lane_xor<4>(v);
+  v += lane_xor<8>(v);
+  v += lane_xor<16>(v);
+  v += lane_xor<32>(v);
+  const int nw = (int)blockDim.x >> 6;
+  if (nw == 1) return v;
+  if ((threadIdx.x & 63) == 0) s_wave[threadIdx.x >> 6] = v;
+  __syncthreads();
+  float t = 0.f;
+  for (int i = 0; i < nw; ++i) t += s_wave[i];
+  return t;
+}
+
+// FMT 0: no MX output.  U: units per thread, U * blockDim.x >= row_units.
+template <typename T, int FMT, int U>
+__global__ void __launch_bounds__(1024) add_rms_norm_kernel(const NormParams p) {
+  __shared__ float s_wave[16];
+  typedef typename T::bits bits;
+  const int64_t row = blockIdx.x;
+  const bits* xr = (const bits*)p.x + row * p.x_stride;
+  const bits* rr = (const bits*)p.res + row * p.res_stride;
+  float v[U][8];
+#pragma unroll
+  for (int k = 0; k < U; ++k) {
+    const int c = 8 * (int)(threadIdx.x + k * blockDim.x);
+    load8<T>(xr, c, p.cols, p.wide_x, v[k]);
+  }
+  if (p.res) {
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int c = 8 * (int)(threadIdx.x + k * blockDim.x);
+      float r[8];
+      load8<T>(rr, c, p.cols, p.wide_res, r);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[k][i] = T::to_f32(T::from_f32(v[k][i] + r[i]));
+    }
+  }
+  float sq = 0.f;
+#pragma unroll
+  for (int k = 0; k < U; ++k)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sq = fmaf(v[k][i], v[k][i], sq);
+  sq = block_sum(sq, s_wave);
+  const float inv = 1.0f / sqrtf(sq / (float)p.cols + p.eps);
+#pragma unroll
+  for (int k = 0; k < U; ++k) {
+    const int u = (int)(threadIdx.x + k * blockDim.x), c = 8 * u;
+    if (u >= p.row_units) continue;   // row_units is a multiple of 4 when FMT: no quad is split
+    if (p.sum && c < p.cols) store8<T>((bits*)p.sum + row * p.cols, c, p.cols, p.wide_sum, v[k]);
+    float w[8];
+    if (p.w) load8_dt(p.w, p.w_dtype, c, p.cols, p.wide_w, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[k][i] = p.w ? v[k][i] * inv * w[i] : v[k][i] * inv;
+    if (p.y && c < p.cols) {
+      const int es = p.y_dtype == GALE_F32 ? 4 : 2;
+      store8_dt((char*)p.y + row * p.cols * es, p.y_dtype, c, p.cols, p.wide_y, v[k]);
+    }
+    if constexpr (FMT != 0) {
+      if (c + 8 > p.cols) {
+        // columns behind the row are zero also where 1 / rms is infinite
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[k][i] = c + i < p.cols ? v[k][i] : 0.f;
+      }
+      uint32_t words[2];
+      const uint32_t s = mx_encode8<FMT>(v[k], words);
+      mx_store8<FMT>(p.codes + row * mx_code_row(FMT, p.cols), p.scales + row * mx_scale_row(p.cols), u, s, words);
+    }
+  }
+}
+
+template <typename T, int FMT>
+static hipError_t launch_norm_t(const NormParams& p, int64_t rows, hipStream_t s) {
+  const int ru = p.row_units;
+  if (ru <= 1024) {
+    const int th = std::max(64, (ru + 63) / 64 * 64);
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(add_rms_norm_kernel<T, FMT, 1>), dim3((unsigned)rows), dim3(th), 0, s, p);
+  } else {
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(add_rms_norm_kernel<T, FMT, 2>), dim3((unsigned)rows),
+                       dim3((ru + 127) / 128 * 64), 0, s, p);
+  }
+  return hipGetLastError();
+}
+
+template <typename T>
+static hipError_t launch_norm_f(const NormParams& p, int fmt, int64_t rows, hipStream_t s) {
+  if (fmt == GALE_MX_E2M1) return launch_norm_t<T, GALE_MX_E2M1>(p, rows, s);
+  if (fmt == GALE_MX_E4M3) return launch_norm_t<T, GALE_MX_E4M3>(p, rows, s);
+  return launch_norm_t<T, 0>(p, rows, s);
+}
+
+hipError_t launch_add_rms_norm(const void* x, int64_t x_stride, const void* res, int64_t res_stride, int dtype,
+                               int64_t rows, int cols, const void* w, int w_dtype, float eps, void* sum, void* y,
+                               int y_dtype, int fmt, uint8_t* codes, uint8_t* scales, hipStream_t s) {
+  auto al = [](const void* q) { return ((uintptr_t)q & 15) == 0; };
+  const int es = dtype == GALE_F32 ? 4 : 2, ys = y_dtype == GALE_F32 ? 4 : 2;
+  NormParams p;
+  p.x_stride = x_stride;
+  p.res_stride = res_stride;
+  p.w = w;
+  p.w_dtype = w_dtype;
+  p.cols = cols;
+  p.row_units = codes ? mx_groups(cols) * (GALE_MX_GROUP / 8) : (cols + 7) / 8;
+  p.eps = eps;
+  p.y_dtype = y_dtype;
+  p.wide_x = al(x) && x_stride * es % 16 == 0;
+  p.wide_res = al(res) && res_stride * es % 16 == 0;
+  p.wide_w = al(w);
+  p.wide_sum = al(sum) && (int64_t)cols * es % 16 == 0;
+  p.wide_y = al(y) && (int64_t)cols * ys % 16 == 0;
+  const int f = codes ? fmt : 0;
+  // a grid has fewer than 2^32 threads: a million rows per launch
+  for (int64_t r = 0; r < rows; r += (1 << 20)) {
+    const int64_t n = std::min<int64_t>(rows - r, 1 << 20);
+    p.x = (const char*)x + r * x_stride * es;
+    p.res = res ? (const char*)res + r * res_stride * es : nullptr;
+    p.sum = sum ? (char*)sum + r * cols * es : nullptr;
+    p.y = y ? (char*)y + r * cols * ys : nullptr;
+    p.codes = codes ? codes + r * mx_code_row(fmt, cols) : nullptr;
+    p.scales = codes ? scales + r * mx_scale_row(cols) : nullptr;
+    const hipError_t e = dtype == GALE_F16    ? launch_norm_f<F16>(p, f, n, s)
+                         : dtype == GALE_BF16 ? launch_norm_f<BF16>(p, f, n, s)
+                                              : launch_norm_f<F32>(p, f, n, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace gale

@@ -239,6 +239,15 @@ __device__ __forceinline__ void topk_wave(const RouteIn& in, int t, int E, int k
     if (E <= 256) topk_rounds<4>(lg, E, k, lane, m, my_v, my_i, lds_idx);
     else topk_rounds<8>(lg, E, k, lane, m, my_v, my_i, lds_idx);
   } else {
+    if (in.weights != nullptr) {
+      // given experts (clamped into range) with given weights: nothing to compute
+      if (lane < k) {
+        const int e = in.fixed[(int64_t)t * k + lane];
+        out_idx[lane] = lds_idx[lane] = e < 0 ? 0 : (e >= E ? E - 1 : e);
+        out_w[lane] = in.weights[(int64_t)t * k + lane];
+      }
+      return;
+    }
     if (in.fixed != nullptr) {
       // given experts (clamped into range, so a bad table cannot reach past the logits)
       const int e = lane < k ? in.fixed[(int64_t)t * k + lane] : 0;
