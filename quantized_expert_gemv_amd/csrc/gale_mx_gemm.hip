@@ -29,6 +29,7 @@ struct MxGemmParams {
   int64_t add_stride;
   void* y;
   int64_t y_stride;
+  bool wide;                 // rows of y and add are aligned for four columns at a time
 };
 
 // Format codes of the MFMA: 0 for E4M3, 4 for E2M1.
@@ -70,15 +71,29 @@ __device__ __forceinline__ f32x4 mx_mfma(const v8i& w, int w_scale, const v8i& a
   }
 }
 
-// Four consecutive columns n0 .. n0 + 3 of row i of y, as far as they exist.
+// Four consecutive columns n0 .. n0 + 3 of row i of y, as far as they exist.  p.wide: y and add take them in one access.
 template <typename T>
-__device__ __forceinline__ void mx_store4(const MxGemmParams& p, int i, int n0, const f32x4& acc) {
+__device__ __forceinline__ void mx_store4(const MxGemmParams& p, int i, int n0, float a0, float a1, float a2, float a3) {
   typedef typename T::bits bits;
+  typedef bits bits4 __attribute__((ext_vector_type(4)));
+  float v[4] = {a0, a1, a2, a3};
   bits* y = (bits*)p.y + (int64_t)i * p.y_stride + n0;
   const bits* c = (const bits*)p.add + (int64_t)i * p.add_stride + n0;
+  if (p.wide && n0 + 4 <= p.n) {
+    if (p.add) {
+      const bits4 u = *reinterpret_cast<const bits4*>(c);
 #pragma unroll
-  for (int r = 0; r < 4; ++r)
-    if (n0 + r < p.n) y[r] = T::from_f32(p.add ? acc[r] + T::to_f32(c[r]) : acc[r]);
+      for (int r = 0; r < 4; ++r) v[r] += T::to_f32(u[r]);
+    }
+    bits4 o;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) o[r] = T::from_f32(v[r]);
+    *reinterpret_cast<bits4*>(y) = o;
+  } else {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (n0 + r < p.n) y[r] = T::from_f32(p.add ? v[r] + T::to_f32(c[r]) : v[r]);
+  }
 }
 
 // One wavefront per 16 x 16 tile of y.
@@ -97,7 +112,252 @@ __global__ void __launch_bounds__(256) mx_gemm_simple_kernel(const MxGemmParams 
     acc = mx_mfma<FMT>(mx_operand<GALE_MX_E2M1>(w, k, g), (int)ws[4 * k], mx_operand<FMT>(a, k, g), (int)as[4 * k], acc);
   // the products stay outside the branch below: an MFMA reads the registers of every lane
   asm volatile("" : "+v"(acc));
-  if (m0 + r < p.m) mx_store4<T>(p, m0 + r, n0 + 4 * g, acc);
+  if (m0 + r < p.m) mx_store4<T>(p, m0 + r, n0 + 4 * g, acc[0], acc[1], acc[2], acc[3]);
+}
+
+// ---------------------------------------------------------------------------
+// Tile kernel
+// ---------------------------------------------------------------------------
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) uint8_t lds_byte;
+
+// A stage of the tile kernel is 256 columns: 8 blocks per row, four v_mfma_scale_f32_32x32x64 steps.  Lane l of a step serves
+// row l % 32 and half h = l / 32: its 4-bit elements are one block, its 8-bit ones 16 columns of either of the
+// instruction's two blocks.  Which 64 columns a step takes is free as long as both operands agree: step s takes blocks s and
+// 4 + s, so the four scales of a lane's steps are four neighbouring bytes, 4 h + s, one register per row and
+// stage whose byte s the instruction selects.
+
+// Rows of a stage in LDS are 128 (4-bit) or 256 bytes, in 16-byte chunks.  A ds_read_b128 serves 16 lanes at a time from
+// 64 banks (256 bytes), here the same chunk c of 16 rows: it sits at place c ^ (r / 2 % 8) of row r (two rows span the
+// banks), or at c ^ (r % 16) of an 8-bit row, and the 16 places are apart.  (With c ^ (r % 8) the counters showed
+// a conflict in every read.)
+template <int FMT>
+__device__ __forceinline__ int stage_swizzle(int row) { return FMT == GALE_MX_E2M1 ? (row >> 1) & 7 : row & 15; }
+
+template <int FMT>
+__device__ __forceinline__ v8i stage_operand(const lds_byte* row, int swz, int h, int s) {
+  if constexpr (FMT == GALE_MX_E2M1) {
+    const mx_u32x4 v = *reinterpret_cast<const __attribute__((address_space(3))) mx_u32x4*>(row + 16 * ((4 * h + s) ^ swz));
+    return v8i{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
+  } else {
+    const mx_u32x4 v = *reinterpret_cast<const __attribute__((address_space(3))) mx_u32x4*>(row + 16 * ((2 * s + h) ^ swz));
+    const mx_u32x4 u = *reinterpret_cast<const __attribute__((address_space(3))) mx_u32x4*>(row + 16 * ((8 + 2 * s + h) ^ swz));
+    return v8i{(int)v.x, (int)v.y, (int)v.z, (int)v.w, (int)u.x, (int)u.y, (int)u.z, (int)u.w};
+  }
+}
+
+template <int FMT, bool EXACT, int S>
+__device__ __forceinline__ f32x16 stage_mfma(const v8i& w, int w_scale, const v8i& a, int a_scale, f32x16 acc) {
+  if constexpr (FMT == GALE_MX_E2M1) {
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, a, acc, 4, 4, S, w_scale, S, a_scale);
+  } else if constexpr (EXACT) {
+    v8i hi, lo;
+    mx_split8(a, hi, lo);
+    acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, lo, acc, 4, 0, S, w_scale, S, a_scale);
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, hi, acc, 4, 0, S, w_scale, S, a_scale);
+  } else {
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, a, acc, 4, 0, S, w_scale, S, a_scale);
+  }
+}
+
+template <int FMT, int TM, int TN>
+struct TileShape {
+  static constexpr int BM = 64 * TM, BN = 64 * TN;
+  static constexpr int AB = FMT == GALE_MX_E2M1 ? 128 : 256;     // bytes of a stage's row of A
+  static constexpr int IA = BM * AB / 4096, IW = BN * 128 / 4096;  // 1 KB copies per wavefront and stage
+  static constexpr int STAGE = BM * AB + BN * 128;
+  static constexpr int READS = TM * (AB / 128) + TN, MFMAS = TM * TN;   // ds_read_b128 and MFMA of a step
+};
+
+// Four wavefronts, 2 x 2, each TM x TN tiles of 32 x 32.
+template <typename T, int FMT, bool EXACT, int TM, int TN>
+__global__ void __launch_bounds__(256, 1) mx_gemm_tile_kernel(const MxGemmParams p) {
+#if defined(__HIP_DEVICE_COMPILE__)   // buffer resources are a device type: the host pass needs the kernel's name only
+  typedef TileShape<FMT, TM, TN> Sh;
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem_raw[];
+  lds_byte* smem = (lds_byte*)smem_raw;
+  const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave >> 1, wn = wave & 1;
+
+  // Workgroup -> tile.  Workgroups go round robin over the 8 XCDs: each XCD gets a contiguous run of tiles, and a run
+  // walks panels of four tile rows column by column, so the ~32 tiles that an XCD works on at once share few
+  // rows of A and W in its L2.
+  const int mt = (p.m + Sh::BM - 1) / Sh::BM, nt = (p.n + Sh::BN - 1) / Sh::BN;
+  const int total = mt * nt, per = total >> 3, rest = total & 7;
+  const int xcd = blockIdx.x & 7, in = blockIdx.x >> 3;
+  const int t = xcd * per + min(xcd, rest) + in;
+  const int panel = t / (4 * nt), left = t - panel * 4 * nt;
+  const int ph = min(4, mt - 4 * panel);
+  const int tn = left / ph, tm = 4 * panel + left - tn * ph;
+  const int m0 = tm * Sh::BM, n0 = tn * Sh::BN;
+
+  const int a_pitch = p.groups * (FMT == GALE_MX_E2M1 ? 64 : 128), w_pitch = p.groups * 64, s_pitch = p.groups * 4;
+  const int am = min(Sh::BM, p.m - m0), wnr = min(Sh::BN, p.n - n0);   // rows that exist: others read as zero
+  const auto ra = __builtin_amdgcn_make_buffer_rsrc((void*)(p.a + (size_t)m0 * a_pitch), 0, am * a_pitch, 0x00020000);
+  const auto rw = __builtin_amdgcn_make_buffer_rsrc((void*)(p.w + (size_t)n0 * w_pitch), 0, wnr * w_pitch, 0x00020000);
+  const auto rsa = __builtin_amdgcn_make_buffer_rsrc((void*)(p.as + (size_t)m0 * s_pitch), 0, am * s_pitch, 0x00020000);
+  const auto rsw = __builtin_amdgcn_make_buffer_rsrc((void*)(p.ws + (size_t)n0 * s_pitch), 0, wnr * s_pitch, 0x00020000);
+
+  // copies: 1 KB of consecutive LDS places, lane l the place 16 l
+  constexpr int AC = Sh::AB / 16, AR = 64 / AC;      // chunks per row of A, rows per copy
+  constexpr int AV = 16 / AR;                        // copies until the swizzle of rows repeats
+  static_assert(Sh::IA % AV == 0 && Sh::IW % 2 == 0, "a wavefront's copies start where the swizzle starts");
+  int va[AV], vw[2];
+#pragma unroll
+  for (int o = 0; o < AV; ++o)
+    va[o] = (lane / AC) * a_pitch + 16 * ((lane % AC) ^ stage_swizzle<FMT>(lane / AC + AR * o));
+#pragma unroll
+  for (int o = 0; o < 2; ++o)
+    vw[o] = (lane >> 3) * w_pitch + 16 * ((lane & 7) ^ stage_swizzle<GALE_MX_E2M1>((lane >> 3) + 8 * o));
+  auto copy_stage = [&](int stage, int buf) {
+    lds_byte* la = smem + buf * Sh::STAGE + wave * Sh::IA * 1024;
+    lds_byte* lw = smem + buf * Sh::STAGE + Sh::BM * Sh::AB + wave * Sh::IW * 1024;
+#pragma unroll
+    for (int i = 0; i < Sh::IA; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (__attribute__((address_space(3))) void*)(la + i * 1024), 16, va[i % AV],
+                                               stage * Sh::AB + (wave * Sh::IA + i) * AR * a_pitch, 0, 0);
+#pragma unroll
+    for (int i = 0; i < Sh::IW; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (__attribute__((address_space(3))) void*)(lw + i * 1024), 16, vw[i & 1],
+                                               stage * 128 + (wave * Sh::IW + i) * 8 * w_pitch, 0, 0);
+  };
+  // Scales.  Loading a stage's four bytes per lane would cost the L1 as many line requests as the copies
+  // themselves, so a lane loads 16 bytes of its row at a time: half h those of stages 2 h and 2 h + 1 of four.  Two
+  // exchanges of the halves of the wavefront then give each half its bytes of every stage: registers (d0, d1) = (stage 0
+  // or 2, blocks 0-3 | 4-7) become (stage 0, blocks of this half | stage 2, same), (d2, d3) those of stages 1 and 3.
+  const int stages = (p.groups + 1) >> 1;
+  const int vsa = (wm * 32 * TM + r) * s_pitch + 16 * h, vsw = (wn * 32 * TN + r) * s_pitch + 16 * h;
+  mx_u32x4 sa_next[TM], sw_next[TN];      // of the next four stages, as loaded
+  mx_u32x4 sa4[TM], sw4[TN];              // of these four: element u for stage u
+  auto load_scales = [&](int four) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) sa_next[i] = __builtin_amdgcn_raw_buffer_load_b128(rsa, vsa, four * 32 + i * 32 * s_pitch, 0);
+#pragma unroll
+    for (int i = 0; i < TN; ++i) sw_next[i] = __builtin_amdgcn_raw_buffer_load_b128(rsw, vsw, four * 32 + i * 32 * s_pitch, 0);
+  };
+  // What lies behind the row's last block gets scales of 0 (2^-127) on both sides, which make its products vanish: the
+  // second half of a last stage of 128 columns, and the stages that fill up the last four.
+  auto exchange_scales = [&](int four) {
+    const int left = p.groups - 8 * four - h;     // stage u is there for this half when 2 u < left
+    auto exchange = [&](const mx_u32x4& v) {
+      const auto p0 = __builtin_amdgcn_permlane32_swap(v.x, v.y, false, false);
+      const auto p1 = __builtin_amdgcn_permlane32_swap(v.z, v.w, false, false);
+      return mx_u32x4{0 < left ? p0[0] : 0u, 2 < left ? p1[0] : 0u, 4 < left ? p0[1] : 0u, 6 < left ? p1[1] : 0u};
+    };
+#pragma unroll
+    for (int i = 0; i < TM; ++i) sa4[i] = exchange(sa_next[i]);
+#pragma unroll
+    for (int i = 0; i < TN; ++i) sw4[i] = exchange(sw_next[i]);
+  };
+  const int swz_a = stage_swizzle<FMT>(r), swz_w = stage_swizzle<GALE_MX_E2M1>(r);
+  auto read_step = [&](int buf, int s, v8i a[TM], v8i w[TN]) {
+    const lds_byte* la = smem + buf * Sh::STAGE + (wm * 32 * TM + r) * Sh::AB;
+    const lds_byte* lw = smem + buf * Sh::STAGE + Sh::BM * Sh::AB + (wn * 32 * TN + r) * 128;
+#pragma unroll
+    for (int i = 0; i < TM; ++i) a[i] = stage_operand<FMT>(la + i * 32 * Sh::AB, swz_a, h, s);
+#pragma unroll
+    for (int i = 0; i < TN; ++i) w[i] = stage_operand<GALE_MX_E2M1>(lw + i * 32 * 128, swz_w, h, s);
+  };
+
+  f32x16 acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int k = 0; k < 16; ++k) acc[i][j][k] = 0.f;
+
+  v8i a0[TM], w0[TN], a1[TM], w1[TN];
+#define MX_STEP(S, A, W)                                                                                       \
+  _Pragma("unroll") for (int i = 0; i < TM; ++i) _Pragma("unroll") for (int j = 0; j < TN; ++j) acc[i][j] =    \
+      stage_mfma<FMT, EXACT, S>(W[j], (int)sw4[j][u], A[i], (int)sa4[i][u], acc[i][j]);
+#define MX_SPREAD                                                                                  \
+  _Pragma("unroll") for (int i = 0; i < Sh::READS; ++i) {                                          \
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                                             \
+    __builtin_amdgcn_sched_group_barrier(0x008, Sh::MFMAS / Sh::READS, 0);                         \
+  }                                                                                                \
+  __builtin_amdgcn_sched_barrier(0)
+
+  copy_stage(0, 0);
+  load_scales(0);
+  __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+  __syncthreads();
+  copy_stage(min(1, stages - 1), 1);
+  read_step(0, 0, a0, w0);
+  // The operands of a step are read from LDS during the products of the step before it; the fences keep the steps
+  // apart and the groups spread each step's reads over its products.
+  exchange_scales(0);
+  // Four stages per turn, without a branch: MFMAs are free to sink past one, and the schedule with them.
+  for (int four = 0; 4 * four < stages; ++four) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int buf = u & 1;
+      if (u == 2) load_scales(four + 1);  // past the end: bytes that nothing takes
+      __builtin_amdgcn_sched_barrier(0);
+      read_step(buf, 1, a1, w1);
+      MX_STEP(0, a0, w0);
+      MX_SPREAD;
+      read_step(buf, 2, a0, w0);
+      MX_STEP(1, a1, w1);
+      MX_SPREAD;
+      read_step(buf, 3, a1, w1);
+      MX_STEP(2, a0, w0);
+      MX_SPREAD;
+      // every wavefront has read its share of this stage, and its copies of the next one have landed
+      __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) lgkmcnt(0)
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      read_step(buf ^ 1, 0, a0, w0);
+      copy_stage(min(4 * four + u + 2, stages - 1), buf);   // past the end: the last stage again
+      MX_STEP(3, a1, w1);
+#pragma unroll
+      for (int i = 0; i < Sh::MFMAS / 2; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 2 * Sh::READS / Sh::MFMAS, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < Sh::MFMAS / 2; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x020, 2 * (Sh::IA + Sh::IW) / Sh::MFMAS, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    exchange_scales(four + 1);
+  }
+  __builtin_amdgcn_s_waitcnt(0x0F70);     // no copy is in flight when the workgroup's LDS goes
+#undef MX_STEP
+#undef MX_SPREAD
+
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) asm volatile("" : "+a"(acc[i][j]));   // no MFMA moves into the branches below
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int row = m0 + (wm * TM + i) * 32 + r;
+    if (row < p.m) {
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int col = n0 + (wn * TN + j) * 32 + 8 * k + 4 * h;
+          if (col < p.n)
+            mx_store4<T>(p, row, col, acc[i][j][4 * k], acc[i][j][4 * k + 1], acc[i][j][4 * k + 2], acc[i][j][4 * k + 3]);
+        }
+    }
+  }
+#endif
+}
+
+template <typename T, int FMT, bool EXACT, int TM, int TN>
+static hipError_t launch_tile(const MxGemmParams& p, hipStream_t s) {
+  typedef TileShape<FMT, TM, TN> Sh;
+  const int64_t tiles = (int64_t)((p.m + Sh::BM - 1) / Sh::BM) * ((p.n + Sh::BN - 1) / Sh::BN);
+  auto kern = mx_gemm_tile_kernel<T, FMT, EXACT, TM, TN>;
+  const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, 2 * Sh::STAGE);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kern, dim3((unsigned)tiles), dim3(256), 2 * Sh::STAGE, s, p);
+  return hipGetLastError();
 }
 
 template <typename T, int FMT>
@@ -110,9 +370,15 @@ static hipError_t mx_gemm_t(const MxGemmParams& p, hipStream_t s) {
     q.as = p.as + (size_t)m0 * p.groups * 4;
     q.y = (typename T::bits*)p.y + m0 * p.y_stride;
     if (p.add) q.add = (const typename T::bits*)p.add + m0 * p.add_stride;
-    hipLaunchKernelGGL(HIP_KERNEL_NAME(mx_gemm_simple_kernel<T, FMT>), dim3((p.n + 63) / 64, (q.m + 15) / 16), dim3(256), 0,
-                       s, q);
-    const hipError_t e = hipGetLastError();
+    hipError_t e;
+    if (q.m > 64) {
+      constexpr bool exact = FMT == GALE_MX_E4M3 && sizeof(typename T::bits) == 4;
+      e = launch_tile<T, FMT, exact, FMT == GALE_MX_E2M1 ? 4 : 2, 4>(q, s);
+    } else {
+      hipLaunchKernelGGL(HIP_KERNEL_NAME(mx_gemm_simple_kernel<T, FMT>), dim3((p.n + 63) / 64, (q.m + 15) / 16), dim3(256),
+                         0, s, q);
+      e = hipGetLastError();
+    }
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
@@ -121,7 +387,10 @@ static hipError_t mx_gemm_t(const MxGemmParams& p, hipStream_t s) {
 hipError_t launch_mx_gemm(int m, int n, int k, const uint8_t* a, const uint8_t* as, int a_fmt, const uint8_t* w,
                           const uint8_t* ws, const void* add, int64_t add_stride, void* y, int y_dtype,
                           int64_t y_stride, hipStream_t s) {
-  MxGemmParams p = {m, n, mx_groups(k), a, as, w, ws, add, add_stride, y, y_stride};
+  const int es = y_dtype == GALE_F32 ? 4 : 2;
+  auto four_wide = [es](const void* q, int64_t stride) { return (uintptr_t)q % (4 * es) == 0 && stride % 4 == 0; };
+  MxGemmParams p = {m, n, mx_groups(k), a, as, w, ws, add, add_stride, y, y_stride,
+                    four_wide(y, y_stride) && (!add || four_wide(add, add_stride))};
   const bool four = a_fmt == GALE_MX_E2M1;
   if (y_dtype == GALE_F16) return four ? mx_gemm_t<F16, GALE_MX_E2M1>(p, s) : mx_gemm_t<F16, GALE_MX_E4M3>(p, s);
   if (y_dtype == GALE_BF16) return four ? mx_gemm_t<BF16, GALE_MX_E2M1>(p, s) : mx_gemm_t<BF16, GALE_MX_E4M3>(p, s);
