@@ -61,6 +61,9 @@ __device__ __forceinline__ void load8(const typename T::bits* row, int c, int co
   }
 }
 
+// Whether every row starts on a 16-byte boundary (es: bytes per element).
+inline bool rows_wide(const void* p, int64_t stride, int es) { return ((uintptr_t)p & 15) == 0 && stride * es % 16 == 0; }
+
 // Stores columns c .. c + 7 below cols, rounded to T; wide as in load8.
 template <typename T>
 __device__ __forceinline__ void store8(typename T::bits* row, int c, int cols, bool wide, const float v[8]) {

@@ -72,8 +72,6 @@ __global__ void __launch_bounds__(256) mx_dequantize_kernel(const uint8_t* __res
   if (8 * u < cols) store8<T>(y + (int64_t)row * y_stride, 8 * u, cols, wide, v);
 }
 
-static bool wide_rows(const void* p, int64_t stride, int es) { return ((uintptr_t)p & 15) == 0 && stride * es % 16 == 0; }
-
 // Rows of one launch: their units stay below 2^31.
 static int64_t slab_rows(int row_units) { return std::max<int64_t>(1, ((int64_t)1 << 31) / row_units - 1); }
 
@@ -83,7 +81,7 @@ static hipError_t quantize_t(const void* x, int64_t x_stride, int64_t rows, int 
   const int ru = mx_groups(cols) * (GALE_MX_GROUP / 8);
   constexpr int es = sizeof(typename T::bits);
   // the up half starts at column cols: its units are wide only when cols keeps the alignment
-  const bool wide = wide_rows(x, x_stride, es) && (!SWIGLU || cols * es % 16 == 0);
+  const bool wide = rows_wide(x, x_stride, es) && (!SWIGLU || cols * es % 16 == 0);
   const int64_t slab = slab_rows(ru);
   for (int64_t r = 0; r < rows; r += slab) {
     const int64_t n = std::min(slab, rows - r);
@@ -118,7 +116,7 @@ template <typename T>
 static hipError_t dequantize_t(const uint8_t* codes, const uint8_t* scales, int fmt, int64_t rows, int cols, void* y,
                                int64_t y_stride, hipStream_t s) {
   const int ru = mx_groups(cols) * (GALE_MX_GROUP / 8);
-  const bool wide = wide_rows(y, y_stride, sizeof(typename T::bits));
+  const bool wide = rows_wide(y, y_stride, sizeof(typename T::bits));
   const int64_t slab = slab_rows(ru);
   for (int64_t r = 0; r < rows; r += slab) {
     const int64_t n = std::min(slab, rows - r);

@@ -29,7 +29,7 @@ struct MxGemmParams {
   int64_t add_stride;
   void* y;
   int64_t y_stride;
-  bool wide;                 // rows of y and add are aligned for four columns at a time
+  bool wide, wide8;          // rows of y and add are aligned for four columns, for 16 bytes at a time
 };
 
 // Format codes of the MFMA: 0 for E4M3, 4 for E2M1.
@@ -332,19 +332,52 @@ __global__ void __launch_bounds__(256, 1) mx_gemm_tile_kernel(const MxGemmParams
   for (int i = 0; i < TM; ++i)
 #pragma unroll
     for (int j = 0; j < TN; ++j) asm volatile("" : "+a"(acc[i][j]));   // no MFMA moves into the branches below
+  // Out through LDS, 16 rows of the wavefront at a time, so that eight columns of a row leave in one or two 16-byte
+  // stores and 4 rows fill whole lines.  (Straight from the registers a store touches 32 rows with 16 bytes each.)
+  __syncthreads();
+  constexpr int OC = 32 * TN, OP = OC * 4 + 16;     // columns and padded bytes of a row
+  lds_byte* lo = smem + wave * 16 * OP;
+  const int lpr = OC / 8;                           // lanes per row on the way out
+  const int orow = lane / lpr, oc = lane % lpr * 8;
 #pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    const int row = m0 + (wm * TM + i) * 32 + r;
-    if (row < p.m) {
+  for (int i = 0; i < 2 * TM; ++i) {
+    if ((r >> 4) == (i & 1)) {
 #pragma unroll
       for (int j = 0; j < TN; ++j)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int col = n0 + (wn * TN + j) * 32 + 8 * k + 4 * h;
-          if (col < p.n)
-            mx_store4<T>(p, row, col, acc[i][j][4 * k], acc[i][j][4 * k + 1], acc[i][j][4 * k + 2], acc[i][j][4 * k + 3]);
+          const f32x16& c = acc[i >> 1][j];
+          *reinterpret_cast<__attribute__((address_space(3))) f32x4*>(lo + (r & 15) * OP + (32 * j + 8 * k + 4 * h) * 4) =
+              f32x4{c[4 * k], c[4 * k + 1], c[4 * k + 2], c[4 * k + 3]};
         }
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int o = 0; o < 16 * lpr / 64; ++o) {
+      const int row16 = o * (64 / lpr) + orow;
+      const int row = m0 + wm * 32 * TM + i * 16 + row16, col = n0 + wn * 32 * TN + oc;
+      float v[8];
+      const f32x4 v0 = *reinterpret_cast<const __attribute__((address_space(3))) f32x4*>(lo + row16 * OP + oc * 4);
+      const f32x4 v1 = *reinterpret_cast<const __attribute__((address_space(3))) f32x4*>(lo + row16 * OP + oc * 4 + 16);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = v0[e];
+        v[4 + e] = v1[e];
+      }
+      if (row < p.m && col < p.n) {
+        typedef typename T::bits bits;
+        if (p.add) {
+          float c[8];
+          load8<T>((const bits*)p.add + (int64_t)row * p.add_stride, col, p.n, p.wide8, c);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] += c[e];
+        }
+        store8<T>((bits*)p.y + (int64_t)row * p.y_stride, col, p.n, p.wide8, v);
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
   }
 #endif
 }
@@ -390,7 +423,8 @@ hipError_t launch_mx_gemm(int m, int n, int k, const uint8_t* a, const uint8_t* 
   const int es = y_dtype == GALE_F32 ? 4 : 2;
   auto four_wide = [es](const void* q, int64_t stride) { return (uintptr_t)q % (4 * es) == 0 && stride % 4 == 0; };
   MxGemmParams p = {m, n, mx_groups(k), a, as, w, ws, add, add_stride, y, y_stride,
-                    four_wide(y, y_stride) && (!add || four_wide(add, add_stride))};
+                    four_wide(y, y_stride) && (!add || four_wide(add, add_stride)),
+                    rows_wide(y, y_stride, es) && (!add || rows_wide(add, add_stride, es))};
   const bool four = a_fmt == GALE_MX_E2M1;
   if (y_dtype == GALE_F16) return four ? mx_gemm_t<F16, GALE_MX_E2M1>(p, s) : mx_gemm_t<F16, GALE_MX_E4M3>(p, s);
   if (y_dtype == GALE_BF16) return four ? mx_gemm_t<BF16, GALE_MX_E2M1>(p, s) : mx_gemm_t<BF16, GALE_MX_E4M3>(p, s);

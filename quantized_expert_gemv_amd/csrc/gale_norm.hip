@@ -120,7 +120,6 @@ static hipError_t launch_norm_f(const NormParams& p, int fmt, int64_t rows, hipS
 hipError_t launch_add_rms_norm(const void* x, int64_t x_stride, const void* res, int64_t res_stride, int dtype,
                                int64_t rows, int cols, const void* w, int w_dtype, float eps, void* sum, void* y,
                                int y_dtype, int fmt, uint8_t* codes, uint8_t* scales, hipStream_t s) {
-  auto al = [](const void* q) { return ((uintptr_t)q & 15) == 0; };
   const int es = dtype == GALE_F32 ? 4 : 2, ys = y_dtype == GALE_F32 ? 4 : 2;
   NormParams p;
   p.x_stride = x_stride;
@@ -131,11 +130,11 @@ hipError_t launch_add_rms_norm(const void* x, int64_t x_stride, const void* res,
   p.row_units = codes ? mx_groups(cols) * (GALE_MX_GROUP / 8) : (cols + 7) / 8;
   p.eps = eps;
   p.y_dtype = y_dtype;
-  p.wide_x = al(x) && x_stride * es % 16 == 0;
-  p.wide_res = al(res) && res_stride * es % 16 == 0;
-  p.wide_w = al(w);
-  p.wide_sum = al(sum) && (int64_t)cols * es % 16 == 0;
-  p.wide_y = al(y) && (int64_t)cols * ys % 16 == 0;
+  p.wide_x = rows_wide(x, x_stride, es);
+  p.wide_res = rows_wide(res, res_stride, es);
+  p.wide_w = rows_wide(w, 0, 1);
+  p.wide_sum = rows_wide(sum, cols, es);
+  p.wide_y = rows_wide(y, cols, ys);
   const int f = codes ? fmt : 0;
   // a grid has fewer than 2^32 threads: a million rows per launch
   for (int64_t r = 0; r < rows; r += (1 << 20)) {
