@@ -160,24 +160,25 @@ __device__ __forceinline__ f32x16 stage_mfma(const v8i& w, int w_scale, const v8
   }
 }
 
-template <int FMT, int TM, int TN>
+template <int FMT, int WM, int WN, int TM, int TN>
 struct TileShape {
-  static constexpr int BM = 64 * TM, BN = 64 * TN;
+  static constexpr int BM = 32 * WM * TM, BN = 32 * WN * TN, WAVES = WM * WN;
   static constexpr int AB = FMT == GALE_MX_E2M1 ? 128 : 256;     // bytes of a stage's row of A
-  static constexpr int IA = BM * AB / 4096, IW = BN * 128 / 4096;  // 1 KB copies per wavefront and stage
+  static constexpr int IA = BM * AB / 1024 / WAVES, IW = BN * 128 / 1024 / WAVES;  // 1 KB copies per wavefront and stage
   static constexpr int STAGE = BM * AB + BN * 128;
   static constexpr int READS = TM * (AB / 128) + TN, MFMAS = TM * TN;   // ds_read_b128 and MFMA of a step
+  static constexpr int RPM = READS > MFMAS ? 2 : 1, MPR = READS > MFMAS ? 1 : MFMAS / READS;   // how they alternate
 };
 
-// Four wavefronts, 2 x 2, each TM x TN tiles of 32 x 32.
-template <typename T, int FMT, bool EXACT, int TM, int TN>
-__global__ void __launch_bounds__(256, 1) mx_gemm_tile_kernel(const MxGemmParams p) {
+// WM x WN wavefronts, each TM x TN tiles of 32 x 32.
+template <typename T, int FMT, bool EXACT, int WM, int WN, int TM, int TN>
+__global__ void __launch_bounds__(64 * WM * WN, 1) mx_gemm_tile_kernel(const MxGemmParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)   // buffer resources are a device type: the host pass needs the kernel's name only
-  typedef TileShape<FMT, TM, TN> Sh;
+  typedef TileShape<FMT, WM, WN, TM, TN> Sh;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem_raw[];
   lds_byte* smem = (lds_byte*)smem_raw;
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h = lane >> 5;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave >> 1, wn = wave & 1;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / WN, wn = wave % WN;
 
   // Workgroup -> tile.  Workgroups go round robin over the 8 XCDs: each XCD gets a contiguous run of tiles, and a run
   // walks panels of four tile rows column by column, so the ~32 tiles that an XCD works on at once share few
@@ -272,9 +273,9 @@ __global__ void __launch_bounds__(256, 1) mx_gemm_tile_kernel(const MxGemmParams
   _Pragma("unroll") for (int i = 0; i < TM; ++i) _Pragma("unroll") for (int j = 0; j < TN; ++j) acc[i][j] =    \
       stage_mfma<FMT, EXACT, S>(W[j], (int)sw4[j][u], A[i], (int)sa4[i][u], acc[i][j]);
 #define MX_SPREAD                                                                                  \
-  _Pragma("unroll") for (int i = 0; i < Sh::READS; ++i) {                                          \
-    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                                             \
-    __builtin_amdgcn_sched_group_barrier(0x008, Sh::MFMAS / Sh::READS, 0);                         \
+  _Pragma("unroll") for (int i = 0; i < Sh::READS / Sh::RPM; ++i) {                                \
+    __builtin_amdgcn_sched_group_barrier(0x100, Sh::RPM, 0);                                       \
+    __builtin_amdgcn_sched_group_barrier(0x008, Sh::MPR, 0);                                       \
   }                                                                                                \
   __builtin_amdgcn_sched_barrier(0)
 
@@ -312,7 +313,7 @@ __global__ void __launch_bounds__(256, 1) mx_gemm_tile_kernel(const MxGemmParams
       MX_STEP(3, a1, w1);
 #pragma unroll
       for (int i = 0; i < Sh::MFMAS / 2; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x100, 2 * Sh::READS / Sh::MFMAS, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, (2 * Sh::READS + Sh::MFMAS - 1) / Sh::MFMAS, 0);
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
       }
 #pragma unroll
@@ -382,14 +383,14 @@ __global__ void __launch_bounds__(256, 1) mx_gemm_tile_kernel(const MxGemmParams
 #endif
 }
 
-template <typename T, int FMT, bool EXACT, int TM, int TN>
+template <typename T, int FMT, bool EXACT, int WM, int WN, int TM, int TN>
 static hipError_t launch_tile(const MxGemmParams& p, hipStream_t s) {
-  typedef TileShape<FMT, TM, TN> Sh;
+  typedef TileShape<FMT, WM, WN, TM, TN> Sh;
   const int64_t tiles = (int64_t)((p.m + Sh::BM - 1) / Sh::BM) * ((p.n + Sh::BN - 1) / Sh::BN);
-  auto kern = mx_gemm_tile_kernel<T, FMT, EXACT, TM, TN>;
+  auto kern = mx_gemm_tile_kernel<T, FMT, EXACT, WM, WN, TM, TN>;
   const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, 2 * Sh::STAGE);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3((unsigned)tiles), dim3(256), 2 * Sh::STAGE, s, p);
+  hipLaunchKernelGGL(kern, dim3((unsigned)tiles), dim3(64 * Sh::WAVES), 2 * Sh::STAGE, s, p);
   return hipGetLastError();
 }
 
@@ -406,7 +407,7 @@ static hipError_t mx_gemm_t(const MxGemmParams& p, hipStream_t s) {
     hipError_t e;
     if (q.m > 64) {
       constexpr bool exact = FMT == GALE_MX_E4M3 && sizeof(typename T::bits) == 4;
-      e = launch_tile<T, FMT, exact, FMT == GALE_MX_E2M1 ? 4 : 2, 4>(q, s);
+      e = launch_tile<T, FMT, exact, 4, 2, FMT == GALE_MX_E2M1 ? 2 : 1, 4>(q, s);
     } else {
       hipLaunchKernelGGL(HIP_KERNEL_NAME(mx_gemm_simple_kernel<T, FMT>), dim3((p.n + 63) / 64, (q.m + 15) / 16), dim3(256),
                          0, s, q);
