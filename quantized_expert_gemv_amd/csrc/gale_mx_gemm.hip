@@ -34,18 +34,6 @@ struct MxGemmParams {
 
 // Format codes of the MFMA: 0 for E4M3, 4 for E2M1.
 
-template <int FMT>
-__device__ __forceinline__ v8i mx_operand(const uint8_t* row, int grp, int g) {
-  if constexpr (FMT == GALE_MX_E2M1) {
-    const mx_u32x4 v = *reinterpret_cast<const mx_u32x4*>(row + 64 * (size_t)grp + 16 * g);
-    return v8i{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
-  } else {
-    const mx_u32x4 v = *reinterpret_cast<const mx_u32x4*>(row + 128 * (size_t)grp + 16 * g);
-    const mx_u32x4 u = *reinterpret_cast<const mx_u32x4*>(row + 128 * (size_t)grp + 64 + 16 * g);
-    return v8i{(int)v.x, (int)v.y, (int)v.z, (int)v.w, (int)u.x, (int)u.y, (int)u.z, (int)u.w};
-  }
-}
-
 // The elements of an 8-bit operand of magnitude 4 and more (codes from 0x48), and the others; zero elsewhere.
 __device__ __forceinline__ void mx_split8(const v8i& v, v8i& hi, v8i& lo) {
 #pragma unroll
@@ -96,23 +84,101 @@ __device__ __forceinline__ void mx_store4(const MxGemmParams& p, int i, int n0, 
   }
 }
 
-// One wavefront per 16 x 16 tile of y.
-template <typename T, int FMT>
-__global__ void __launch_bounds__(256) mx_gemm_simple_kernel(const MxGemmParams p) {
+// ---------------------------------------------------------------------------
+// Streaming kernel, for few rows of A
+// ---------------------------------------------------------------------------
+// Bound by reading W once.  A workgroup owns 16 rows of W (16 columns of y) and up to 16 MT rows of A; its wavefronts split
+// the row's 128-column groups into consecutive runs and take them four at a time: the loads of four groups (of W from
+// HBM, of A from the caches) and their scales (16 bytes of a row: one load) are issued a turn ahead of their products.
+// The partial sums meet in LDS in wavefront order.
+constexpr int kFar = 0x7FFFFFF0;      // an offset past every buffer: such a load gives 0 and reads nothing
+
+template <int FMT, int MT>
+struct StreamTurn {
+  mx_u32x4 w[4], a[4][MT][FMT == GALE_MX_E2M1 ? 1 : 2], ws, as[MT];
+};
+
+template <typename T, int FMT, int MT>
+__global__ void __launch_bounds__(512) mx_gemm_stream_kernel(const MxGemmParams p, int per_wave) {
+#if defined(__HIP_DEVICE_COMPILE__)   // buffer resources are a device type: the host pass needs the kernel's name only
+  __shared__ f32x4 part[8][MT][64];
   const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-  const int n0 = ((int)blockIdx.x * 4 + ((int)threadIdx.x >> 6)) * 16, m0 = (int)blockIdx.y * 16;
-  if (n0 >= p.n) return;
-  const int wr = min(n0 + r, p.n - 1), ar = min(m0 + r, p.m - 1);
-  const uint8_t* w = p.w + (size_t)wr * p.groups * 64;
-  const uint8_t* a = p.a + (size_t)ar * p.groups * (FMT == GALE_MX_E2M1 ? 64 : 128);
-  const uint8_t* ws = p.ws + (size_t)wr * p.groups * 4 + g;
-  const uint8_t* as = p.as + (size_t)ar * p.groups * 4 + g;
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  for (int k = 0; k < p.groups; ++k)
-    acc = mx_mfma<FMT>(mx_operand<GALE_MX_E2M1>(w, k, g), (int)ws[4 * k], mx_operand<FMT>(a, k, g), (int)as[4 * k], acc);
-  // the products stay outside the branch below: an MFMA reads the registers of every lane
-  asm volatile("" : "+v"(acc));
-  if (m0 + r < p.m) mx_store4<T>(p, m0 + r, n0 + 4 * g, acc[0], acc[1], acc[2], acc[3]);
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), waves = (int)blockDim.x >> 6;
+  const int n0 = (int)blockIdx.x * 16, m0 = (int)blockIdx.y * 16 * MT;
+  const int a_pitch = p.groups * (FMT == GALE_MX_E2M1 ? 64 : 128), w_pitch = p.groups * 64, s_pitch = p.groups * 4;
+  const int am = min(16 * MT, p.m - m0), wn = min(16, p.n - n0);        // rows that exist: others read as zero
+  const auto ra = __builtin_amdgcn_make_buffer_rsrc((void*)(p.a + (size_t)m0 * a_pitch), 0, am * a_pitch, 0x00020000);
+  const auto rw = __builtin_amdgcn_make_buffer_rsrc((void*)(p.w + (size_t)n0 * w_pitch), 0, wn * w_pitch, 0x00020000);
+  const auto rsa = __builtin_amdgcn_make_buffer_rsrc((void*)(p.as + (size_t)m0 * s_pitch), 0, am * s_pitch, 0x00020000);
+  const auto rsw = __builtin_amdgcn_make_buffer_rsrc((void*)(p.ws + (size_t)n0 * s_pitch), 0, wn * s_pitch, 0x00020000);
+  const int g0 = wave * per_wave, g1 = min(p.groups, g0 + per_wave);
+  const int va = r * a_pitch + 16 * g, vw = r * w_pitch + 16 * g, vs = r * s_pitch;
+  auto load = [&](int k, StreamTurn<FMT, MT>& t) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool in = k + j < g1;      // groups behind the run read as zero, whatever lies there
+      t.w[j] = __builtin_amdgcn_raw_buffer_load_b128(rw, in ? vw : kFar, (k + j) * 64, 0);
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        if constexpr (FMT == GALE_MX_E2M1) {
+          t.a[j][i][0] = __builtin_amdgcn_raw_buffer_load_b128(ra, in ? va + i * 16 * a_pitch : kFar, (k + j) * 64, 0);
+        } else {
+          t.a[j][i][0] = __builtin_amdgcn_raw_buffer_load_b128(ra, in ? va + i * 16 * a_pitch : kFar, (k + j) * 128, 0);
+          t.a[j][i][1] = __builtin_amdgcn_raw_buffer_load_b128(ra, in ? va + i * 16 * a_pitch + 64 : kFar, (k + j) * 128, 0);
+        }
+    }
+    t.ws = __builtin_amdgcn_raw_buffer_load_b128(rsw, vs, k * 4, 0);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) t.as[i] = __builtin_amdgcn_raw_buffer_load_b128(rsa, vs + i * 16 * s_pitch, k * 4, 0);
+  };
+  f32x4 acc[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  StreamTurn<FMT, MT> cur;
+  load(g0, cur);
+  for (int k = g0; k < g1; k += 4) {
+    StreamTurn<FMT, MT> next;
+    load(k + 4, next);                 // behind the run: nothing is read
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const v8i w = {(int)cur.w[j].x, (int)cur.w[j].y, (int)cur.w[j].z, (int)cur.w[j].w, 0, 0, 0, 0};
+      const bool in = k + j < g1;      // the scales of the next run's groups, or of the next row, do not count
+      const int sw = in ? (int)(cur.ws[j] >> (8 * g)) : 0;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const int sa = in ? (int)(cur.as[i][j] >> (8 * g)) : 0;
+        v8i a = {(int)cur.a[j][i][0].x, (int)cur.a[j][i][0].y, (int)cur.a[j][i][0].z, (int)cur.a[j][i][0].w, 0, 0, 0, 0};
+        if constexpr (FMT == GALE_MX_E4M3) {
+          a[4] = (int)cur.a[j][i][1].x;
+          a[5] = (int)cur.a[j][i][1].y;
+          a[6] = (int)cur.a[j][i][1].z;
+          a[7] = (int)cur.a[j][i][1].w;
+        }
+        acc[i] = mx_mfma<FMT>(w, sw, a, sa, acc[i]);
+      }
+    }
+    cur = next;
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i) part[wave][i][lane] = acc[i];
+  __syncthreads();
+  for (int x = (int)threadIdx.x; x < MT * 64; x += (int)blockDim.x) {
+    const int i = x >> 6, l = x & 63;
+    f32x4 v = part[0][i][l];
+    for (int o = 1; o < waves; ++o) v += part[o][i][l];
+    const int row = m0 + 16 * i + (l & 15), col = n0 + 4 * (l >> 4);
+    if (row < p.m && col < p.n) mx_store4<T>(p, row, col, v[0], v[1], v[2], v[3]);
+  }
+#endif
+}
+
+template <typename T, int FMT, int MT>
+static hipError_t launch_stream(const MxGemmParams& p, hipStream_t s) {
+  // a wavefront gets at least one turn of four groups
+  const int waves = std::min(8, (p.groups + 3) / 4);
+  hipLaunchKernelGGL(HIP_KERNEL_NAME(mx_gemm_stream_kernel<T, FMT, MT>), dim3((p.n + 15) / 16, (p.m + 16 * MT - 1) / (16 * MT)),
+                     dim3(64 * waves), 0, s, p, (p.groups + waves - 1) / waves);
+  return hipGetLastError();
 }
 
 // ---------------------------------------------------------------------------
@@ -210,16 +276,26 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) mx_gemm_tile_kernel(const MxG
 #pragma unroll
   for (int o = 0; o < 2; ++o)
     vw[o] = (lane >> 3) * w_pitch + 16 * ((lane & 7) ^ stage_swizzle<GALE_MX_E2M1>((lane >> 3) + 8 * o));
+  // chunks behind the row's last group (the second half of an odd last stage) come from nowhere: the next row's codes
+  // could be NaN
+  bool ha[AV], hw[2];
+#pragma unroll
+  for (int o = 0; o < AV; ++o) ha[o] = ((lane % AC) ^ stage_swizzle<FMT>(lane / AC + AR * o)) >= AC / 2;
+#pragma unroll
+  for (int o = 0; o < 2; ++o) hw[o] = ((lane & 7) ^ stage_swizzle<GALE_MX_E2M1>((lane >> 3) + 8 * o)) >= 4;
   auto copy_stage = [&](int stage, int buf) {
+    const bool half = 2 * stage + 1 == p.groups;
     lds_byte* la = smem + buf * Sh::STAGE + wave * Sh::IA * 1024;
     lds_byte* lw = smem + buf * Sh::STAGE + Sh::BM * Sh::AB + wave * Sh::IW * 1024;
 #pragma unroll
     for (int i = 0; i < Sh::IA; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (__attribute__((address_space(3))) void*)(la + i * 1024), 16, va[i % AV],
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (__attribute__((address_space(3))) void*)(la + i * 1024), 16,
+                                               half && ha[i % AV] ? kFar : va[i % AV],
                                                stage * Sh::AB + (wave * Sh::IA + i) * AR * a_pitch, 0, 0);
 #pragma unroll
     for (int i = 0; i < Sh::IW; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (__attribute__((address_space(3))) void*)(lw + i * 1024), 16, vw[i & 1],
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (__attribute__((address_space(3))) void*)(lw + i * 1024), 16,
+                                               half && hw[i & 1] ? kFar : vw[i & 1],
                                                stage * 128 + (wave * Sh::IW + i) * 8 * w_pitch, 0, 0);
   };
   // Scales.  Loading a stage's four bytes per lane would cost the L1 as many line requests as the copies
@@ -408,10 +484,12 @@ static hipError_t mx_gemm_t(const MxGemmParams& p, hipStream_t s) {
     if (q.m > 64) {
       constexpr bool exact = FMT == GALE_MX_E4M3 && sizeof(typename T::bits) == 4;
       e = launch_tile<T, FMT, exact, 4, 2, FMT == GALE_MX_E2M1 ? 2 : 1, 4>(q, s);
+    } else if (q.m > 32 && FMT == GALE_MX_E2M1) {   // four row tiles of 8-bit A do not fit the registers
+      e = launch_stream<T, FMT, FMT == GALE_MX_E2M1 ? 4 : 2>(q, s);
+    } else if (q.m > 16) {
+      e = launch_stream<T, FMT, 2>(q, s);
     } else {
-      hipLaunchKernelGGL(HIP_KERNEL_NAME(mx_gemm_simple_kernel<T, FMT>), dim3((p.n + 63) / 64, (q.m + 15) / 16), dim3(256),
-                         0, s, q);
-      e = hipGetLastError();
+      e = launch_stream<T, FMT, 1>(q, s);
     }
     if (e != hipSuccess) return e;
   }

@@ -281,6 +281,18 @@ def test_gemm_nan_blocks_and_extreme_scales(q, fmt, m):
     check_product(q, q.mx_quantize(a, fmt), q.mx_quantize(w, 1), torch.float32)
 
 
+@pytest.mark.parametrize("m", [2, 20, 70, 300])
+@pytest.mark.parametrize("k", [128, 384, 640, 1152])
+def test_gemm_nan_elements_stay_in_their_row(q, m, k):
+    """An 8-bit element may be NaN by itself: its row is, and the row before it, whose last columns lie next to it in
+    memory, is not."""
+    a, w = operand(q, m, k, 2, 1), operand(q, 70, k, 1, 2)
+    want = q.mx_gemm(a, w)
+    a.codes[m - 1] = 0x7F
+    y = q.mx_gemm(a, w)
+    assert y[m - 1].isnan().all() and torch.equal(y[:-1], want[:-1])
+
+
 @pytest.mark.parametrize("m", [3, 200])
 def test_gemm_rows_hang_on_their_own_row(q, m):
     a, w = operand(q, m, 640, 2, 1), operand(q, 96, 640, 1, 2)
