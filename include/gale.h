@@ -424,9 +424,9 @@ int gale_moe_layer_fwd_given(int32_t hidden, int32_t inter, const gale_expert* e
  * An expert whose logit is NaN or -infinity, or whose bias is, is never chosen and has score 0;
  * a group of only such experts never stays.  Slots left without an expert get index -1 and
  * weight 0.  +infinity logits count as the largest finite fp32 number.  Without a bias the
- * order of c is taken from the logits themselves (the scores have the same order), otherwise
- * scores, sums and group values are computed and compared in 64 bits, so that the choice does
- * not hang on a rounding; equal values are ties.
+ * experts' order is that of the logits themselves (the scores have the same); sums with a bias and
+ * group values are those of 64-bit arithmetic, so that the choice does not hang on a rounding;
+ * equal values are ties.
  * logits: [n_tok] rows of n_experts values of logits_dtype (GALE_F32, GALE_F16 or GALE_BF16),
  * logits_stride elements apart.  topk_idx: int32 [n_tok][top_k]; topk_w: fp32 [n_tok][top_k].
  * n_experts <= GALE_MAX_EXPERTS and a multiple of n_groups <= GALE_MAX_GROUPS, 1 <= keep_groups <=

@@ -587,7 +587,8 @@ def _enqueue(fn: str, dev: int, *args) -> None:
     if dev < 0:
         raise ValueError("libgale compute calls take device (cuda) tensors")
     f = getattr(_lib or lib(), fn)
-    if dev == torch.cuda.current_device():
+    # what torch.cuda.current_device() and current_stream() return, without their few microseconds
+    if dev == torch._C._cuda_getDevice():
         st = f(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
@@ -610,6 +611,8 @@ def _as_rows(x: torch.Tensor):
             raise ValueError("a tensor of at least one dimension is needed")
         x = x.reshape(-1, x.shape[-1]) if x.shape[-1] else x.reshape(0, 0)
     rows, cols = x.shape
+    if x.is_contiguous():
+        return x, rows, cols
     if cols > 1 and x.stride(1) != 1 or rows > 1 and x.stride(0) < cols:
         x = x.contiguous()
     return x, rows, x.stride(0) if rows > 1 else cols
@@ -617,14 +620,11 @@ def _as_rows(x: torch.Tensor):
 
 def _out_rows(out: torch.Tensor, rows: int, cols: int) -> int:
     """Row stride of a caller's output, which is written in place: [rows, cols], whole rows that do not overlap."""
-    if tuple(out.shape) != (rows, cols) or (cols > 1 and out.stride(1) != 1) or (rows > 1 and out.stride(0) < cols):
+    if out.shape == (rows, cols) and out.is_contiguous():
+        return cols
+    if out.shape != (rows, cols) or (cols > 1 and out.stride(1) != 1) or (rows > 1 and out.stride(0) < cols):
         raise ValueError(f"out must be [{rows}, {cols}] with whole rows")
     return out.stride(0) if rows > 1 else cols
-
-
-def _out_packed(out: torch.Tensor, like: torch.Tensor) -> None:
-    if out.shape != like.shape or not out.is_contiguous():
-        raise ValueError(f"an output must be contiguous and shaped {tuple(like.shape)}")
 
 
 class MXTensor:
@@ -638,10 +638,10 @@ class MXTensor:
         if fmt not in (GALE_MX_E2M1, GALE_MX_E4M3):
             raise ValueError(f"unknown MX format {fmt}")
         g = -(-cols // GALE_MX_GROUP)
-        if cols < 1 or codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or codes.dim() != 2 or \
-                codes.shape[1] != g * (64 if fmt == GALE_MX_E2M1 else 128) or \
-                tuple(scales.shape) != (codes.shape[0], g * 4) or not codes.is_contiguous() or \
-                not scales.is_contiguous() or codes.get_device() != scales.get_device():
+        rows = codes.shape[0] if codes.dim() else 0
+        if cols < 1 or codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8 or \
+                codes.shape != (rows, g * (64 if fmt == GALE_MX_E2M1 else 128)) or scales.shape != (rows, g * 4) or \
+                not codes.is_contiguous() or not scales.is_contiguous() or codes.get_device() != scales.get_device():
             raise ValueError(f"codes and scales do not hold MX rows of {cols} columns")
         self.codes, self.scales, self.cols, self.fmt = codes, scales, cols, fmt
 
@@ -717,7 +717,7 @@ def mx_gemm(a: MXTensor, w: MXTensor, add: Optional[torch.Tensor] = None, out: O
     stride = _out_rows(out, m, n)
     add_ptr, add_stride = None, 0
     if add is not None:
-        if tuple(add.shape) != (m, n) or add.dtype != out.dtype:
+        if add.shape != (m, n) or add.dtype is not out.dtype:
             raise ValueError(f"add must be [{m}, {n}] of y's dtype")
         add, _, add_stride = _as_rows(add)
         add_ptr = add.data_ptr()
@@ -733,35 +733,39 @@ def add_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor], residual: Opti
                  mx_out: Optional[MXTensor] = None):
     """(y, s, mx): s = x + residual rounded to x's dtype (x itself without a residual), y = s / rms(s) * weight in
     out_dtype (default: x's), mx = y as MX numbers when mx_fmt or mx_out asks for them, else None."""
-    shape = x.shape
-    dev = x.get_device()
+    dtype, shape, dev = x.dtype, x.shape, x.get_device()
     rx, rows, xs = _as_rows(x)
     cols = rx.shape[1]
-    r_ptr, rs = None, 0
+    code = _dt3(x)
+    r_ptr = s_ptr = w_ptr = None
+    rs, w_code = 0, code
     if residual is not None:
-        if residual.shape != shape or residual.dtype != x.dtype:
+        if residual.shape != shape or residual.dtype is not dtype:
             raise ValueError("residual must have x's shape and dtype")
         rr, _, rs = _as_rows(residual)
         r_ptr = rr.data_ptr()
-    if weight is not None and (tuple(weight.shape) != (cols,) or not weight.is_contiguous()):
-        raise ValueError(f"weight must be contiguous with {cols} entries")
+        if sum_out is None:
+            sum_out = torch.empty(shape, dtype=dtype, device=x.device)
+    if weight is not None:
+        if weight.shape != (cols,) or not weight.is_contiguous():
+            raise ValueError(f"weight must be contiguous with {cols} entries")
+        w_ptr, w_code = weight.data_ptr(), code if weight.dtype is dtype else _dt3(weight)
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype or x.dtype, device=x.device)
-    else:
-        _out_packed(out, x)
+        out = torch.empty(shape, dtype=out_dtype or dtype, device=x.device)
+    elif out.shape != shape or not out.is_contiguous():
+        raise ValueError(f"out must be contiguous and shaped {tuple(shape)}")
     if sum_out is not None:
-        _out_packed(sum_out, x)
-        if sum_out.dtype != x.dtype:
-            raise ValueError("sum_out must have x's dtype")
-    elif residual is not None:
-        sum_out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        if sum_out.shape != shape or sum_out.dtype is not dtype or not sum_out.is_contiguous():
+            raise ValueError(f"sum_out must be contiguous, of x's dtype and shaped {tuple(shape)}")
+        s_ptr = sum_out.data_ptr()
+    fmt, codes, scales = 0, None, None
     if mx_out is not None or mx_fmt is not None:
         mx_out = _mx_out(mx_out, rows, cols, mx_fmt if mx_fmt is not None else mx_out.fmt, x.device)
-    _same_device(dev, residual, weight, out, sum_out, mx_out.codes if mx_out is not None else None)
-    _enqueue("gale_add_rms_norm", dev, rx.data_ptr(), xs, r_ptr, rs, _dt3(x), rows, cols, _ptr(weight),
-             GALE_F32 if weight is None else _dt3(weight), eps, _ptr(sum_out), out.data_ptr(), _dt3(out),
-             0 if mx_out is None else mx_out.fmt, None if mx_out is None else mx_out.codes.data_ptr(),
-             None if mx_out is None else mx_out.scales.data_ptr())
+        fmt, codes, scales = mx_out.fmt, mx_out.codes.data_ptr(), mx_out.scales.data_ptr()
+        _same_device(dev, mx_out.codes)
+    _same_device(dev, residual, weight, out, sum_out)
+    _enqueue("gale_add_rms_norm", dev, rx.data_ptr(), xs, r_ptr, rs, code, rows, cols, w_ptr, w_code, eps, s_ptr,
+             out.data_ptr(), code if out.dtype is dtype else _dt3(out), fmt, codes, scales)
     return out, x if sum_out is None else sum_out, mx_out
 
 
@@ -781,15 +785,15 @@ def route_scored(logits: torch.Tensor, top_k: int, score: str = "softmax", bias:
         raise ValueError("logits must be [n_tok, n_experts]")
     logits, T, stride = _as_rows(logits)
     E, dev = logits.shape[1], logits.get_device()
-    if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (E,) or not bias.is_contiguous()):
+    if bias is not None and (bias.dtype is not torch.float32 or bias.shape != (E,) or not bias.is_contiguous()):
         raise ValueError("bias must be a contiguous fp32 tensor of n_experts entries")
     if out is None:
         idx = torch.empty(T, top_k, dtype=torch.int32, device=logits.device)
         w = torch.empty(T, top_k, dtype=torch.float32, device=logits.device)
     else:
         idx, w = out
-        if idx.dtype != torch.int32 or w.dtype != torch.float32 or tuple(idx.shape) != (T, top_k) or \
-                w.shape != idx.shape or not idx.is_contiguous() or not w.is_contiguous():
+        if idx.dtype is not torch.int32 or w.dtype is not torch.float32 or idx.shape != (T, top_k) or \
+                w.shape != (T, top_k) or not idx.is_contiguous() or not w.is_contiguous():
             raise ValueError("out must be contiguous int32 and fp32 tensors [n_tok, top_k]")
     _same_device(dev, bias, idx, w)
     _enqueue("gale_route_scored", dev, logits.data_ptr(), _dt3(logits), stride, T, E, _ptr(bias), _SCORES[score],

@@ -2,9 +2,10 @@
 //
 // One wavefront per token.  Each of the n_groups groups gets L = 64 / (n_groups rounded up to a power of two) lanes, and
 // lane i of a group holds its experts i, i + L, ...: a group's value is a reduction over L neighbouring lanes, and with one
-// group the wavefront reads the logits in whole lines.  Scores, their sums with the bias and the group values are
-// computed and compared in 64 bits: rounding them to 32 would let the order of close experts hang on the exponential's last
-// bit.  Without a bias the order is that of the logits, compared exactly in 32 bits.
+// group the wavefront reads the logits in whole lines.  The choice is that of scores, sums and group values in 64 bits: in
+// 32 the order of close experts would hang on the exponential's last bit.  64-bit exponentials of every expert and
+// 64-bit keys cost most of the time, though, and nearly every token's choice is clear in 32 bits: so the choice is
+// made in 32 bits with margins, and made again in 64 where a margin is not kept.
 #include "gale_internal.h"
 #include "gale_lanes.h"
 #include "gale_mx.h"
@@ -54,37 +55,24 @@ __device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
   return v;
 }
 
-// NJ: experts per lane, NJ * L >= gsize.
-template <typename T, int NJ>
-__global__ void __launch_bounds__(256) route_scored_kernel(const ScoredParams p) {
-  const int lane = threadIdx.x & 63;
-  const int t = (int)blockIdx.x * 4 + ((int)threadIdx.x >> 6);
-  if (t >= p.n_tok) return;
-  const typename T::bits* lg = (const typename T::bits*)p.logits + (int64_t)t * p.stride;
-  const int L = 1 << p.log2L, g = lane >> p.log2L, li = lane & (L - 1);
-  float l[NJ];       // logit; -infinity: no expert, or one that cannot be chosen
-  float b[NJ];
-#pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    const int i = li + (j << p.log2L);
-    const bool in = g < p.G && i < p.gsize;
-    const int e = in ? g * p.gsize + i : 0;
-    const float v = T::to_f32(lg[e]);
-    b[j] = p.bias ? p.bias[e] : 0.f;
-    l[j] = in && v == v && b[j] == b[j] && b[j] != -INFINITY ? fminf(v, 3.402823466e38f) : -INFINITY;
-  }
-  // scores in 64 bits
-  double s[NJ], m = 0.0, Z = 0.0;
+// What both ways of choosing leave: lane r < k holds slot r's expert (-1: none).  NJ: experts per lane, NJ * L >= gsize.
+// l: the lane's logits (-infinity: no expert, or one that cannot be chosen), b its biases.
+
+// Scores, sums with the bias and group values in 64 bits, compared exactly; equal values are ties.
+template <int NJ>
+__device__ __forceinline__ int choose_exact(const ScoredParams& p, const float l[NJ], const float b[NJ], int lane, int g,
+                                            int li) {
+  double s[NJ];
   if (p.score == GALE_SCORE_SOFTMAX) {
     float mf = l[0];
 #pragma unroll
     for (int j = 1; j < NJ; ++j) mf = fmaxf(mf, l[j]);
 #pragma unroll
     for (int x = 1; x < 64; x <<= 1) mf = fmaxf(mf, __shfl_xor(mf, x, 64));
-    m = mf;
+    double Z = 0.0;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      s[j] = l[j] == -INFINITY ? 0.0 : exp((double)l[j] - m);
+      s[j] = l[j] == -INFINITY ? 0.0 : exp((double)l[j] - (double)mf);
       Z += s[j];
     }
 #pragma unroll
@@ -98,8 +86,7 @@ __global__ void __launch_bounds__(256) route_scored_kernel(const ScoredParams p)
   double c[NJ];
 #pragma unroll
   for (int j = 0; j < NJ; ++j) c[j] = l[j] == -INFINITY ? -INFINITY : s[j] + (double)b[j];
-  // group values: the largest c, or the sum of the two largest
-  bool kept = g < p.G;
+  bool kept = true;
   if (p.keep < p.G) {
     double v1 = -INFINITY, v2 = -INFINITY;
 #pragma unroll
@@ -107,7 +94,7 @@ __global__ void __launch_bounds__(256) route_scored_kernel(const ScoredParams p)
       v2 = fmax(v2, fmin(v1, c[j]));
       v1 = fmax(v1, c[j]);
     }
-    for (int x = 1; x < L; x <<= 1) {
+    for (int x = 1; x < (1 << p.log2L); x <<= 1) {
       const double o1 = shfl_xor_f64(v1, x), o2 = shfl_xor_f64(v2, x);
       v2 = fmax(fmin(v1, o1), fmax(v2, o2));
       v1 = fmax(v1, o1);
@@ -118,14 +105,12 @@ __global__ void __launch_bounds__(256) route_scored_kernel(const ScoredParams p)
       const double ov = readlane_f64(v, o << p.log2L);
       rank += ov > v || (ov == v && o < g) ? 1 : 0;
     }
-    kept = kept && rank < p.keep;
+    kept = rank < p.keep;
   }
-  // keys: 0 is no candidate
-  uint64_t key[NJ];
+  uint64_t key[NJ];      // 0: no candidate
 #pragma unroll
   for (int j = 0; j < NJ; ++j)
     key[j] = kept && l[j] != -INFINITY ? (p.bias ? f64_key(c[j]) : f64_key((double)l[j])) : 0ull;
-  double mine = 0.0, sum = 0.0;
   int my_e = -1;
   for (int r = 0; r < p.k; ++r) {
     uint64_t best = key[0];
@@ -139,27 +124,181 @@ __global__ void __launch_bounds__(256) route_scored_kernel(const ScoredParams p)
     for (int j = NJ - 1; j >= 0; --j)
       if (key[j] == best) e = (uint32_t)(g * p.gsize + li + (j << p.log2L));
     const uint32_t w = wave_min_u32(e);
-    double sv = 0.0;
-    bool have = false;
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
-      if (e == w && key[j] == best && !have) {   // the lowest j of this lane is the one that e names
-        sv = s[j];
-        key[j] = 0ull;
-        have = true;
+      if ((uint32_t)(g * p.gsize + li + (j << p.log2L)) == w) key[j] = 0ull;
+    my_e = lane == r ? (int)w : my_e;
+  }
+  return my_e;
+}
+
+// The same in 32 bits, with margins: returns false (and no choice) when two values that the choice compares lie closer
+// than their errors could explain; the exact way then decides.
+//   Without a bias the candidates compare by their logits: exact, ties included.
+//   The scores' errors.  Sigmoid: x = l log2 e is off by 2^-24 |x|, which moves e^-|l| by |l| e^-|l| 2^-24 < 2^-25; the hardware
+//   exponential and reciprocal are within 1 ulp, two additions within half of one: below 2^-21 together.  Softmax: the
+//   same for each e^(l - max), and below 2^-20 after a sum of 512 terms (a tree of nine levels) and the reciprocal.
+//   Adding the bias rounds by 2^-24 |c|, adding two sums for a group the same once more.
+// So two experts' c are apart in truth when they differ here by more than 2^-18 + 2^-22 |c|, two groups' by twice that.
+template <int NJ>
+__device__ __forceinline__ bool choose_fast(const ScoredParams& p, const float l[NJ], const float b[NJ], int lane, int g,
+                                            int li, int& my_e) {
+  const bool by_score = p.bias != nullptr || p.keep < p.G;
+  float c[NJ];
+  if (by_score) {
+    if (p.score == GALE_SCORE_SOFTMAX) {
+      float m = l[0];
+#pragma unroll
+      for (int j = 1; j < NJ; ++j) m = fmaxf(m, l[j]);
+      m = key_to_logit(wave_max_u32_v(logit_key(m)));
+      float Z = 0.f;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        c[j] = l[j] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((l[j] - m) * 1.44269504088896341f);
+        Z += c[j];
       }
-    const uint64_t who = __ballot(have);
-    const double ws = readlane_f64(sv, __builtin_ctzll(who));
-    sum += ws;
-    if (lane == r) {
-      mine = ws;
-      my_e = (int)w;
+      Z += lane_xor<1>(Z);
+      Z += lane_xor<2>(Z);
+      Z += lane_xor<4>(Z);
+      Z += lane_xor<8>(Z);
+      Z += lane_xor<16>(Z);
+      Z += lane_xor<32>(Z);
+      const float inv = __builtin_amdgcn_rcpf(Z);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) c[j] *= inv;
+    } else {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const float z = __builtin_amdgcn_exp2f(-fabsf(l[j]) * 1.44269504088896341f);   // e^-|l| in [0, 1]
+        c[j] = (l[j] < 0.f ? z : 1.f) * __builtin_amdgcn_rcpf(1.f + z);
+      }
     }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) c[j] = l[j] == -INFINITY ? -INFINITY : c[j] + b[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) c[j] = l[j];
+  }
+  constexpr float kAbs = 0x1p-18f, kRel = 0x1p-22f;
+  bool kept = true;
+  if (p.keep < p.G) {
+    float v1 = -INFINITY, v2 = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      v2 = fmaxf(v2, fminf(v1, c[j]));
+      v1 = fmaxf(v1, c[j]);
+    }
+    auto merge = [&](float o1, float o2) {
+      v2 = fmaxf(fminf(v1, o1), fmaxf(v2, o2));
+      v1 = fmaxf(v1, o1);
+    };
+    if (p.log2L > 0) merge(lane_xor<1>(v1), lane_xor<1>(v2));
+    if (p.log2L > 1) merge(lane_xor<2>(v1), lane_xor<2>(v2));
+    if (p.log2L > 2) merge(lane_xor<4>(v1), lane_xor<4>(v2));
+    if (p.log2L > 3) merge(lane_xor<8>(v1), lane_xor<8>(v2));
+    if (p.log2L > 4) merge(lane_xor<16>(v1), lane_xor<16>(v2));
+    const float v = p.rule == GALE_GROUP_TOP2 && v2 != -INFINITY ? v1 + v2 : v1;
+    const float margin = 2.f * (kAbs + kRel * fabsf(v));
+    int over = 0, near = 0;       // groups surely better, groups at least nearly as good (this one among them)
+    for (int o = 0; o < p.G; ++o) {
+      const float ov = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), o << p.log2L));
+      over += ov > v + margin ? 1 : 0;
+      near += ov >= v - margin ? 1 : 0;
+    }
+    kept = near <= p.keep;
+    // infinite values have no margin: they go the exact way, except the empty groups behind enough others
+    if (__ballot(g < p.G && !kept && over < p.keep) != 0ull) return false;
+  }
+  uint32_t key[NJ];      // 0: no candidate
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) key[j] = kept && l[j] != -INFINITY ? logit_key(p.bias ? c[j] : l[j]) : 0u;
+  my_e = -1;
+  float last = INFINITY;
+  bool safe = true;
+  const int rounds = p.bias ? p.k + 1 : p.k;
+  for (int r = 0; r < rounds; ++r) {
+    uint32_t lb = key[0];
+    int lj = 0;
+#pragma unroll
+    for (int j = 1; j < NJ; ++j) {
+      const bool gt = key[j] > lb;
+      lb = gt ? key[j] : lb;
+      lj = gt ? j : lj;
+    }
+    const uint32_t m = (uint32_t)__builtin_amdgcn_readfirstlane((int)wave_max_u32_v(lb));
+    if (m == 0u) break;               // no candidate is left
+    if (p.bias) {
+      const float cv = key_to_logit(m);
+      safe = safe && (r == 0 || last - cv > kAbs + kRel * fabsf(last));
+      last = cv;
+    }
+    const uint64_t cand = __ballot(lb == m);
+    const int mine = g * p.gsize + li + (lj << p.log2L);
+    int e;
+    if (__builtin_popcountll(cand) == 1) e = __builtin_amdgcn_readlane(mine, __builtin_ctzll(cand));
+    else e = (int)wave_min_u32(lb == m ? (uint32_t)mine : 0xFFFFFFFFu);
+    e = __builtin_amdgcn_readfirstlane(e);
+    my_e = lane == r ? e : my_e;
+    const bool won = lb == m && mine == e;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) key[j] = won && j == lj ? 0u : key[j];
+  }
+  if (lane >= p.k) my_e = -1;          // the round past the last slot
+  return safe;
+}
+
+template <typename T, int NJ>
+__global__ void __launch_bounds__(256) route_scored_kernel(const ScoredParams p) {
+  __shared__ float s_l[4][GALE_MAX_EXPERTS];
+  const int lane = threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+  const int t = (int)blockIdx.x * 4 + wave;
+  if (t >= p.n_tok) return;
+  const typename T::bits* lg = (const typename T::bits*)p.logits + (int64_t)t * p.stride;
+  const int g = lane >> p.log2L, li = lane & ((1 << p.log2L) - 1);
+  float l[NJ], b[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const int i = li + (j << p.log2L);
+    const bool in = g < p.G && i < p.gsize;
+    const int e = in ? g * p.gsize + i : 0;
+    const float v = T::to_f32(lg[e]);
+    b[j] = p.bias ? p.bias[e] : 0.f;
+    l[j] = in && v == v && b[j] == b[j] && b[j] != -INFINITY ? fminf(v, 3.402823466e38f) : -INFINITY;
+    if (in) s_l[wave][e] = l[j];
+  }
+  int my_e = -1;
+  if (!choose_fast<NJ>(p, l, b, lane, g, li, my_e)) my_e = choose_exact<NJ>(p, l, b, lane, g, li);
+  // weights of the chosen in 64 bits, one slot per lane (k <= 8: lanes 0 .. 7)
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  const double lv = my_e >= 0 ? (double)s_l[wave][my_e] : 0.0;
+  double s = 0.0, f = 1.0;
+  if (p.score == GALE_SCORE_SOFTMAX) {
+    // relative to the token's largest logit, as the softmax is; its sum only where it does not cancel
+    float m = l[0];
+#pragma unroll
+    for (int j = 1; j < NJ; ++j) m = fmaxf(m, l[j]);
+    m = key_to_logit(wave_max_u32_v(logit_key(m)));
+    s = my_e >= 0 ? exp(lv - (double)m) : 0.0;
+    if (!p.renorm) {
+      double Z = 0.0;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) Z += l[j] == -INFINITY ? 0.0 : exp((double)l[j] - (double)m);
+#pragma unroll
+      for (int x = 1; x < 64; x <<= 1) Z += shfl_xor_f64(Z, x);
+      f = Z;
+    }
+  } else {
+    s = my_e >= 0 ? 1.0 / (1.0 + exp(-lv)) : 0.0;
+  }
+  if (p.renorm) {
+    f = s;
+    f += shfl_xor_f64(f, 1);
+    f += shfl_xor_f64(f, 2);
+    f += shfl_xor_f64(f, 4);
   }
   if (lane < p.k) {
-    const double f = p.renorm ? (sum > 0.0 ? mine / sum : 0.0) : mine;
     p.idx[(int64_t)t * p.k + lane] = my_e;
-    p.w[(int64_t)t * p.k + lane] = my_e < 0 ? 0.f : (float)(f * (double)p.scale);
+    p.w[(int64_t)t * p.k + lane] = my_e >= 0 && f > 0.0 ? (float)(s / f * (double)p.scale) : 0.f;
   }
 }
 
@@ -167,8 +306,10 @@ template <typename T>
 static hipError_t launch_scored_t(const ScoredParams& p, hipStream_t s) {
   const int L = 1 << p.log2L, nj = (p.gsize + L - 1) / L;
   const dim3 grid((unsigned)((p.n_tok + 3) / 4));
-  if (nj <= 2) hipLaunchKernelGGL(HIP_KERNEL_NAME(route_scored_kernel<T, 2>), grid, dim3(256), 0, s, p);
+  if (nj <= 1) hipLaunchKernelGGL(HIP_KERNEL_NAME(route_scored_kernel<T, 1>), grid, dim3(256), 0, s, p);
+  else if (nj <= 2) hipLaunchKernelGGL(HIP_KERNEL_NAME(route_scored_kernel<T, 2>), grid, dim3(256), 0, s, p);
   else if (nj <= 4) hipLaunchKernelGGL(HIP_KERNEL_NAME(route_scored_kernel<T, 4>), grid, dim3(256), 0, s, p);
+  else if (nj <= 6) hipLaunchKernelGGL(HIP_KERNEL_NAME(route_scored_kernel<T, 6>), grid, dim3(256), 0, s, p);
   else if (nj <= 8) hipLaunchKernelGGL(HIP_KERNEL_NAME(route_scored_kernel<T, 8>), grid, dim3(256), 0, s, p);
   else hipLaunchKernelGGL(HIP_KERNEL_NAME(route_scored_kernel<T, 16>), grid, dim3(256), 0, s, p);
   return hipGetLastError();
