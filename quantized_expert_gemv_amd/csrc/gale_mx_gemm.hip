@@ -470,6 +470,46 @@ static hipError_t launch_tile(const MxGemmParams& p, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Time of a tile shape in microseconds, fitted to K = 4096 (16 stages) and N = 4096 at M = 64 .. 4096: about 6 to start and
+// end a round of resident tiles; per tile and 16 stages 4.5e-4 per result (6e-4 with 8-bit A, twice that in two parts) and
+// 0.02 per 128 bytes of its rows.  With it, M = 128 / 512 / 1024 / 2048 / 4096 in 4 bits take 7.9 / 11.3 / 16.6 / 27.7 / 46.8 us,
+// against 28 / 31 / 33 / 37 / 47 us in 256 x 256 tiles throughout and 8.4 / 11.3 / 22 / 43 / 84 us in 64 x 64.
+template <int FMT, bool EXACT, int WM, int WN, int TM, int TN>
+static float tile_cost(const MxGemmParams& p, int cus) {
+  typedef TileShape<FMT, WM, WN, TM, TN> Sh;
+  const int64_t tiles = (int64_t)((p.m + Sh::BM - 1) / Sh::BM) * ((p.n + Sh::BN - 1) / Sh::BN);
+  const int resident = std::min(3, (160 * 1024) / (2 * Sh::STAGE));
+  const float per_result = FMT == GALE_MX_E2M1 ? 4.5e-4f : EXACT ? 12e-4f : 6e-4f;
+  const float turns = (float)((p.groups + 7) / 8) / 4;       // of 16 stages: whole turns of four
+  const float tile = turns * (per_result * Sh::BM * Sh::BN + 0.02f * (Sh::BM * Sh::AB / 128 + Sh::BN));
+  const int64_t per_cu = (tiles + cus - 1) / cus;
+  return 6.f * (float)((per_cu + resident - 1) / resident) + tile * (float)per_cu;
+}
+
+template <typename T, int FMT>
+static hipError_t launch_best_tile(const MxGemmParams& p, hipStream_t s) {
+  constexpr bool exact = FMT == GALE_MX_E4M3 && sizeof(typename T::bits) == 4;
+  const int cus = device_cu_count();
+  float best = 1e30f;
+  hipError_t (*run)(const MxGemmParams&, hipStream_t) = nullptr;
+  auto offer = [&](float cost, hipError_t (*f)(const MxGemmParams&, hipStream_t)) {
+    if (cost < best) {
+      best = cost;
+      run = f;
+    }
+  };
+  if constexpr (FMT == GALE_MX_E2M1) {
+    offer(tile_cost<FMT, exact, 4, 2, 2, 4>(p, cus), launch_tile<T, FMT, exact, 4, 2, 2, 4>);   // 256 x 256
+    offer(tile_cost<FMT, exact, 2, 2, 2, 4>(p, cus), launch_tile<T, FMT, exact, 2, 2, 2, 4>);   // 128 x 256
+  } else {
+    offer(tile_cost<FMT, exact, 4, 2, 1, 4>(p, cus), launch_tile<T, FMT, exact, 4, 2, 1, 4>);   // 128 x 256
+  }
+  offer(tile_cost<FMT, exact, 2, 2, 2, 2>(p, cus), launch_tile<T, FMT, exact, 2, 2, 2, 2>);     // 128 x 128
+  offer(tile_cost<FMT, exact, 2, 2, 1, 2>(p, cus), launch_tile<T, FMT, exact, 2, 2, 1, 2>);     // 64 x 128
+  offer(tile_cost<FMT, exact, 2, 2, 1, 1>(p, cus), launch_tile<T, FMT, exact, 2, 2, 1, 1>);     // 64 x 64
+  return run(p, s);
+}
+
 template <typename T, int FMT>
 static hipError_t mx_gemm_t(const MxGemmParams& p, hipStream_t s) {
   // at most 2^16 rows of tiles per launch
@@ -480,17 +520,9 @@ static hipError_t mx_gemm_t(const MxGemmParams& p, hipStream_t s) {
     q.as = p.as + (size_t)m0 * p.groups * 4;
     q.y = (typename T::bits*)p.y + m0 * p.y_stride;
     if (p.add) q.add = (const typename T::bits*)p.add + m0 * p.add_stride;
-    hipError_t e;
-    if (q.m > 64) {
-      constexpr bool exact = FMT == GALE_MX_E4M3 && sizeof(typename T::bits) == 4;
-      e = launch_tile<T, FMT, exact, 4, 2, FMT == GALE_MX_E2M1 ? 2 : 1, 4>(q, s);
-    } else if (q.m > 32 && FMT == GALE_MX_E2M1) {   // four row tiles of 8-bit A do not fit the registers
-      e = launch_stream<T, FMT, FMT == GALE_MX_E2M1 ? 4 : 2>(q, s);
-    } else if (q.m > 16) {
-      e = launch_stream<T, FMT, 2>(q, s);
-    } else {
-      e = launch_stream<T, FMT, 1>(q, s);
-    }
+    const hipError_t e = q.m > 32   ? launch_best_tile<T, FMT>(q, s)
+                         : q.m > 16 ? launch_stream<T, FMT, 2>(q, s)
+                                    : launch_stream<T, FMT, 1>(q, s);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
