@@ -1,6 +1,6 @@
 // Expert choice from softmax or sigmoid scores, with a selection bias, expert groups and renormalised weights.
 //
-// One wavefront per token.  Each of the n_groups groups gets L = 64 / (n_groups rounded up to a power of two) lanes, and
+// One wavefront chooses for one token.  Each of the n_groups groups gets L = 64 / (n_groups rounded up to a power of two) lanes, and
 // lane i of a group holds its experts i, i + L, ...: a group's value is a reduction over L neighbouring lanes, and with one
 // group the wavefront reads the logits in whole lines.  The choice is that of scores, sums and group values in 64 bits: in
 // 32 the order of close experts would hang on the exponential's last bit.  64-bit exponentials of every expert and
@@ -55,13 +55,37 @@ __device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
   return v;
 }
 
+// LDS accesses of one wavefront complete in order: this keeps the compiler from reordering them.
+__device__ __forceinline__ void wave_lds_done() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// A key that the lanes' largest keys reach at least `need` times, by a bitwise search over their counts that ends early
+// where only a few more do; at least 1, which leaves out the lanes without a candidate.
+__device__ __forceinline__ uint32_t head_threshold(uint32_t head, int need) {
+  uint32_t thr = 0;
+  for (uint32_t bit = 0x80000000u; bit != 0; bit >>= 1) {
+    const int n = __builtin_popcountll(__ballot(head >= (thr | bit)));
+    if (n >= need) {
+      thr |= bit;
+      if (n <= need + 6) break;
+    }
+  }
+  return max(thr, 1u);
+}
+
+__device__ __forceinline__ int lanes_below(uint64_t mask) {
+  return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
+}
+
 // What both ways of choosing leave: lane r < k holds slot r's expert (-1: none).  NJ: experts per lane, NJ * L >= gsize.
 // l: the lane's logits (-infinity: no expert, or one that cannot be chosen), b its biases.
 
 // Scores, sums with the bias and group values in 64 bits, compared exactly; equal values are ties.
 template <int NJ>
 __device__ __forceinline__ int choose_exact(const ScoredParams& p, const float l[NJ], const float b[NJ], int lane, int g,
-                                            int li) {
+                                            int li, uint64_t* s_cand, uint32_t* s_id) {
   double s[NJ];
   if (p.score == GALE_SCORE_SOFTMAX) {
     float mf = l[0];
@@ -111,6 +135,40 @@ __device__ __forceinline__ int choose_exact(const ScoredParams& p, const float l
 #pragma unroll
   for (int j = 0; j < NJ; ++j)
     key[j] = kept && l[j] != -INFINITY ? (p.bias ? f64_key(c[j]) : f64_key((double)l[j])) : 0ull;
+  // Candidates by the keys' upper halves, as below in 32 bits: equal halves come along, and their ranks compare whole keys.
+  uint32_t head = 0;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) head = max(head, (uint32_t)(key[j] >> 32));
+  const uint32_t thr = head_threshold(head, p.k);
+  int at = 0;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const bool in = (uint32_t)(key[j] >> 32) >= thr;
+    const uint64_t mask = __ballot(in);
+    const int pos = at + lanes_below(mask);
+    if (in && pos < 64) {
+      s_cand[pos] = key[j];
+      s_id[pos] = (uint32_t)(g * p.gsize + li + (j << p.log2L));
+    }
+    at += __builtin_popcountll(mask);
+  }
+  wave_lds_done();
+  if (at <= 64) {
+    const uint64_t mine = lane < at ? s_cand[lane] : 0ull;
+    const uint32_t id = lane < at ? s_id[lane] : 0xFFFFFFFFu;
+    int rank = 0;
+    for (int i = 0; i < at; ++i) {
+      const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)mine, i);
+      const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(mine >> 32), i);
+      const uint64_t o = (uint64_t)hi << 32 | lo;
+      rank += o > mine || (o == mine && (uint32_t)__builtin_amdgcn_readlane((int)id, i) < id) ? 1 : 0;
+    }
+    wave_lds_done();
+    if (lane < at) s_id[rank] = id;          // ranks are all different
+    wave_lds_done();
+    return lane < p.k && lane < at ? (int)s_id[lane] : -1;
+  }
+  // more than 64 candidates (as many equal keys): slot by slot
   int my_e = -1;
   for (int r = 0; r < p.k; ++r) {
     uint64_t best = key[0];
@@ -142,7 +200,7 @@ __device__ __forceinline__ int choose_exact(const ScoredParams& p, const float l
 // So two experts' c are apart in truth when they differ here by more than 2^-18 + 2^-22 |c|, two groups' by twice that.
 template <int NJ>
 __device__ __forceinline__ bool choose_fast(const ScoredParams& p, const float l[NJ], const float b[NJ], int lane, int g,
-                                            int li, int& my_e) {
+                                            int li, uint64_t* s_cand, int& my_e) {
   const bool by_score = p.bias != nullptr || p.keep < p.G;
   float c[NJ];
   if (by_score) {
@@ -212,83 +270,107 @@ __device__ __forceinline__ bool choose_fast(const ScoredParams& p, const float l
   uint32_t key[NJ];      // 0: no candidate
 #pragma unroll
   for (int j = 0; j < NJ; ++j) key[j] = kept && l[j] != -INFINITY ? logit_key(p.bias ? c[j] : l[j]) : 0u;
+  // The slots' keys (one more with a bias, for the last margin) are found among few candidates: those that reach a
+  // threshold which as many lanes' largest keys reach, at most 64 or the exact way decides.  Compacted one per lane, their
+  // ranks are counted directly.
   my_e = -1;
-  float last = INFINITY;
-  bool safe = true;
-  const int rounds = p.bias ? p.k + 1 : p.k;
-  for (int r = 0; r < rounds; ++r) {
-    uint32_t lb = key[0];
-    int lj = 0;
+  uint32_t head = key[0];
 #pragma unroll
-    for (int j = 1; j < NJ; ++j) {
-      const bool gt = key[j] > lb;
-      lb = gt ? key[j] : lb;
-      lj = gt ? j : lj;
-    }
-    const uint32_t m = (uint32_t)__builtin_amdgcn_readfirstlane((int)wave_max_u32_v(lb));
-    if (m == 0u) break;               // no candidate is left
-    if (p.bias) {
-      const float cv = key_to_logit(m);
-      safe = safe && (r == 0 || last - cv > kAbs + kRel * fabsf(last));
-      last = cv;
-    }
-    const uint64_t cand = __ballot(lb == m);
-    const int mine = g * p.gsize + li + (lj << p.log2L);
-    int e;
-    if (__builtin_popcountll(cand) == 1) e = __builtin_amdgcn_readlane(mine, __builtin_ctzll(cand));
-    else e = (int)wave_min_u32(lb == m ? (uint32_t)mine : 0xFFFFFFFFu);
-    e = __builtin_amdgcn_readfirstlane(e);
-    my_e = lane == r ? e : my_e;
-    const bool won = lb == m && mine == e;
+  for (int j = 1; j < NJ; ++j) head = max(head, key[j]);
+  const uint32_t thr = head_threshold(head, p.bias ? p.k + 1 : p.k);
+  int count = 0;
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) key[j] = won && j == lj ? 0u : key[j];
-  }
-  if (lane >= p.k) my_e = -1;          // the round past the last slot
-  return safe;
-}
-
-template <typename T, int NJ>
-__global__ void __launch_bounds__(256) route_scored_kernel(const ScoredParams p) {
-  __shared__ float s_l[4][GALE_MAX_EXPERTS];
-  const int lane = threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
-  const int t = (int)blockIdx.x * 4 + wave;
-  if (t >= p.n_tok) return;
-  const typename T::bits* lg = (const typename T::bits*)p.logits + (int64_t)t * p.stride;
-  const int g = lane >> p.log2L, li = lane & ((1 << p.log2L) - 1);
-  float l[NJ], b[NJ];
+  for (int j = 0; j < NJ; ++j) count += __builtin_popcountll(__ballot(key[j] >= thr));
+  if (count > 64) return false;
+  int at = 0;
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    const int i = li + (j << p.log2L);
-    const bool in = g < p.G && i < p.gsize;
-    const int e = in ? g * p.gsize + i : 0;
-    const float v = T::to_f32(lg[e]);
-    b[j] = p.bias ? p.bias[e] : 0.f;
-    l[j] = in && v == v && b[j] == b[j] && b[j] != -INFINITY ? fminf(v, 3.402823466e38f) : -INFINITY;
-    if (in) s_l[wave][e] = l[j];
+    const uint64_t mask = __ballot(key[j] >= thr);
+    if (key[j] >= thr)
+      s_cand[at + lanes_below(mask)] =
+          (uint64_t)key[j] << 32 | (uint32_t)~(g * p.gsize + li + (j << p.log2L));   // lower experts are larger
+    at += __builtin_popcountll(mask);
   }
-  int my_e = -1;
-  if (!choose_fast<NJ>(p, l, b, lane, g, li, my_e)) my_e = choose_exact<NJ>(p, l, b, lane, g, li);
-  // weights of the chosen in 64 bits, one slot per lane (k <= 8: lanes 0 .. 7)
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  const double lv = my_e >= 0 ? (double)s_l[wave][my_e] : 0.0;
-  double s = 0.0, f = 1.0;
-  if (p.score == GALE_SCORE_SOFTMAX) {
-    // relative to the token's largest logit, as the softmax is; its sum only where it does not cancel
-    float m = l[0];
+  wave_lds_done();
+  const uint64_t mine = lane < count ? s_cand[lane] : 0ull;
+  int rank = 0;
+  for (int i = 0; i < count; ++i) {
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)mine, i);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(mine >> 32), i);
+    rank += ((uint64_t)hi << 32 | lo) > mine ? 1 : 0;
+  }
+  wave_lds_done();
+  if (lane < count) s_cand[rank] = mine;        // ranks are all different: a permutation
+  wave_lds_done();
+  const uint64_t own = lane < count ? s_cand[lane] : 0ull;
+  if (p.bias) {
+    const uint64_t after = lane + 1 < count ? s_cand[lane + 1] : 0ull;
+    const float c0 = key_to_logit((uint32_t)(own >> 32)), c1 = key_to_logit((uint32_t)(after >> 32));
+    if (__ballot(lane < p.k && after != 0ull && !(c0 - c1 > kAbs + kRel * fabsf(c0))) != 0ull) return false;
+  }
+  if (lane < p.k && own != 0ull) my_e = (int)~(uint32_t)own;
+  return true;
+}
+
+// Eight tokens per workgroup, one wavefront each; then one wavefront computes the weights of all eight, a lane per slot
+// (64-bit exponentials and divisions of 8 tokens at the price of one).
+constexpr int kScoredTokens = 8;
+
+template <typename T, int NJ>
+__global__ void __launch_bounds__(64 * kScoredTokens) route_scored_kernel(const ScoredParams p) {
+  __shared__ float s_l[kScoredTokens][GALE_MAX_EXPERTS];
+  __shared__ uint64_t s_cand[kScoredTokens][64];
+  __shared__ uint32_t s_id[kScoredTokens][64];
+  __shared__ int s_e[kScoredTokens][GALE_MAX_TOPK];
+  __shared__ float s_m[kScoredTokens];       // a softmax: the token's largest logit
+  __shared__ double s_Z[kScoredTokens];      // and the sum relative to it, where it is needed
+  const int lane = threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+  const int t0 = (int)blockIdx.x * kScoredTokens, t = t0 + wave;
+  if (t < p.n_tok) {
+    const typename T::bits* lg = (const typename T::bits*)p.logits + (int64_t)t * p.stride;
+    const int g = lane >> p.log2L, li = lane & ((1 << p.log2L) - 1);
+    float l[NJ], b[NJ];
 #pragma unroll
-    for (int j = 1; j < NJ; ++j) m = fmaxf(m, l[j]);
-    m = key_to_logit(wave_max_u32_v(logit_key(m)));
-    s = my_e >= 0 ? exp(lv - (double)m) : 0.0;
-    if (!p.renorm) {
-      double Z = 0.0;
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) Z += l[j] == -INFINITY ? 0.0 : exp((double)l[j] - (double)m);
-#pragma unroll
-      for (int x = 1; x < 64; x <<= 1) Z += shfl_xor_f64(Z, x);
-      f = Z;
+    for (int j = 0; j < NJ; ++j) {
+      const int i = li + (j << p.log2L);
+      const bool in = g < p.G && i < p.gsize;
+      const int e = in ? g * p.gsize + i : 0;
+      const float v = T::to_f32(lg[e]);
+      b[j] = p.bias ? p.bias[e] : 0.f;
+      l[j] = in && v == v && b[j] == b[j] && b[j] != -INFINITY ? fminf(v, 3.402823466e38f) : -INFINITY;
+      if (in) s_l[wave][e] = l[j];
     }
+    int my_e = -1;
+    if (!choose_fast<NJ>(p, l, b, lane, g, li, s_cand[wave], my_e)) my_e = choose_exact<NJ>(p, l, b, lane, g, li, s_cand[wave], s_id[wave]);
+    if (lane < GALE_MAX_TOPK) s_e[wave][lane] = lane < p.k ? my_e : -1;
+    if (p.score == GALE_SCORE_SOFTMAX) {
+      float m = l[0];
+#pragma unroll
+      for (int j = 1; j < NJ; ++j) m = fmaxf(m, l[j]);
+      m = key_to_logit(wave_max_u32_v(logit_key(m)));
+      if (lane == 0) s_m[wave] = m;
+      if (!p.renorm) {
+        double Z = 0.0;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) Z += l[j] == -INFINITY ? 0.0 : exp((double)l[j] - (double)m);
+#pragma unroll
+        for (int x = 1; x < 64; x <<= 1) Z += shfl_xor_f64(Z, x);
+        if (lane == 0) s_Z[wave] = Z;
+      }
+    }
+  }
+  __syncthreads();
+  if (wave != 0) return;
+  const int w = lane >> 3, slot = lane & 7;         // token of the eight, and its slot
+  const bool there = t0 + w < p.n_tok;
+  const int e = there ? s_e[w][slot] : -1;
+  const float lv = e >= 0 ? s_l[w][e] : -INFINITY;
+  double s, f = 1.0;
+  if (p.score == GALE_SCORE_SOFTMAX) {
+    if (!p.renorm) f = s_Z[w];       // renormalised, the sum of all cancels
+    s = e >= 0 ? exp((double)lv - (double)s_m[w]) : 0.0;
   } else {
-    s = my_e >= 0 ? 1.0 / (1.0 + exp(-lv)) : 0.0;
+    s = e >= 0 ? 1.0 / (1.0 + exp(-(double)lv)) : 0.0;
   }
   if (p.renorm) {
     f = s;
@@ -296,22 +378,22 @@ __global__ void __launch_bounds__(256) route_scored_kernel(const ScoredParams p)
     f += shfl_xor_f64(f, 2);
     f += shfl_xor_f64(f, 4);
   }
-  if (lane < p.k) {
-    p.idx[(int64_t)t * p.k + lane] = my_e;
-    p.w[(int64_t)t * p.k + lane] = my_e >= 0 && f > 0.0 ? (float)(s / f * (double)p.scale) : 0.f;
+  if (there && slot < p.k) {
+    p.idx[(int64_t)(t0 + w) * p.k + slot] = e;
+    p.w[(int64_t)(t0 + w) * p.k + slot] = e >= 0 && f > 0.0 ? (float)(s / f * (double)p.scale) : 0.f;
   }
 }
 
 template <typename T>
 static hipError_t launch_scored_t(const ScoredParams& p, hipStream_t s) {
   const int L = 1 << p.log2L, nj = (p.gsize + L - 1) / L;
-  const dim3 grid((unsigned)((p.n_tok + 3) / 4));
-  if (nj <= 1) hipLaunchKernelGGL(HIP_KERNEL_NAME(route_scored_kernel<T, 1>), grid, dim3(256), 0, s, p);
-  else if (nj <= 2) hipLaunchKernelGGL(HIP_KERNEL_NAME(route_scored_kernel<T, 2>), grid, dim3(256), 0, s, p);
-  else if (nj <= 4) hipLaunchKernelGGL(HIP_KERNEL_NAME(route_scored_kernel<T, 4>), grid, dim3(256), 0, s, p);
-  else if (nj <= 6) hipLaunchKernelGGL(HIP_KERNEL_NAME(route_scored_kernel<T, 6>), grid, dim3(256), 0, s, p);
-  else if (nj <= 8) hipLaunchKernelGGL(HIP_KERNEL_NAME(route_scored_kernel<T, 8>), grid, dim3(256), 0, s, p);
-  else hipLaunchKernelGGL(HIP_KERNEL_NAME(route_scored_kernel<T, 16>), grid, dim3(256), 0, s, p);
+  const dim3 grid((unsigned)((p.n_tok + kScoredTokens - 1) / kScoredTokens)), block(64 * kScoredTokens);
+  if (nj <= 1) hipLaunchKernelGGL(HIP_KERNEL_NAME(route_scored_kernel<T, 1>), grid, block, 0, s, p);
+  else if (nj <= 2) hipLaunchKernelGGL(HIP_KERNEL_NAME(route_scored_kernel<T, 2>), grid, block, 0, s, p);
+  else if (nj <= 4) hipLaunchKernelGGL(HIP_KERNEL_NAME(route_scored_kernel<T, 4>), grid, block, 0, s, p);
+  else if (nj <= 6) hipLaunchKernelGGL(HIP_KERNEL_NAME(route_scored_kernel<T, 6>), grid, block, 0, s, p);
+  else if (nj <= 8) hipLaunchKernelGGL(HIP_KERNEL_NAME(route_scored_kernel<T, 8>), grid, block, 0, s, p);
+  else hipLaunchKernelGGL(HIP_KERNEL_NAME(route_scored_kernel<T, 16>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 

@@ -235,6 +235,17 @@ def test_gemm_add_and_strides(q, fmt, m, n, k, dtype):
 
 
 @pytest.mark.parametrize("fmt", [1, 2])
+@pytest.mark.parametrize("m,n", [(40, 90), (100, 300), (500, 4090), (1020, 4090), (2040, 4090), (4090, 4090), (3000, 5000)])
+@pytest.mark.parametrize("k", [128, 900])
+def test_gemm_tile_shapes(q, fmt, m, n, k):
+    """Sizes for which each tile shape is taken (64 x 64 to 256 x 256), with ragged last tiles and odd column groups."""
+    a, w = operand(q, m, k, fmt, m + k), operand(q, n, k, 1, n)
+    rows = None if m * n < 10 ** 6 else torch.randint(0, m, (300,), device=DEV, generator=torch.Generator(DEV).manual_seed(m))
+    for dtype in DTS:
+        check_product(q, a, w, dtype, rows=rows)
+
+
+@pytest.mark.parametrize("fmt", [1, 2])
 @pytest.mark.parametrize("m,n,k", [(1, 48, 640), (33, 65, 512), (300, 270, 384), (520, 516, 256)])
 def test_gemm_closed_form(q, fmt, m, n, k):
     """Small whole numbers and scales of 2^-2 .. 2^2: every sum fits 24 bits, so the product is exact and any misplaced
@@ -431,6 +442,25 @@ def test_route_masks_ties_and_special_values(q, score, G, keep):
     idx, w = q.route_scored(lg, 6, score=score, n_groups=G, keep_groups=keep)
     assert (idx[0] == -1).all() and (w[0] == 0).all() and (idx[8] == -1).all()
     assert idx[1].tolist() == [17, -1, -1, -1, -1, -1] and w[1].tolist() == [1, 0, 0, 0, 0, 0]
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_many_equal_keys(q, score):
+    """More equal candidates than a wavefront has lanes, with and without a bias, in one group and in eight."""
+    lg = torch.zeros(3, 512, device=DEV)
+    lg[1, 300:] = 1.0
+    lg[2, ::2] = -2.0
+    for b in (None, torch.zeros(512, device=DEV)):
+        for G, keep in ((1, 1), (8, 5)):
+            check_route(q, lg, 8, score=score, bias=b, n_groups=G, keep_groups=keep)
+
+
+def test_route_large_batch_of_ties(q):
+    """16-bit logits and stepped biases: many margins are not kept, and the choice is the oracle's all the same."""
+    lg = rand((1500, 384), 8, torch.bfloat16, 0.02)
+    bias = 0.001 * torch.randint(-3, 4, (384,), device=DEV, generator=torch.Generator(DEV).manual_seed(1)).float()
+    check_route(q, lg, 8, score="sigmoid", bias=bias, n_groups=8, keep_groups=4)
+    check_route(q, lg, 8, score="softmax", bias=bias, n_groups=8, keep_groups=4, renormalize=False)
 
 
 def test_route_close_scores_keep_their_order(q):
