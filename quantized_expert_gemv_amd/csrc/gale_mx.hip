@@ -6,10 +6,19 @@
 
 namespace gale {
 
-// g sigmoid(g) with z = e^-|g| <= 1, which neither overflows nor loses a small sigmoid to 1 / infinity.
+// g sigmoid(g), within a few ulp for every finite g.  With e = e^(-|g| / 2), sigmoid is 1 / (1 + e^2), or e^2 / (1 + e^2) for
+// negative g: multiplied as (g e) (e / (1 + e^2)), no factor underflows before the result does.  The exponent
+// -|g| log2(e) / 2 is taken with the rounding of its product (x + lo), since the hardware's 2^x turns an absolute error of
+// x into a relative one.  The library's exponential and division bound this kernel by its arithmetic: 12.0 us for
+// 4096 x 2048 fp16 against 9 us.
 __device__ __forceinline__ float silu(float g) {
-  const float z = expf(-fabsf(g));
-  return g * ((g < 0.f ? z : 1.0f) / (1.0f + z));
+  const float a = fabsf(g), kHi = 0.72134752044448170f, kLo = 9.62981496e-9f;   // log2(e) / 2 = kHi + kLo
+  const float x = -a * kHi;
+  const float lo = fmaf(-a, kHi, -x) - a * kLo;
+  float e = __builtin_amdgcn_exp2f(x);
+  e = fmaf(e, lo * 0.693147180559945309f, e);
+  const float r = __builtin_amdgcn_rcpf(fmaf(e, e, 1.0f));
+  return g < 0.f ? (g * e) * (e * r) : g * r;
 }
 
 // Units (8 columns, padded rows) of a launch are numbered row by row; the host keeps their count below 2^31.
@@ -17,23 +26,31 @@ template <typename T, int FMT, bool SWIGLU>
 __global__ void __launch_bounds__(256) mx_quantize_kernel(const typename T::bits* __restrict__ x, int64_t x_stride,
                                                           uint32_t n_units, int cols, int row_units, bool wide,
                                                           uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
-  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
-  if (i >= n_units) return;      // n_units is a multiple of 16: no quad is split
-  const uint32_t row = i / (uint32_t)row_units;
-  const int u = (int)(i - row * (uint32_t)row_units);
-  const typename T::bits* xr = x + (int64_t)row * x_stride;
-  float v[8];
-  load8<T>(xr, 8 * u, cols, wide, v);
-  if constexpr (SWIGLU) {
-    float up[8];
-    load8<T>(xr + cols, 8 * u, cols, wide, up);
+  // two units per thread, 256 apart, all loads first.  n_units is a multiple of 16: no quad is split.
+  float v[2][8], up[2][8];
+  uint32_t row[2];
+  int u[2];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = silu(v[j]) * up[j];
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t i = min(blockIdx.x * 512u + 256u * k + threadIdx.x, n_units - 1u);
+    row[k] = i / (uint32_t)row_units;
+    u[k] = (int)(i - row[k] * (uint32_t)row_units);
+    const typename T::bits* xr = x + (int64_t)row[k] * x_stride;
+    load8<T>(xr, 8 * u[k], cols, wide, v[k]);
+    if constexpr (SWIGLU) load8<T>(xr + cols, 8 * u[k], cols, wide, up[k]);
   }
-  uint32_t words[2];
-  const uint32_t s = mx_encode8<FMT>(v, words);
-  mx_store8<FMT>(codes + (size_t)row * row_units * (FMT == GALE_MX_E2M1 ? 4 : 8),
-                 scales + (size_t)row * (row_units >> 2), u, s, words);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (blockIdx.x * 512u + 256u * k + threadIdx.x >= n_units) return;
+    if constexpr (SWIGLU) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[k][j] = silu(v[k][j]) * up[k][j];
+    }
+    uint32_t words[2];
+    const uint32_t s = mx_encode8<FMT>(v[k], words);
+    mx_store8<FMT>(codes + (size_t)row[k] * row_units * (FMT == GALE_MX_E2M1 ? 4 : 8),
+                   scales + (size_t)row[k] * (row_units >> 2), u[k], s, words);
+  }
 }
 
 template <typename T>
@@ -86,7 +103,7 @@ static hipError_t quantize_t(const void* x, int64_t x_stride, int64_t rows, int 
   for (int64_t r = 0; r < rows; r += slab) {
     const int64_t n = std::min(slab, rows - r);
     const uint32_t units = (uint32_t)(n * ru);
-    hipLaunchKernelGGL(HIP_KERNEL_NAME(mx_quantize_kernel<T, FMT, SWIGLU>), dim3((units + 255) / 256), dim3(256), 0, s,
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(mx_quantize_kernel<T, FMT, SWIGLU>), dim3((units + 511) / 512), dim3(256), 0, s,
                        (const typename T::bits*)x + r * x_stride, x_stride, units, cols, ru, wide,
                        codes + (size_t)r * mx_code_row(FMT, cols), scales + (size_t)r * mx_scale_row(cols));
     const hipError_t e = hipGetLastError();
