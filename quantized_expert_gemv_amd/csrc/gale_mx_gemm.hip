@@ -232,6 +232,8 @@ struct TileShape {
   static constexpr int AB = FMT == GALE_MX_E2M1 ? 128 : 256;     // bytes of a stage's row of A
   static constexpr int IA = BM * AB / 1024 / WAVES, IW = BN * 128 / 1024 / WAVES;  // 1 KB copies per wavefront and stage
   static constexpr int STAGE = BM * AB + BN * 128;
+  static constexpr int SCALES = (BM + BN) * 32;        // scale bytes of four stages
+  static constexpr int LDS = 2 * STAGE + 2 * SCALES;
   static constexpr int READS = TM * (AB / 128) + TN, MFMAS = TM * TN;   // ds_read_b128 and MFMA of a step
   static constexpr int RPM = READS > MFMAS ? 2 : 1, MPR = READS > MFMAS ? 1 : MFMAS / READS;   // how they alternate
 };
@@ -298,33 +300,43 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) mx_gemm_tile_kernel(const MxG
                                                half && hw[i & 1] ? kFar : vw[i & 1],
                                                stage * 128 + (wave * Sh::IW + i) * 8 * w_pitch, 0, 0);
   };
-  // Scales.  Loading a stage's four bytes per lane would cost the L1 as many line requests as the copies
-  // themselves, so a lane loads 16 bytes of its row at a time: half h those of stages 2 h and 2 h + 1 of four.  Two
-  // exchanges of the halves of the wavefront then give each half its bytes of every stage: registers (d0, d1) = (stage 0
-  // or 2, blocks 0-3 | 4-7) become (stage 0, blocks of this half | stage 2, same), (d2, d3) those of stages 1 and 3.
+  // Scales, 32 bytes per row for four stages, also through LDS: from the registers' side every wavefront would ask the
+  // L1 for all its rows, 40 such loads of 32 lines each per workgroup and four stages (128 x 256) where 12 do, next to 256
+  // copies of 8 lines.
   const int stages = (p.groups + 1) >> 1;
-  const int vsa = (wm * 32 * TM + r) * s_pitch + 16 * h, vsw = (wn * 32 * TN + r) * s_pitch + 16 * h;
-  mx_u32x4 sa_next[TM], sw_next[TN];      // of the next four stages, as loaded
-  mx_u32x4 sa4[TM], sw4[TN];              // of these four: element u for stage u
-  auto load_scales = [&](int four) {
+  const int vs = (lane >> 1) * s_pitch + 16 * (lane & 1);
+  auto copy_scales = [&](int four, int half) {
+    lds_byte* ls = smem + 2 * Sh::STAGE + half * Sh::SCALES;
 #pragma unroll
-    for (int i = 0; i < TM; ++i) sa_next[i] = __builtin_amdgcn_raw_buffer_load_b128(rsa, vsa, four * 32 + i * 32 * s_pitch, 0);
+    for (int k = 0; k < (Sh::BM / 32 + Sh::WAVES - 1) / Sh::WAVES; ++k) {
+      const int i = (wave + k * Sh::WAVES) % (Sh::BM / 32);       // too many wavefronts copy some rows twice
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsa, (__attribute__((address_space(3))) void*)(ls + i * 1024), 16, vs,
+                                               four * 32 + i * 32 * s_pitch, 0, 0);
+    }
 #pragma unroll
-    for (int i = 0; i < TN; ++i) sw_next[i] = __builtin_amdgcn_raw_buffer_load_b128(rsw, vsw, four * 32 + i * 32 * s_pitch, 0);
+    for (int k = 0; k < (Sh::BN / 32 + Sh::WAVES - 1) / Sh::WAVES; ++k) {
+      const int i = (wave + k * Sh::WAVES) % (Sh::BN / 32);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsw, (__attribute__((address_space(3))) void*)(ls + Sh::BM * 32 + i * 1024), 16,
+                                               vs, four * 32 + i * 32 * s_pitch, 0, 0);
+    }
+  };
+  int sa[TM], sw[TN], sa_next[TM], sw_next[TN];      // of this stage and the next
+  auto read_scales = [&](int half, int u) {
+    const lds_byte* la = smem + 2 * Sh::STAGE + half * Sh::SCALES + (wm * 32 * TM + r) * 32 + 8 * u + 4 * h;
+    const lds_byte* lw = smem + 2 * Sh::STAGE + half * Sh::SCALES + Sh::BM * 32 + (wn * 32 * TN + r) * 32 + 8 * u + 4 * h;
+#pragma unroll
+    for (int i = 0; i < TM; ++i) sa_next[i] = *reinterpret_cast<const __attribute__((address_space(3))) int*>(la + i * 1024);
+#pragma unroll
+    for (int i = 0; i < TN; ++i) sw_next[i] = *reinterpret_cast<const __attribute__((address_space(3))) int*>(lw + i * 1024);
   };
   // What lies behind the row's last block gets scales of 0 (2^-127) on both sides, which make its products vanish: the
   // second half of a last stage of 128 columns, and the stages that fill up the last four.
-  auto exchange_scales = [&](int four) {
-    const int left = p.groups - 8 * four - h;     // stage u is there for this half when 2 u < left
-    auto exchange = [&](const mx_u32x4& v) {
-      const auto p0 = __builtin_amdgcn_permlane32_swap(v.x, v.y, false, false);
-      const auto p1 = __builtin_amdgcn_permlane32_swap(v.z, v.w, false, false);
-      return mx_u32x4{0 < left ? p0[0] : 0u, 2 < left ? p1[0] : 0u, 4 < left ? p0[1] : 0u, 6 < left ? p1[1] : 0u};
-    };
+  auto take_scales = [&](int stage) {
+    const bool there = 2 * stage + h < p.groups;
 #pragma unroll
-    for (int i = 0; i < TM; ++i) sa4[i] = exchange(sa_next[i]);
+    for (int i = 0; i < TM; ++i) sa[i] = there ? sa_next[i] : 0;
 #pragma unroll
-    for (int i = 0; i < TN; ++i) sw4[i] = exchange(sw_next[i]);
+    for (int i = 0; i < TN; ++i) sw[i] = there ? sw_next[i] : 0;
   };
   const int swz_a = stage_swizzle<FMT>(r), swz_w = stage_swizzle<GALE_MX_E2M1>(r);
   auto read_step = [&](int buf, int s, v8i a[TM], v8i w[TN]) {
@@ -336,6 +348,9 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) mx_gemm_tile_kernel(const MxG
     for (int i = 0; i < TN; ++i) w[i] = stage_operand<GALE_MX_E2M1>(lw + i * 32 * 128, swz_w, h, s);
   };
 
+  copy_stage(0, 0);
+  copy_scales(0, 0);
+  copy_stage(min(1, stages - 1), 1);
   f32x16 acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
@@ -347,7 +362,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) mx_gemm_tile_kernel(const MxG
   v8i a0[TM], w0[TN], a1[TM], w1[TN];
 #define MX_STEP(S, A, W)                                                                                       \
   _Pragma("unroll") for (int i = 0; i < TM; ++i) _Pragma("unroll") for (int j = 0; j < TN; ++j) acc[i][j] =    \
-      stage_mfma<FMT, EXACT, S>(W[j], (int)sw4[j][u], A[i], (int)sa4[i][u], acc[i][j]);
+      stage_mfma<FMT, EXACT, S>(W[j], sw[j], A[i], sa[i], acc[i][j]);
 #define MX_SPREAD                                                                                  \
   _Pragma("unroll") for (int i = 0; i < Sh::READS / Sh::RPM; ++i) {                                \
     __builtin_amdgcn_sched_group_barrier(0x100, Sh::RPM, 0);                                       \
@@ -355,21 +370,21 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) mx_gemm_tile_kernel(const MxG
   }                                                                                                \
   __builtin_amdgcn_sched_barrier(0)
 
-  copy_stage(0, 0);
-  load_scales(0);
-  __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
-  __syncthreads();
-  copy_stage(min(1, stages - 1), 1);
+  static_assert(Sh::IA + Sh::IW <= 15, "the wait counts below");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (Sh::IA + Sh::IW));   // all but the second stage's copies have landed
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  read_scales(0, 0);
   read_step(0, 0, a0, w0);
   // The operands of a step are read from LDS during the products of the step before it; the fences keep the steps
   // apart and the groups spread each step's reads over its products.
-  exchange_scales(0);
   // Four stages per turn, without a branch: MFMAs are free to sink past one, and the schedule with them.
   for (int four = 0; 4 * four < stages; ++four) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int buf = u & 1;
-      if (u == 2) load_scales(four + 1);  // past the end: bytes that nothing takes
+      if (u == 2) copy_scales(four + 1, (four + 1) & 1);   // past the end: bytes that nothing takes
+      take_scales(4 * four + u);
       __builtin_amdgcn_sched_barrier(0);
       read_step(buf, 1, a1, w1);
       MX_STEP(0, a0, w0);
@@ -384,12 +399,13 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) mx_gemm_tile_kernel(const MxG
       __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) lgkmcnt(0)
       __builtin_amdgcn_s_barrier();
       __builtin_amdgcn_sched_barrier(0);
+      read_scales(u == 3 ? (four + 1) & 1 : four & 1, (u + 1) & 3);
       read_step(buf ^ 1, 0, a0, w0);
       copy_stage(min(4 * four + u + 2, stages - 1), buf);   // past the end: the last stage again
       MX_STEP(3, a1, w1);
 #pragma unroll
       for (int i = 0; i < Sh::MFMAS / 2; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x100, (2 * Sh::READS + Sh::MFMAS - 1) / Sh::MFMAS, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, (2 * (Sh::READS + TM + TN) + Sh::MFMAS - 1) / Sh::MFMAS, 0);
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
       }
 #pragma unroll
@@ -399,7 +415,6 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) mx_gemm_tile_kernel(const MxG
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    exchange_scales(four + 1);
   }
   __builtin_amdgcn_s_waitcnt(0x0F70);     // no copy is in flight when the workgroup's LDS goes
 #undef MX_STEP
@@ -464,9 +479,9 @@ static hipError_t launch_tile(const MxGemmParams& p, hipStream_t s) {
   typedef TileShape<FMT, WM, WN, TM, TN> Sh;
   const int64_t tiles = (int64_t)((p.m + Sh::BM - 1) / Sh::BM) * ((p.n + Sh::BN - 1) / Sh::BN);
   auto kern = mx_gemm_tile_kernel<T, FMT, EXACT, WM, WN, TM, TN>;
-  const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, 2 * Sh::STAGE);
+  const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, Sh::LDS);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3((unsigned)tiles), dim3(64 * Sh::WAVES), 2 * Sh::STAGE, s, p);
+  hipLaunchKernelGGL(kern, dim3((unsigned)tiles), dim3(64 * Sh::WAVES), Sh::LDS, s, p);
   return hipGetLastError();
 }
 
@@ -478,7 +493,7 @@ template <int FMT, bool EXACT, int WM, int WN, int TM, int TN>
 static float tile_cost(const MxGemmParams& p, int cus) {
   typedef TileShape<FMT, WM, WN, TM, TN> Sh;
   const int64_t tiles = (int64_t)((p.m + Sh::BM - 1) / Sh::BM) * ((p.n + Sh::BN - 1) / Sh::BN);
-  const int resident = std::min(3, (160 * 1024) / (2 * Sh::STAGE));
+  const int resident = std::min(3, (160 * 1024) / Sh::LDS);
   const float per_result = FMT == GALE_MX_E2M1 ? 4.5e-4f : EXACT ? 12e-4f : 6e-4f;
   const float turns = (float)((p.groups + 7) / 8) / 4;       // of 16 stages: whole turns of four
   const float tile = turns * (per_result * Sh::BM * Sh::BN + 0.02f * (Sh::BM * Sh::AB / 128 + Sh::BN));
