@@ -2,6 +2,15 @@
 //
 // s = x + r (rounded to the rows' type), y = s / sqrt(mean(s^2) + eps) * w.  One pass over memory: a workgroup
 // holds its row in registers between the sum of squares and the outputs.
+//
+// The 8- or 4-bit form of y is that of the exact number (to a few 2^-30): with plain 32-bit arithmetic a few elements in a million
+// took the neighbouring code and two blocks in a million the other of two scales, as the last bit of y fell.  The squares of eight
+// columns are added in 32 bits and the eights in 64, 1 / rms is held as two floats ih + il, and s w as p + q: y = p ih + t,
+// t = p il + q ih, is rounded once.  A second rounding, to the element, differs from that of the exact number only where y
+// fell on a border: halfway between two elements, or the largest number at a scale.  All borders end in 19 zero bits, which
+// one element in 2^19 does: for those the rest p ih + t - y pushes y off the border, to the side it came from.  (All in 64
+// bits the arithmetic, not HBM, bounds the kernel: 123 us for 16,384 x 4,096 bf16 with an 8-bit output.)  Rows whose squares or rms 32
+// bits do not hold well are computed in 64.
 #include "gale_mx.h"
 #include "gale_lanes.h"
 
@@ -23,19 +32,26 @@ struct NormParams {
   bool wide_x, wide_res, wide_w, wide_sum, wide_y;
 };
 
+template <int M>
+__device__ __forceinline__ double xor_f64(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = lane_xor_u32<M>((uint32_t)b), hi = lane_xor_u32<M>((uint32_t)(b >> 32));
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
 // Sum over the workgroup, in an order fixed by its size: lanes first, then wavefronts.
-__device__ __forceinline__ float block_sum(float v, float* s_wave) {
-  v += lane_xor<1>(v);
-  v += lane_xor<2>(v);
-  v += lane_xor<4>(v);
-  v += lane_xor<8>(v);
-  v += lane_xor<16>(v);
-  v += lane_xor<32>(v);
+__device__ __forceinline__ double block_sum(double v, double* s_wave) {
+  v += xor_f64<1>(v);
+  v += xor_f64<2>(v);
+  v += xor_f64<4>(v);
+  v += xor_f64<8>(v);
+  v += xor_f64<16>(v);
+  v += xor_f64<32>(v);
   const int nw = (int)blockDim.x >> 6;
   if (nw == 1) return v;
   if ((threadIdx.x & 63) == 0) s_wave[threadIdx.x >> 6] = v;
   __syncthreads();
-  float t = 0.f;
+  double t = 0.0;
   for (int i = 0; i < nw; ++i) t += s_wave[i];
   return t;
 }
@@ -43,7 +59,7 @@ __device__ __forceinline__ float block_sum(float v, float* s_wave) {
 // FMT 0: no MX output.  U: units per thread, U * blockDim.x >= row_units.
 template <typename T, int FMT, int U>
 __global__ void __launch_bounds__(1024) add_rms_norm_kernel(const NormParams p) {
-  __shared__ float s_wave[16];
+  __shared__ double s_wave[16];
   typedef typename T::bits bits;
   const int64_t row = blockIdx.x;
   const bits* xr = (const bits*)p.x + row * p.x_stride;
@@ -64,13 +80,32 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(const NormParams p) 
       for (int i = 0; i < 8; ++i) v[k][i] = T::to_f32(T::from_f32(v[k][i] + r[i]));
     }
   }
-  float sq = 0.f;
+  double sq = 0.0;
 #pragma unroll
-  for (int k = 0; k < U; ++k)
+  for (int k = 0; k < U; ++k) {
+    float e = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sq = fmaf(v[k][i], v[k][i], sq);
+    for (int i = 0; i < 8; ++i) e = fmaf(v[k][i], v[k][i], e);
+    sq += (double)e;
+  }
   sq = block_sum(sq, s_wave);
-  const float inv = 1.0f / sqrtf(sq / (float)p.cols + p.eps);
+  // the same for the whole workgroup: squares near the ends of 32 bits, or rows without a finite sum
+  const bool ordinary = sq > 1e-20 && sq < 1e35;
+  if (!ordinary) {
+    __syncthreads();
+    sq = 0.0;
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sq = fma((double)v[k][i], (double)v[k][i], sq);
+    sq = block_sum(sq, s_wave);
+  }
+  const double ms = sq / p.cols + (double)p.eps;
+  // 1 / sqrt(ms): the hardware's estimate and one Newton step, or as written for rows out of the ordinary
+  double inv = __builtin_amdgcn_rsq(ms);
+  inv = fma(inv * 0.5, fma(-ms * inv, inv, 1.0), inv);
+  if (!ordinary) inv = 1.0 / sqrt(ms);
+  const float ih = (float)inv, il = (float)(inv - (double)ih);
 #pragma unroll
   for (int k = 0; k < U; ++k) {
     const int u = (int)(threadIdx.x + k * blockDim.x), c = 8 * u;
@@ -78,20 +113,44 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(const NormParams p) 
     if (p.sum && c < p.cols) store8<T>((bits*)p.sum + row * p.cols, c, p.cols, p.wide_sum, v[k]);
     float w[8];
     if (p.w) load8_dt(p.w, p.w_dtype, c, p.cols, p.wide_w, w);
+    if (!p.w) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[k][i] = p.w ? v[k][i] * inv * w[i] : v[k][i] * inv;
+      for (int i = 0; i < 8; ++i) w[i] = 1.0f;
+    }
+    float y[8];
+    uint32_t low = 0xFFFFFFFFu;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (ordinary) {
+        const float pr = v[k][i] * w[i], q = fmaf(v[k][i], w[i], -pr);
+        y[i] = fmaf(pr, ih, fmaf(pr, il, q * ih));
+      } else {
+        y[i] = (float)((double)v[k][i] * inv * (double)w[i]);
+      }
+      if constexpr (FMT != 0) low = min(low, __float_as_uint(y[i]) & 0x7FFFFu);
+    }
     if (p.y && c < p.cols) {
       const int es = p.y_dtype == GALE_F32 ? 4 : 2;
-      store8_dt((char*)p.y + row * p.cols * es, p.y_dtype, c, p.cols, p.wide_y, v[k]);
+      store8_dt((char*)p.y + row * p.cols * es, p.y_dtype, c, p.cols, p.wide_y, y);
     }
     if constexpr (FMT != 0) {
+      if (low == 0 && ordinary) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float pr = v[k][i] * w[i], q = fmaf(v[k][i], w[i], -pr);
+          const float rest = fmaf(pr, ih, -y[i]) + fmaf(pr, il, q * ih);
+          const uint32_t b = __float_as_uint(y[i]);
+          const bool border = (b & 0x7FFFFu) == 0 && rest != 0.f && y[i] != 0.f;
+          y[i] = border ? __uint_as_float(b + ((rest > 0.f) == (y[i] > 0.f) ? 1 : -1)) : y[i];
+        }
+      }
       if (c + 8 > p.cols) {
         // columns behind the row are zero also where 1 / rms is infinite
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[k][i] = c + i < p.cols ? v[k][i] : 0.f;
+        for (int i = 0; i < 8; ++i) y[i] = c + i < p.cols ? y[i] : 0.f;
       }
       uint32_t words[2];
-      const uint32_t s = mx_encode8<FMT>(v[k], words);
+      const uint32_t s = mx_encode8<FMT>(y, words);
       mx_store8<FMT>(p.codes + row * mx_code_row(FMT, p.cols), p.scales + row * mx_scale_row(p.cols), u, s, words);
     }
   }
@@ -100,9 +159,10 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(const NormParams p) 
 template <typename T, int FMT>
 static hipError_t launch_norm_t(const NormParams& p, int64_t rows, hipStream_t s) {
   const int ru = p.row_units;
-  if (ru <= 1024) {
-    const int th = std::max(64, (ru + 63) / 64 * 64);
-    hipLaunchKernelGGL(HIP_KERNEL_NAME(add_rms_norm_kernel<T, FMT, 1>), dim3((unsigned)rows), dim3(th), 0, s, p);
+  // Few rows: one unit per thread, the shortest way through a row.  More rows than the card holds at once: two per thread,
+  // which keeps more rows in flight per CU (16,384 x 4,096 bf16: see above; 317 rows take either the same).
+  if (ru <= 512 && rows <= 2 * device_cu_count()) {
+    hipLaunchKernelGGL(HIP_KERNEL_NAME(add_rms_norm_kernel<T, FMT, 1>), dim3((unsigned)rows), dim3((ru + 63) / 64 * 64), 0, s, p);
   } else {
     hipLaunchKernelGGL(HIP_KERNEL_NAME(add_rms_norm_kernel<T, FMT, 2>), dim3((unsigned)rows),
                        dim3((ru + 127) / 128 * 64), 0, s, p);
