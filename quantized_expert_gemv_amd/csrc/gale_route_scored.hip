@@ -197,7 +197,8 @@ __device__ __forceinline__ int choose_exact(const ScoredParams& p, const float l
 //   exponential and reciprocal are within 1 ulp, two additions within half of one: below 2^-21 together.  Softmax: the
 //   same for each e^(l - max), and below 2^-20 after a sum of 512 terms (a tree of nine levels) and the reciprocal.
 //   Adding the bias rounds by 2^-24 |c|, adding two sums for a group the same once more.
-// So two experts' c are apart in truth when they differ here by more than 2^-18 + 2^-22 |c|, two groups' by twice that.
+// So two experts' c are apart in truth when they differ here by more than 2^-18 + 2^-22 |c|, two groups' values by twice that
+// with the largest |c| that any group adds.
 template <int NJ>
 __device__ __forceinline__ bool choose_fast(const ScoredParams& p, const float l[NJ], const float b[NJ], int lane, int g,
                                             int li, uint64_t* s_cand, int& my_e) {
@@ -256,7 +257,10 @@ __device__ __forceinline__ bool choose_fast(const ScoredParams& p, const float l
     if (p.log2L > 3) merge(lane_xor<8>(v1), lane_xor<8>(v2));
     if (p.log2L > 4) merge(lane_xor<16>(v1), lane_xor<16>(v2));
     const float v = p.rule == GALE_GROUP_TOP2 && v2 != -INFINITY ? v1 + v2 : v1;
-    const float margin = 2.f * (kAbs + kRel * fabsf(v));
+    // the terms' size, not their sum's, sets the error: large biases may cancel
+    float size = fmaxf(fabsf(v1), v2 == -INFINITY ? 0.f : fabsf(v2));
+    size = g < p.G && v1 != -INFINITY ? size : 0.f;
+    const float margin = 2.f * (kAbs + kRel * __uint_as_float(wave_max_u32_v(__float_as_uint(size))));
     int over = 0, near = 0;       // groups surely better, groups at least nearly as good (this one among them)
     for (int o = 0; o < p.G; ++o) {
       const float ov = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), o << p.log2L));

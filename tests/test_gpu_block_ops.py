@@ -463,6 +463,15 @@ def test_route_large_batch_of_ties(q):
     check_route(q, lg, 8, score="softmax", bias=bias, n_groups=8, keep_groups=4, renormalize=False)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_biases_that_cancel(q, score):
+    """Biases of 10,000 and -10,000 meet in the groups' sums of two: what is left is far below their own rounding in 32 bits."""
+    lg = rand((3000, 32), 5)
+    bias = torch.full((32,), -10000.0, device=DEV)
+    bias[::4] = 10000.0
+    check_route(q, lg, 4, score=score, bias=bias, n_groups=8, keep_groups=3)
+
+
 def test_route_close_scores_keep_their_order(q):
     """Biases that differ by one part in 2^40 of the scores' sum order experts that 32 bits cannot tell apart."""
     lg = torch.zeros(1, 16, device=DEV)
