@@ -10,7 +10,7 @@ namespace gale {
 // negative g: multiplied as (g e) (e / (1 + e^2)), no factor underflows before the result does.  The exponent
 // -|g| log2(e) / 2 is taken with the rounding of its product (x + lo), since the hardware's 2^x turns an absolute error of
 // x into a relative one.  The library's exponential and division bound this kernel by its arithmetic: 12.0 us for
-// 4096 x 2048 fp16 against 9 us.
+// 4096 x 2048 fp16 against 10.2.
 __device__ __forceinline__ float silu(float g) {
   const float a = fabsf(g), kHi = 0.72134752044448170f, kLo = 9.62981496e-9f;   // log2(e) / 2 = kHi + kLo
   const float x = -a * kHi;

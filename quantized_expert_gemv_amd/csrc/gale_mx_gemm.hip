@@ -487,8 +487,8 @@ static hipError_t launch_tile(const MxGemmParams& p, hipStream_t s) {
 
 // Time of a tile shape in microseconds, fitted to K = 4096 (16 stages) and N = 4096 at M = 64 .. 4096: about 6 to start and
 // end a round of resident tiles; per tile and 16 stages 4.5e-4 per result (6e-4 with 8-bit A, twice that in two parts) and
-// 0.02 per 128 bytes of its rows.  With it, M = 128 / 512 / 1024 / 2048 / 4096 in 4 bits take 7.9 / 11.3 / 16.6 / 27.7 / 46.8 us,
-// against 28 / 31 / 33 / 37 / 47 us in 256 x 256 tiles throughout and 8.4 / 11.3 / 22 / 43 / 84 us in 64 x 64.
+// 0.02 per 128 bytes of its rows.  With it, M = 128 / 512 / 1024 / 2048 / 4096 in 4 bits take 8 / 11 / 16 / 30 / 45 us, against
+// 28 / 31 / 33 / 37 / 47 us in 256 x 256 tiles throughout and 8 / 11 / 22 / 43 / 84 us in 64 x 64.
 template <int FMT, bool EXACT, int WM, int WN, int TM, int TN>
 static float tile_cost(const MxGemmParams& p, int cus) {
   typedef TileShape<FMT, WM, WN, TM, TN> Sh;
