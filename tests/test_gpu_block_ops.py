@@ -155,6 +155,16 @@ def test_swiglu_quantize(q, fmt, dtype, rows, cols):
     assert_mx_of(mx, O.swiglu(f64(x)))
 
 
+@pytest.mark.parametrize("fmt", [1, 2])
+@pytest.mark.parametrize("dtype", DTS)
+def test_swiglu_codes_are_those_of_64_bits(q, fmt, dtype):
+    """400,000 elements: about 25 of them lie within the 32-bit arithmetic's error of a border, and take the 64-bit side."""
+    x = rand((200, 4096), 21, dtype, 3.0)
+    codes, scales = elements(q.mx_swiglu_quantize(x, fmt))
+    want_c, want_s = O.mx_quantize(O.swiglu(f64(x)), fmt)
+    assert np.array_equal(scales, want_s) and np.array_equal(codes, want_c)
+
+
 def test_quantize_past_2_31_elements(q):
     rows, cols = 33000, 65536                      # 2.16e9 fp16 numbers
     x = torch.zeros(rows, cols, dtype=torch.float16, device=DEV)
