@@ -457,7 +457,7 @@ int gale_mx_quantize(const void* x, int32_t x_dtype, int64_t x_stride, int64_t r
 
 /* The same of silu(g) * u, computed in fp32 and rounded only to the element: rows of x hold g in
  * columns [0, cols) and u in [cols, 2 cols) (the output of one product with gate and up rows
- * stacked). */
+ * stacked).  A block with a product past fp32's largest number is a NaN block. */
 int gale_mx_swiglu_quantize(const void* x, int32_t x_dtype, int64_t x_stride, int64_t rows, int32_t cols,
                             int32_t fmt, uint8_t* codes, uint8_t* scales, hipStream_t stream);
 

@@ -1,0 +1,41 @@
+"""The operators around the routed layer at the ends of their range, on the GPU against the fp64 oracle.
+
+Where a test compares codes or results for equality, the operator's definition leaves no room: codes are the roundings of
+the exact numbers, and the sums of the closed forms fit the 24 bits of fp32."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import block_oracle as O
+from tests.test_gpu_block_ops import DEV, elements, q  # noqa: F401  (q: the module's fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- SwiGLU ------------------------------------------------------------------------------------------------------
+def swiglu_in_fp32(x):
+    """silu(g) u of the fp64 rows x, infinite where fp32 does not hold it."""
+    with np.errstate(over="ignore", invalid="ignore"):
+        d = O.swiglu(x)
+        return np.where(np.isinf(d.astype(np.float32)), np.sign(d) * np.inf, d)
+
+
+@pytest.mark.parametrize("fmt", [1, 2])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_swiglu_overflow_makes_its_block_nan(q, fmt, dtype):
+    """Products past fp32's largest number, infinities and NaN in either half; the last row's product stays below."""
+    x = torch.ones(8, 256, dtype=dtype)
+    x[0, 3], x[0, 131] = 1e20, 1e20
+    x[1, 40], x[1, 168] = 1e30, -1e30
+    x[2, 70], x[2, 198] = 100.0, 1e38
+    x[3, 5] = math.inf
+    x[4, 133] = -math.inf
+    x[5, 33] = math.nan
+    x[6, 100] = -math.inf
+    x[7, 0], x[7, 128] = 2.0, 1.5e38
+    codes, scales = elements(q.mx_swiglu_quantize(x.to(DEV), fmt))
+    want_c, want_s = O.mx_quantize(swiglu_in_fp32(x.double().numpy()), fmt)
+    assert [tuple(np.flatnonzero(r == 255)) for r in want_s] == [(0,), (1,), (2,), (0,), (0,), (1,), (3,), ()]
+    assert np.array_equal(scales, want_s) and np.array_equal(codes, want_c)
