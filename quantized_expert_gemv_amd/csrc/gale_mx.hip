@@ -6,13 +6,14 @@
 
 namespace gale {
 
-// g sigmoid(g), within a few ulp for every finite g.  With e = e^(-|g| / 2), sigmoid is 1 / (1 + e^2), or e^2 / (1 + e^2) for
-// negative g: multiplied as (g e) (e / (1 + e^2)), no factor underflows before the result does.  The exponent
+// g sigmoid(g), within a few ulp where the result is a normal number.  With e = e^(-|g| / 2), sigmoid is 1 / (1 + e^2), or e^2 /
+// (1 + e^2) for negative g: multiplied as (g e) (e / (1 + e^2)), no factor underflows before the result does.  The exponent
 // -|g| log2(e) / 2 is taken with the rounding of its product (x + lo), since the hardware's 2^x turns an absolute error of
 // x into a relative one.  With the library's exponential and division the arithmetic bounds the kernel
 // (4096 x 2048 fp16 into 8 bits: 12.2 us against 10.2 with two units per thread).  The codes are made those of 64-bit arithmetic: where the result
 // lies so near a border of the rounding that its error matters, one element in 16,000, it is computed in 64 bits
-// (together 10.7 us, one unit per thread).
+// (together 10.7 us, one unit per thread).  So are the results that 32 bits hold with fewer bits: subnormal products, and those
+// of a silu below 2^-120 (g under -87 or next to 0) and an up value above 1, which may bring it back among the normal numbers.
 __device__ __forceinline__ float silu(float g) {
   const float a = fabsf(g), kHi = 0.72134752044448170f, kLo = 9.62981496e-9f;   // log2(e) / 2 = kHi + kLo
   const float x = -a * kHi;
@@ -55,16 +56,27 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(const typename T::bits
   for (int k = 0; k < U; ++k) {
     if (blockIdx.x * (256u * U) + 256u * k + threadIdx.x >= n_units) return;
     if constexpr (SWIGLU) {
-      float g[8];
+      float g[8], least = INFINITY;
       uint32_t near = 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         g[j] = v[k][j];
-        v[k][j] = silu(g[j]) * up[k][j];
+        const float a = silu(g[j]);
+        v[k][j] = a * up[k][j];
+        least = fminf(least, fminf(fabsf(a), fabsf(v[k][j])));
         // off by less than 16 of its last place; borders between elements and between scales end in 19 zero bits
         near |= ((__float_as_uint(v[k][j]) + 16u) & 0x7FFFFu) <= 32u && v[k][j] != 0.f ? 1u << j : 0u;
       }
-      while (near != 0) {      // one element in 16,000
+      if (least < 0x1p-120f) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          // below g = -200 no up value brings the product back; a product rounded to zero lies far below half of the
+          // smallest element, 2^-137
+          const bool lost = fabsf(silu(g[j])) < 0x1p-120f && fabsf(up[k][j]) > 1.f && g[j] != 0.f && g[j] > -200.f;
+          near |= lost || (v[k][j] != 0.f && fabsf(v[k][j]) < 0x1p-126f) ? 1u << j : 0u;
+        }
+      }
+      while (near != 0) {
         const int n = __builtin_ctz(near);
         near &= near - 1;
         float gn = g[0], un = up[k][0];

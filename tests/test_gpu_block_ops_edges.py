@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from oracle import block_oracle as O
-from tests.test_gpu_block_ops import DEV, elements, q  # noqa: F401  (q: the module's fixture)
+from tests.test_gpu_block_ops import DEV, DTS, elements, q, rand  # noqa: F401  (q: the module's fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +39,38 @@ def test_swiglu_overflow_makes_its_block_nan(q, fmt, dtype):
     want_c, want_s = O.mx_quantize(swiglu_in_fp32(x.double().numpy()), fmt)
     assert [tuple(np.flatnonzero(r == 255)) for r in want_s] == [(0,), (1,), (2,), (0,), (0,), (1,), (3,), ()]
     assert np.array_equal(scales, want_s) and np.array_equal(codes, want_c)
+
+
+@pytest.mark.parametrize("fmt", [1, 2])
+@pytest.mark.parametrize("dtype", DTS)
+def test_swiglu_of_vanishing_gates_and_large_ups(q, fmt, dtype):
+    """silu down to 2^-190 and below, times up values of up to 2^120 (fp16: 2^13): also where silu alone is subnormal or 0."""
+    g = torch.Generator().manual_seed(1)
+    gate = -80 - 60 * torch.rand(256, 2048, generator=g)
+    gate[::4] = torch.randn(64, 2048, generator=g) * 2.0 ** -130
+    top = 13 if dtype == torch.float16 else 120
+    up = torch.randn(256, 2048, generator=g) * torch.exp2(top * torch.rand(256, 64, generator=g)).repeat_interleave(32, 1)
+    x = torch.cat((gate, up), 1).to(dtype)
+    codes, scales = elements(q.mx_swiglu_quantize(x.to(DEV), fmt))
+    want_c, want_s = O.mx_quantize(O.swiglu(x.double().numpy()), fmt)
+    assert np.array_equal(scales, want_s) and np.array_equal(codes, want_c)
+
+
+@pytest.mark.parametrize("fmt", [1, 2])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_swiglu_of_subnormal_products(q, fmt, dtype):
+    g = torch.Generator().manual_seed(2)
+    gate = torch.randn(128, 4096, generator=g)
+    x = torch.cat((gate, torch.randn(128, 4096, generator=g) * 2.0 ** -131), 1).to(dtype)
+    codes, scales = elements(q.mx_swiglu_quantize(x.to(DEV), fmt))
+    want_c, want_s = O.mx_quantize(O.swiglu(x.double().numpy()), fmt)
+    assert np.array_equal(scales, want_s) and np.array_equal(codes, want_c)
+
+
+def test_swiglu_repeats_itself(q):
+    x = rand((2048, 4096), 21, torch.float16, 3.0)
+    a = q.mx_swiglu_quantize(x, 2)
+    codes, scales = a.codes.clone(), a.scales.clone()
+    for _ in range(5):
+        b = q.mx_swiglu_quantize(x, 2)
+        assert torch.equal(b.codes, codes) and torch.equal(b.scales, scales)
