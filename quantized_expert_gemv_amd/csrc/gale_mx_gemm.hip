@@ -212,17 +212,15 @@ __device__ __forceinline__ v8i stage_operand(const lds_byte* row, int swz, int h
   }
 }
 
-template <int FMT, bool EXACT, int S>
+template <int FMT, int S>
 __device__ __forceinline__ f32x16 stage_mfma(const v8i& w, int w_scale, const v8i& a, int a_scale, f32x16 acc) {
   if constexpr (FMT == GALE_MX_E2M1) {
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, a, acc, 4, 4, S, w_scale, S, a_scale);
-  } else if constexpr (EXACT) {
+  } else {
     v8i hi, lo;
     mx_split8(a, hi, lo);
     acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, lo, acc, 4, 0, S, w_scale, S, a_scale);
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, hi, acc, 4, 0, S, w_scale, S, a_scale);
-  } else {
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, a, acc, 4, 0, S, w_scale, S, a_scale);
   }
 }
 
@@ -239,7 +237,7 @@ struct TileShape {
 };
 
 // WM x WN wavefronts, each TM x TN tiles of 32 x 32.
-template <typename T, int FMT, bool EXACT, int WM, int WN, int TM, int TN>
+template <typename T, int FMT, int WM, int WN, int TM, int TN>
 __global__ void __launch_bounds__(64 * WM * WN, 1) mx_gemm_tile_kernel(const MxGemmParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)   // buffer resources are a device type: the host pass needs the kernel's name only
   typedef TileShape<FMT, WM, WN, TM, TN> Sh;
@@ -362,7 +360,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) mx_gemm_tile_kernel(const MxG
   v8i a0[TM], w0[TN], a1[TM], w1[TN];
 #define MX_STEP(S, A, W)                                                                                       \
   _Pragma("unroll") for (int i = 0; i < TM; ++i) _Pragma("unroll") for (int j = 0; j < TN; ++j) acc[i][j] =    \
-      stage_mfma<FMT, EXACT, S>(W[j], sw[j], A[i], sa[i], acc[i][j]);
+      stage_mfma<FMT, S>(W[j], sw[j], A[i], sa[i], acc[i][j]);
 #define MX_SPREAD                                                                                  \
   _Pragma("unroll") for (int i = 0; i < Sh::READS / Sh::RPM; ++i) {                                \
     __builtin_amdgcn_sched_group_barrier(0x100, Sh::RPM, 0);                                       \
@@ -474,11 +472,11 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) mx_gemm_tile_kernel(const MxG
 #endif
 }
 
-template <typename T, int FMT, bool EXACT, int WM, int WN, int TM, int TN>
+template <typename T, int FMT, int WM, int WN, int TM, int TN>
 static hipError_t launch_tile(const MxGemmParams& p, hipStream_t s) {
   typedef TileShape<FMT, WM, WN, TM, TN> Sh;
   const int64_t tiles = (int64_t)((p.m + Sh::BM - 1) / Sh::BM) * ((p.n + Sh::BN - 1) / Sh::BN);
-  auto kern = mx_gemm_tile_kernel<T, FMT, EXACT, WM, WN, TM, TN>;
+  auto kern = mx_gemm_tile_kernel<T, FMT, WM, WN, TM, TN>;
   const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, Sh::LDS);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, dim3((unsigned)tiles), dim3(64 * Sh::WAVES), Sh::LDS, s, p);
@@ -486,15 +484,15 @@ static hipError_t launch_tile(const MxGemmParams& p, hipStream_t s) {
 }
 
 // Time of a tile shape in microseconds, fitted to K = 4096 (16 stages) and N = 4096 at M = 64 .. 4096: about 6 to start and
-// end a round of resident tiles; per tile and 16 stages 4.5e-4 per result (6e-4 with 8-bit A, twice that in two parts) and
+// end a round of resident tiles; per tile and 16 stages 4.5e-4 per result (12e-4 with 8-bit A in its two parts) and
 // 0.02 per 128 bytes of its rows.  With it, M = 128 / 512 / 1024 / 2048 / 4096 in 4 bits take 8 / 11 / 16 / 30 / 45 us, against
 // 28 / 31 / 33 / 37 / 47 us in 256 x 256 tiles throughout and 8 / 11 / 22 / 43 / 84 us in 64 x 64.
-template <int FMT, bool EXACT, int WM, int WN, int TM, int TN>
+template <int FMT, int WM, int WN, int TM, int TN>
 static float tile_cost(const MxGemmParams& p, int cus) {
   typedef TileShape<FMT, WM, WN, TM, TN> Sh;
   const int64_t tiles = (int64_t)((p.m + Sh::BM - 1) / Sh::BM) * ((p.n + Sh::BN - 1) / Sh::BN);
   const int resident = std::min(3, (160 * 1024) / Sh::LDS);
-  const float per_result = FMT == GALE_MX_E2M1 ? 4.5e-4f : EXACT ? 12e-4f : 6e-4f;
+  const float per_result = FMT == GALE_MX_E2M1 ? 4.5e-4f : 12e-4f;
   const float turns = (float)((p.groups + 7) / 8) / 4;       // of 16 stages: whole turns of four
   const float tile = turns * (per_result * Sh::BM * Sh::BN + 0.02f * (Sh::BM * Sh::AB / 128 + Sh::BN));
   const int64_t per_cu = (tiles + cus - 1) / cus;
@@ -503,7 +501,6 @@ static float tile_cost(const MxGemmParams& p, int cus) {
 
 template <typename T, int FMT>
 static hipError_t launch_best_tile(const MxGemmParams& p, hipStream_t s) {
-  constexpr bool exact = FMT == GALE_MX_E4M3 && sizeof(typename T::bits) == 4;
   const int cus = device_cu_count();
   float best = 1e30f;
   hipError_t (*run)(const MxGemmParams&, hipStream_t) = nullptr;
@@ -514,14 +511,14 @@ static hipError_t launch_best_tile(const MxGemmParams& p, hipStream_t s) {
     }
   };
   if constexpr (FMT == GALE_MX_E2M1) {
-    offer(tile_cost<FMT, exact, 4, 2, 2, 4>(p, cus), launch_tile<T, FMT, exact, 4, 2, 2, 4>);   // 256 x 256
-    offer(tile_cost<FMT, exact, 2, 2, 2, 4>(p, cus), launch_tile<T, FMT, exact, 2, 2, 2, 4>);   // 128 x 256
+    offer(tile_cost<FMT, 4, 2, 2, 4>(p, cus), launch_tile<T, FMT, 4, 2, 2, 4>);   // 256 x 256
+    offer(tile_cost<FMT, 2, 2, 2, 4>(p, cus), launch_tile<T, FMT, 2, 2, 2, 4>);   // 128 x 256
   } else {
-    offer(tile_cost<FMT, exact, 4, 2, 1, 4>(p, cus), launch_tile<T, FMT, exact, 4, 2, 1, 4>);   // 128 x 256
+    offer(tile_cost<FMT, 4, 2, 1, 4>(p, cus), launch_tile<T, FMT, 4, 2, 1, 4>);   // 128 x 256
   }
-  offer(tile_cost<FMT, exact, 2, 2, 2, 2>(p, cus), launch_tile<T, FMT, exact, 2, 2, 2, 2>);     // 128 x 128
-  offer(tile_cost<FMT, exact, 2, 2, 1, 2>(p, cus), launch_tile<T, FMT, exact, 2, 2, 1, 2>);     // 64 x 128
-  offer(tile_cost<FMT, exact, 2, 2, 1, 1>(p, cus), launch_tile<T, FMT, exact, 2, 2, 1, 1>);     // 64 x 64
+  offer(tile_cost<FMT, 2, 2, 2, 2>(p, cus), launch_tile<T, FMT, 2, 2, 2, 2>);     // 128 x 128
+  offer(tile_cost<FMT, 2, 2, 1, 2>(p, cus), launch_tile<T, FMT, 2, 2, 1, 2>);     // 64 x 128
+  offer(tile_cost<FMT, 2, 2, 1, 1>(p, cus), launch_tile<T, FMT, 2, 2, 1, 1>);     // 64 x 64
   return run(p, s);
 }
 

@@ -9,7 +9,8 @@ import pytest
 import torch
 
 from oracle import block_oracle as O
-from tests.test_gpu_block_ops import DEV, DTS, elements, q, rand  # noqa: F401  (q: the module's fixture)
+from tests.test_gpu_block_ops import (DEV, DTS, MFMA, elements, half_step, operand, q, rand,  # noqa: F401
+                                      subnormal)
 
 pytestmark = pytest.mark.gpu
 
@@ -74,3 +75,36 @@ def test_swiglu_repeats_itself(q):
     for _ in range(5):
         b = q.mx_swiglu_quantize(x, 2)
         assert torch.equal(b.codes, codes) and torch.equal(b.scales, scales)
+
+
+# ---- products of 8-bit rows --------------------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", DTS)
+@pytest.mark.parametrize("m", [1, 20, 32, 33, 40, 300, 2100])
+def test_gemm_keeps_small_elements_in_every_type(q, m, dtype):
+    """8-bit elements of 2^-9 next to 256 and -256, whose products cancel: the sums fit 24 bits, so y is their rounding,
+    by either side of the kernels' 32-row border."""
+    g = torch.Generator(device=DEV).manual_seed(m)
+    k, n = 384, 80
+    a = torch.randint(-7, 8, (m, k), generator=g, device=DEV).float() * 2.0 ** -9
+    a[:, ::8] = 256.0
+    a[:, 8::16] = -256.0
+    w = torch.randint(-1, 2, (n, k), generator=g, device=DEV).float()
+    w[:, 0::8] = 6.0                               # scales of 1
+    qa, qw = q.mx_quantize(a, 2), q.mx_quantize(w, 1)
+    assert torch.equal(qa.dequantize(), a) and torch.equal(qw.dequantize(), w)
+    want = (a.double() @ w.double().T).float()
+    assert torch.equal(q.mx_gemm(qa, qw, out_dtype=dtype), want.to(dtype))
+
+
+@pytest.mark.parametrize("dtype", DTS)
+@pytest.mark.parametrize("m,n,k", [(33, 257, 640), (200, 130, 2048), (600, 1030, 1500), (2050, 2050, 512)])
+def test_gemm_of_8_bit_rows_loses_no_product(q, m, n, k, dtype):
+    """The bound of an fp32 sum and one rounding, with nothing for cut products; rows with elements twenty times the rest."""
+    x = rand((m, k), 3)
+    x[:, ::29] *= 20.0
+    a, w = q.mx_quantize(x, 2), operand(q, n, k, 1, 4)
+    y = q.mx_gemm(a, w, out_dtype=dtype).double()
+    A, W = a.dequantize().double(), w.dequantize().double()
+    want, size = A @ W.T, A.abs() @ W.abs().T
+    err = (y - want).abs()
+    assert (err <= half_step(dtype) * want.abs() + MFMA * size * (1 + half_step(dtype)) + subnormal(dtype)).all()
