@@ -108,3 +108,54 @@ def test_gemm_of_8_bit_rows_loses_no_product(q, m, n, k, dtype):
     want, size = A @ W.T, A.abs() @ W.abs().T
     err = (y - want).abs()
     assert (err <= half_step(dtype) * want.abs() + MFMA * size * (1 + half_step(dtype)) + subnormal(dtype)).all()
+
+
+def cornered(m, n, k):
+    """Operands of zeros whose blocks have scales of 1, set by a 448 of a and a 6 of w that meet zeros."""
+    a, w = torch.zeros(m, k, device=DEV), torch.zeros(n, k, device=DEV)
+    a[:, 31::32], w[:, 30::32] = 448.0, 6.0
+    return a, w
+
+
+def assert_exact_product(q, a, w):
+    qa, qw = q.mx_quantize(a, 2), q.mx_quantize(w, 1)
+    assert torch.equal(qa.dequantize(), a) and torch.equal(qw.dequantize(), w)
+    assert torch.equal(q.mx_gemm(qa, qw, out_dtype=torch.float32).double(), a.double() @ w.double().T)
+
+
+@pytest.mark.parametrize("m", [1, 20, 40, 300])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("large,small,by", [(3.75, 2.0 ** -9, 0.5), (3.75, 3 * 2.0 ** -9, 0.5), (3.75, 13 * 2.0 ** -9, 1.5),
+                                            (3.5, 5 * 2.0 ** -9, 0.5), (2.0, 2.0 ** -9, 0.5), (448.0, 4.5, 0.5),
+                                            (448.0, 4.5, 1.5), (448.0, 5.0, 0.5), (416.0, 4.5, 0.5)])
+def test_gemm_split_keeps_products_whole(q, m, sign, large, small, by):
+    """The largest product of either part of an 8-bit operand, times 6 with a carry, next to the smallest of the same part in
+    the same eight columns: the sums fit 24 bits, so any cut shows."""
+    a, w = cornered(m, 64, 128)
+    for b in range(0, 128, 32):
+        a[:, b], w[:, b] = sign * large, 6.0
+        a[:, b + 1:b + 8] = small * torch.tensor([1, 1, 0, 1, 1, 0, 1.0], device=DEV)
+        w[:, b + 1:b + 8] = by
+    assert_exact_product(q, a, w)
+
+
+@pytest.mark.parametrize("m", [4, 30, 64, 1000])
+def test_gemm_of_any_four_products_is_exact(q, m):
+    """Four elements of one eight, any of either format: their sum fits 24 bits."""
+    g = torch.Generator().manual_seed(m)
+    a, w = cornered(m, 512, 128)
+    sign = lambda *shape: 1 - 2 * torch.randint(0, 2, shape, generator=g)    # noqa: E731
+    four = torch.zeros(m, 8).scatter_(1, torch.rand(m, 8, generator=g).argsort(1)[:, :4], 1.0)
+    a[:, :8] = (torch.from_numpy(O.E4M3).float()[torch.randint(0, 127, (m, 8), generator=g)] * four * sign(m, 8)).to(DEV)
+    w[:, :8] = (torch.from_numpy(O.E2M1).float()[torch.randint(0, 8, (512, 8), generator=g)] * sign(512, 8)).to(DEV)
+    assert_exact_product(q, a, w)
+
+
+@pytest.mark.parametrize("fmt", [1, 2])
+@pytest.mark.parametrize("m", [4, 64])
+def test_gemm_of_subnormal_results(q, fmt, m):
+    a, w = q.mx_quantize(rand((m, 128), 3) * 2.0 ** -68, fmt), q.mx_quantize(rand((64, 128), 4) * 2.0 ** -68, 1)
+    y = q.mx_gemm(a, w, out_dtype=torch.float32).double()
+    A, W = a.dequantize().double(), w.dequantize().double()
+    # each of the two parts' eights may round to 2^-149
+    assert ((y - A @ W.T).abs() <= MFMA * (A.abs() @ W.abs().T) + 32 * 2.0 ** -150).all()
