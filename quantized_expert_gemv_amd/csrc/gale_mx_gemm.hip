@@ -528,7 +528,7 @@ static hipError_t launch_best_tile(const MxGemmParams& p, hipStream_t s) {
 
 template <typename T, int FMT>
 static hipError_t mx_gemm_t(const MxGemmParams& p, hipStream_t s) {
-  // at most 2^16 rows of tiles per launch
+  // 2^19 rows per launch, so that a launch's tiles stay far below a grid's limit
   for (int m0 = 0; m0 < p.m; m0 += 1 << 19) {
     MxGemmParams q = p;
     q.m = std::min(p.m - m0, 1 << 19);

@@ -159,3 +159,15 @@ def test_gemm_of_subnormal_results(q, fmt, m):
     A, W = a.dequantize().double(), w.dequantize().double()
     # each of the two parts' eights may round to 2^-149
     assert ((y - A @ W.T).abs() <= MFMA * (A.abs() @ W.abs().T) + 32 * 2.0 ** -150).all()
+
+
+@pytest.mark.parametrize("fmt", [1, 2])
+def test_gemm_of_more_rows_than_a_launch_takes(q, fmt):
+    """2^19 rows and a few: the second launch starts at its own rows of a, add and y."""
+    m, n, k = (1 << 19) + 17, 40, 160
+    a, w, c = operand(q, m, k, fmt, 1), operand(q, n, k, 1, 2), rand((m, n + 3), 3, torch.float16)[:, 1:1 + n]
+    y = q.mx_gemm(a, w, add=c)
+    A, W = a.dequantize().double(), w.dequantize().double()
+    want, size = A @ W.T + c.double(), A.abs() @ W.abs().T + c.double().abs()
+    t = half_step(torch.float16)
+    assert ((y.double() - want).abs() <= t * want.abs() + MFMA * size * (1 + t) + subnormal(torch.float16)).all()
