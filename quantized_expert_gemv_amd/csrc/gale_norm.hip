@@ -140,7 +140,8 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(const NormParams p) 
           const float pr = v[k][i] * w[i], q = fmaf(v[k][i], w[i], -pr);
           const float rest = fmaf(pr, ih, -y[i]) + fmaf(pr, il, q * ih);
           const uint32_t b = __float_as_uint(y[i]);
-          const bool border = (b & 0x7FFFFu) == 0 && rest != 0.f && y[i] != 0.f;
+          // infinity is no border: it stays, and makes its block NaN
+          const bool border = (b & 0x7FFFFu) == 0 && rest != 0.f && y[i] != 0.f && fabsf(y[i]) < INFINITY;
           y[i] = border ? __uint_as_float(b + ((rest > 0.f) == (y[i] > 0.f) ? 1 : -1)) : y[i];
         }
       }

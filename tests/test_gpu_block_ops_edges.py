@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from oracle import block_oracle as O
-from tests.test_gpu_block_ops import (DEV, DTS, MFMA, elements, half_step, operand, q, rand,  # noqa: F401
+from tests.test_gpu_block_ops import (DEV, DTS, MFMA, WORK, elements, f64, half_step, operand, q, rand,  # noqa: F401
                                       subnormal)
 
 pytestmark = pytest.mark.gpu
@@ -171,3 +171,30 @@ def test_gemm_of_more_rows_than_a_launch_takes(q, fmt):
     want, size = A @ W.T + c.double(), A.abs() @ W.abs().T + c.double().abs()
     t = half_step(torch.float16)
     assert ((y.double() - want).abs() <= t * want.abs() + MFMA * size * (1 + t) + subnormal(torch.float16)).all()
+
+
+# ---- norm --------------------------------------------------------------------------------------------------------
+def check_norm(q, x, w, fmt, eps=0.0):
+    """y and, with fmt, the codes of the exact numbers; what fp32 does not hold is infinite, and its block NaN."""
+    y, _, mx = q.add_rms_norm(x, w, eps=eps, out_dtype=torch.float32, mx_fmt=fmt)
+    exact = O.rms_norm(f64(x), f64(w), eps)
+    with np.errstate(over="ignore"):
+        near = exact.astype(np.float32).astype(np.float64)
+    held = np.isfinite(near)
+    assert np.array_equal(f64(y)[~held], near[~held])
+    err = np.abs(f64(y) - exact)[held]
+    assert (err <= (half_step(torch.float32) + WORK) * np.abs(exact[held]) + subnormal(torch.float32)).all()
+    if fmt:
+        want_c, want_s = O.mx_quantize(np.where(held, exact, near), fmt)
+        codes, scales = elements(mx)
+        assert np.array_equal(scales, want_s) and np.array_equal(codes, want_c)
+    return held
+
+
+@pytest.mark.parametrize("fmt", [None, 1, 2])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_norm_overflow_makes_its_block_nan(q, fmt, dtype):
+    x = rand((6, 96), 1, dtype, 1e-9)
+    w = (rand((96,), 2).double() * 1e38).clamp(-3e38, 3e38).float()
+    held = check_norm(q, x, w, fmt)
+    assert held.any() and not held.all()
