@@ -143,6 +143,17 @@ __device__ __forceinline__ uint32_t mx_encode8(const float v[8], uint32_t words[
   return nan ? 255u : (uint32_t)s;
 }
 
+// A 64-bit number is rounded to odd in 32: a second rounding then goes as it would from the number itself.  odd_step: what
+// that adds to the bits of f, d rounded to nearest.  What 32 bits do not hold stays infinite, and makes its block NaN.
+__device__ __forceinline__ int odd_step(double d, float f) {
+  if (!(fabsf(f) < INFINITY) || (double)f == d || (__float_as_uint(f) & 1u)) return 0;
+  return fabs(d) > fabs((double)f) ? 1 : -1;
+}
+__device__ __forceinline__ float f32_to_odd(double d) {
+  const float f = (float)d;
+  return __uint_as_float(__float_as_uint(f) + odd_step(d, f));
+}
+
 // Stores a lane's part of an encoded block: unit u = column / 8 of the row; the quad's first lane stores the
 // scale.
 template <int FMT>

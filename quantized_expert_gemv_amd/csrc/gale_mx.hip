@@ -24,14 +24,9 @@ __device__ __forceinline__ float silu(float g) {
   return g < 0.f ? (g * e) * (e * r) : g * r;
 }
 
-// silu(g) u in 64 bits, rounded to odd in 32: a second rounding then goes as it would from the number itself.  What 32 bits
-// do not hold stays infinite, so that its block becomes a NaN block.
+// silu(g) u in 64 bits, rounded to odd in 32.
 __device__ __forceinline__ float swiglu_odd(float g, float u) {
-  const double d = (double)g * (1.0 / (1.0 + exp(-(double)g))) * (double)u;
-  const float f = (float)d;
-  if (!(fabsf(f) < INFINITY)) return f;
-  const uint32_t b = __float_as_uint(f);
-  return (double)f != d && !(b & 1u) ? __uint_as_float(b + (fabs(d) > fabs((double)f) ? 1 : -1)) : f;
+  return f32_to_odd((double)g * (1.0 / (1.0 + exp(-(double)g))) * (double)u);
 }
 
 // Units (8 columns, padded rows) of a launch are numbered row by row; the host keeps their count below 2^31.

@@ -10,7 +10,7 @@
 // fell on a border: halfway between two elements, or the largest number at a scale.  All borders end in 19 zero bits, which
 // one element in 2^19 does: for those the rest p ih + t - y pushes y off the border, to the side it came from.  (All in 64
 // bits the arithmetic, not HBM, bounds the kernel: 123 us for 16,384 x 4,096 bf16 with an 8-bit output.)  Rows whose squares or rms 32
-// bits do not hold well are computed in 64.
+// bits do not hold well are computed in 64, and so are eights of columns with a product or result near the ends of 32 bits.
 #include "gale_mx.h"
 #include "gale_lanes.h"
 
@@ -117,24 +117,47 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(const NormParams p) 
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[i] = 1.0f;
     }
-    float y[8];
+    float y[8], least = INFINITY, most = 0.f;
     uint32_t low = 0xFFFFFFFFu;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if (ordinary) {
-        const float pr = v[k][i] * w[i], q = fmaf(v[k][i], w[i], -pr);
-        y[i] = fmaf(pr, ih, fmaf(pr, il, q * ih));
-      } else {
-        y[i] = (float)((double)v[k][i] * inv * (double)w[i]);
-      }
+      const float pr = v[k][i] * w[i], q = fmaf(v[k][i], w[i], -pr);
+      y[i] = fmaf(pr, ih, fmaf(pr, il, q * ih));
+      least = fminf(least, fminf(fabsf(pr), fabsf(y[i])));
+      most = fmaxf(most, fabsf(pr));
       if constexpr (FMT != 0) low = min(low, __float_as_uint(y[i]) & 0x7FFFFu);
+    }
+    // Products and results near the ends of 32 bits, where p + q or t are not whole, go by 64.  A zero factor needs neither: its
+    // product is y, with its sign.
+    bool far = !ordinary;
+    if (least < 0x1p-100f || most > 0x1p126f) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float pr = v[k][i] * w[i];
+        const bool zero = v[k][i] == 0.f || w[i] == 0.f;
+        far = far || fabsf(pr) > 0x1p126f || (fminf(fabsf(pr), fabsf(y[i])) < 0x1p-100f && !zero);
+        y[i] = zero ? pr : y[i];
+      }
+    }
+    uint32_t odd = 0;                 // two bits per column: the step of its rounding to odd, and one
+    if (far) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const double d = (double)v[k][i] * inv * (double)w[i];
+        y[i] = (float)d;
+        if constexpr (FMT != 0) odd |= (uint32_t)(odd_step(d, y[i]) + 1) << (2 * i);
+        __builtin_amdgcn_sched_barrier(0);     // one after the other: registers for eight at once would cost occupancy
+      }
     }
     if (p.y && c < p.cols) {
       const int es = p.y_dtype == GALE_F32 ? 4 : 2;
       store8_dt((char*)p.y + row * p.cols * es, p.y_dtype, c, p.cols, p.wide_y, y);
     }
     if constexpr (FMT != 0) {
-      if (low == 0 && ordinary) {
+      if (far) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = __uint_as_float(__float_as_uint(y[i]) + ((odd >> (2 * i)) & 3u) - 1u);
+      } else if (low == 0) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float pr = v[k][i] * w[i], q = fmaf(v[k][i], w[i], -pr);

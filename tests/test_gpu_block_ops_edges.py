@@ -198,3 +198,16 @@ def test_norm_overflow_makes_its_block_nan(q, fmt, dtype):
     w = (rand((96,), 2).double() * 1e38).clamp(-3e38, 3e38).float()
     held = check_norm(q, x, w, fmt)
     assert held.any() and not held.all()
+
+
+@pytest.mark.parametrize("fmt", [None, 1, 2])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("scale,weight,cols", [(1e16, 1e23, 64), (1e16, 1e22, 100), (1e-9, 1e-31, 96), (1e-9, 1e-37, 33),
+                                               (1.0, 1e38, 64), (1.0, 3e38, 64), (1.0, 1e-38, 64), (1e10, 1e-38, 520),
+                                               (1e18, 1.0, 64), (1e-30, 1.0, 64), (1e-30, 1e30, 64)])
+def test_norm_of_extreme_rows_and_weights(q, fmt, dtype, scale, weight, cols):
+    """Products of a row and its weights that pass fp32's ends where the result does not, subnormal results, and rows that go
+    by 64 bits; zeros among them."""
+    x, w = rand((40, cols), 1, dtype, scale), (rand((cols,), 2).double() * weight).clamp(-3e38, 3e38).float()
+    x[:, 5], w[7] = 0, 0
+    check_norm(q, x, w, fmt)
