@@ -404,9 +404,9 @@ int gale_route_topk(const float* logits, int32_t n_tok, int32_t n_experts, int32
 /* The routed layer of gale_moe_layer_fwd_routed with each token's experts AND their weights given
  * (the outputs of gale_route_scored, or any other router): y[t] = sum over slots j, in order, of
  * topk_w[t][j] * FFN_{topk_idx[t][j]}(x[t]).  topk_idx: int32 [n_tok][top_k]; topk_w: fp32
- * [n_tok][top_k].  A slot with no expert has index -1 and weight 0 (an index outside
- * [0, n_experts) is clamped into it, so such a slot still computes an expert and adds 0 times its
- * output).  Same workspace, paths and flags as gale_moe_layer_fwd; fp16 x and y. */
+ * [n_tok][top_k].  A slot with a negative index has no expert and adds nothing, whatever its
+ * weight; a token with no expert at all gets y = 0.  An index past the last expert is clamped to it.
+ * Same workspace, paths and flags as gale_moe_layer_fwd; fp16 x and y. */
 int gale_moe_layer_fwd_given(int32_t hidden, int32_t inter, const gale_expert* experts_dev,
                              int32_t n_experts, const int32_t* topk_idx, const float* topk_w, int32_t top_k,
                              const void* x, int32_t n_tok, void* y, void* ws, size_t ws_bytes, uint32_t flags,

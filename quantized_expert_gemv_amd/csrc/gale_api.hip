@@ -672,7 +672,7 @@ static int moe_layer(const char* fn, int32_t hidden, int32_t inter, const gale_e
                                             max_tiles, ht16, yp, hidden, stream));
     if (st) return st;
   }
-  return hip_status(fn, launch_combine(yp, wts, n_tok, top_k, hidden, y, GALE_F16, stream));
+  return hip_status(fn, launch_combine(yp, wts, fixed_w ? idx : nullptr, n_tok, top_k, hidden, y, GALE_F16, stream));
 }
 
 extern "C" int gale_moe_layer_fwd(int32_t hidden, int32_t inter, const gale_expert* experts_dev,

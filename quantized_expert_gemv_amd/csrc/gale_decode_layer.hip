@@ -686,6 +686,13 @@ __global__ void __launch_bounds__(512) decode_stack_kernel(const StackParams P) 
         topk_wave_vals(lgv, P.E, Pk, lane, s_exp, s_w, s_exp);
       else
         topk_wave(RouteIn{io.logits, io.select_bias, io.fixed_idx, P.weights0}, 0, P.E, Pk, lane, s_exp, s_w, s_exp);
+      if (P.weights0 != nullptr) {
+        // slots without an expert run expert 0 along with the others; their sums are dropped below
+        const bool none = lane < Pk && s_exp[lane] < 0;
+        const uint64_t mask = __ballot(none);
+        if (lane == 0) s_hdr[4] = (uint32_t)mask;
+        if (none) s_exp[lane] = 0;
+      }
       __builtin_amdgcn_s_setprio(0);
     }
     if (wave == W - 1 && l == 0) warm_table(table, P.E, lane, s_hdr + 3);
@@ -915,6 +922,14 @@ __global__ void __launch_bounds__(512) decode_stack_kernel(const StackParams P) 
       __syncthreads();
       // wave 0: y = sum over slots in order of w_j (sum over chunks in order + outliers)
       if (wave == 0 && lane < 16) {
+        if (P.weights0 != nullptr) {
+          for (uint32_t mask = (uint32_t)uni((int)s_hdr[4]); mask != 0; mask &= mask - 1) {
+            const int j = __builtin_ctz(mask);
+            for (int c = 0; c < C_I; ++c) dpart[(j * C_I + c) * 16 + lane] = 0.f;
+            dout[j * 16 + lane] = 0.f;
+            s_w[j] = 0.f;
+          }
+        }
         float acc;
         switch (C_I) {
           case 1: acc = combine_y<1>(dpart, dout, s_w, Pk, lane); break;

@@ -122,6 +122,7 @@ __device__ __forceinline__ bool filter_keep(const VecFilter& f, int64_t v) {
   bool keep = false;
   for (int s = 0; s < n; ++s) {
     const int e = __builtin_amdgcn_readfirstlane(ex[s]);
+    if (e < 0) continue;      // a slot without an expert
     const bool items = f.offsets[e + 1] - f.offsets[e] < f.split;
     keep = keep || (items == (f.items_side != 0));
   }
@@ -171,7 +172,7 @@ hipError_t launch_route_large(const RouteIn& rin, int n_tok, int n_exp, int k, i
 inline size_t route_chunk_count_bytes(int n_tok, int n_exp) {
   return (size_t)4 * ((n_tok + 63) / 64) * n_exp;
 }
-hipError_t launch_combine(const float* ypairs, const float* w, int n_tok, int k, int hidden,
+hipError_t launch_combine(const float* ypairs, const float* w, const int32_t* idx, int n_tok, int k, int hidden,
                           void* y, int y_dtype, hipStream_t s);
 hipError_t launch_cast(const float* src, void* dst, int dst_dtype, int64_t n, hipStream_t s);
 

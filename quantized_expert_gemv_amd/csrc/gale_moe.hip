@@ -60,8 +60,9 @@ __device__ __forceinline__ void route_small_body(const RouteIn& rin, int T, int 
   }
   const int P = T * k;
   __syncthreads();
-  // per-expert counts (integer atomics: order-free)
-  for (int p = tid; p < P; p += blockDim.x) atomicAdd(&s_cnt[s_idx[p]], 1);
+  // per-expert counts (integer atomics: order-free); pairs without an expert are in no list
+  for (int p = tid; p < P; p += blockDim.x)
+    if (s_idx[p] >= 0) atomicAdd(&s_cnt[s_idx[p]], 1);
   __syncthreads();
   {
     // blockDim.x == 512 >= E: thread e owns expert e
@@ -79,7 +80,8 @@ __device__ __forceinline__ void route_small_body(const RouteIn& rin, int T, int 
   }
   __syncthreads();
   // each pair into its expert's range, in any order
-  for (int p = tid; p < P; p += blockDim.x) s_pairs[atomicAdd(&s_fill[s_idx[p]], 1)] = p;
+  for (int p = tid; p < P; p += blockDim.x)
+    if (s_idx[p] >= 0) s_pairs[atomicAdd(&s_fill[s_idx[p]], 1)] = p;
   __syncthreads();
   if (offsets)
     for (int e = tid; e <= E; e += blockDim.x) offsets[e] = s_off[e];
@@ -188,7 +190,8 @@ __global__ void __launch_bounds__(1024) route_topk_count_kernel(const RouteIn ri
     topk_wave(rin, t, E, k, lane, idx + (int64_t)t * k, w + (int64_t)t * k,
               s_idx + (t - t0) * k);
   __syncthreads();
-  for (int p = tid; p < (t1 - t0) * k; p += blockDim.x) atomicAdd(&s_cnt[s_idx[p]], 1);
+  for (int p = tid; p < (t1 - t0) * k; p += blockDim.x)
+    if (s_idx[p] >= 0) atomicAdd(&s_cnt[s_idx[p]], 1);
   __syncthreads();
   if (chunk_cnt)
     for (int e = tid; e < E; e += blockDim.x) chunk_cnt[(int64_t)chunk * E + e] = s_cnt[e];
@@ -267,13 +270,14 @@ hipError_t launch_route_large(const RouteIn& rin, int n_tok, int n_exp, int k, i
 }
 
 // ---------------------------------------------------------------------------
-// combine: y[t][n] = sum_j w[t][j] * ypairs[t k + j][n], slots in order
+// combine: y[t][n] = sum_j w[t][j] * ypairs[t k + j][n], slots in order.  idx (NULL: every slot has an
+// expert): slots of index -1 have no row of ypairs and are left out.
 // ---------------------------------------------------------------------------
 // Four columns per thread: the partial rows (workspace, 16-byte aligned, H % 4 == 0) are read
 // as float4.  Each element's sum is the same fp32 sequence as before: fma over the k slots in
 // order from 0.
 __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ yp, const float* __restrict__ w,
-                                                      int T, int k, int H, void* __restrict__ y, int y_dtype) {
+                                                      const int32_t* __restrict__ idx, int T, int k, int H, void* __restrict__ y, int y_dtype) {
   const int H4 = H >> 2;
   const int64_t total = (int64_t)T * H4;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
@@ -281,6 +285,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
     const int n = 4 * (int)(i - (int64_t)t * H4);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int j = 0; j < k; ++j) {
+      if (idx && idx[t * k + j] < 0) continue;
       const float wj = w[t * k + j];
       const float4 v = *reinterpret_cast<const float4*>(yp + ((int64_t)t * k + j) * H + n);
       acc.x = fmaf(wj, v.x, acc.x);
@@ -305,12 +310,12 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
   }
 }
 
-hipError_t launch_combine(const float* ypairs, const float* w, int n_tok, int k, int hidden, void* y,
+hipError_t launch_combine(const float* ypairs, const float* w, const int32_t* idx, int n_tok, int k, int hidden, void* y,
                           int y_dtype, hipStream_t s) {
   const int64_t total = (int64_t)n_tok * (hidden / 4);
   if (total == 0) return hipSuccess;
   int g = (int)std::min<int64_t>((total + 255) / 256, 16384);
-  hipLaunchKernelGGL(combine_kernel, dim3(g), dim3(256), 0, s, ypairs, w, n_tok, k, hidden, y, y_dtype);
+  hipLaunchKernelGGL(combine_kernel, dim3(g), dim3(256), 0, s, ypairs, w, idx, n_tok, k, hidden, y, y_dtype);
   return hipGetLastError();
 }
 

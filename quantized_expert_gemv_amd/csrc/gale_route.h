@@ -240,10 +240,11 @@ __device__ __forceinline__ void topk_wave(const RouteIn& in, int t, int E, int k
     else topk_rounds<8>(lg, E, k, lane, m, my_v, my_i, lds_idx);
   } else {
     if (in.weights != nullptr) {
-      // given experts (clamped into range) with given weights: nothing to compute
+      // given experts with given weights: nothing to compute.  -1: a slot without an expert, which the caller leaves out
+      // (others are clamped into range)
       if (lane < k) {
         const int e = in.fixed[(int64_t)t * k + lane];
-        out_idx[lane] = lds_idx[lane] = e < 0 ? 0 : (e >= E ? E - 1 : e);
+        out_idx[lane] = lds_idx[lane] = e < 0 ? -1 : (e >= E ? E - 1 : e);
         out_w[lane] = in.weights[(int64_t)t * k + lane];
       }
       return;

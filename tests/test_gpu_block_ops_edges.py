@@ -211,3 +211,63 @@ def test_norm_of_extreme_rows_and_weights(q, fmt, dtype, scale, weight, cols):
     x, w = rand((40, cols), 1, dtype, scale), (rand((cols,), 2).double() * weight).clamp(-3e38, 3e38).float()
     x[:, 5], w[7] = 0, 0
     check_norm(q, x, w, fmt)
+
+
+# ---- the routed layer with slots that have no expert ------------------------------------------------------------
+@pytest.fixture(scope="module")
+def two_tables(q):
+    """The same experts twice; in the second table every number of expert 0 is NaN."""
+    from synth import config_seed, gen_matrices
+    seed = config_seed(72)
+    H, I, E = 2048, 1024, 12
+    up = gen_matrices(seed, [(e, m) for e in range(E) for m in (0, 1)], I, H, device=torch.device(DEV))
+    down = gen_matrices(seed, [(e, 2) for e in range(E)], H, I, device=torch.device(DEV))
+    packed = [(q.pack_matrix(up[2 * e]), q.pack_matrix(up[2 * e + 1]), q.pack_matrix(down[e])) for e in range(E)]
+    for m in (up[0], up[1], down[0]):
+        m.block_scales.fill_(0x7E00)
+    bad = tuple(q.pack_matrix(m) for m in (up[0], up[1], down[0]))
+    return H, I, E, q.expert_table(packed), q.expert_table([bad] + packed[1:])
+
+
+def paths(q, T):
+    """Flags of every path of the layer that takes T tokens."""
+    flags = [0, q.GALE_PATH_GROUPED]
+    return flags + [q.GALE_DECODE_STAGED, q.GALE_PATH_DECODE] if T <= 64 else flags
+
+
+@pytest.mark.parametrize("T", [1, 3, 64, 100, 700])
+@pytest.mark.parametrize("k", [1, 4, 8])
+def test_given_slots_without_an_expert_add_nothing(q, two_tables, T, k):
+    """No bit of y hangs on expert 0 where no slot names it, even if all its numbers are NaN; tokens without any expert are
+    zero, and the weight of an empty slot does not matter."""
+    H, I, E, good, bad = two_tables
+    g = torch.Generator().manual_seed(100 * T + k)
+    idx = 1 + torch.rand(T, E - 1, generator=g).argsort(1)[:, :k].int()
+    idx[torch.rand(T, k, generator=g) < 0.4] = -1
+    idx[T // 2] = -1 if T > 1 else idx[T // 2]
+    w = torch.rand(T, k, generator=g)
+    x = rand((T, H), 5, torch.float16)
+    for flags in paths(q, T):
+        for choice in (idx, torch.full_like(idx, -1)):
+            i = choice.to(DEV)
+            y = q.moe_layer_fwd_given(good, H, I, i, w.to(DEV), x, flags=flags)
+            assert y.isfinite().all() and (y[(i < 0).all(1)] == 0).all()
+            assert torch.equal(q.moe_layer_fwd_given(bad, H, I, i, w.to(DEV), x, flags=flags), y)
+            odd = torch.where(i < 0, torch.full_like(i, 3).float() * math.nan, w.to(DEV))
+            assert torch.equal(q.moe_layer_fwd_given(bad, H, I, i, odd, x, flags=flags), y)
+
+
+@pytest.mark.parametrize("T", [1, 5, 64, 300])
+def test_given_empty_slots_are_as_if_absent(q, two_tables, T):
+    """With one column of slots empty for every token, y is that of the call without this column."""
+    H, I, E, good, _ = two_tables
+    idx = torch.rand(T, E, generator=torch.Generator().manual_seed(T)).argsort(1)[:, :4].int().to(DEV)
+    w, x = torch.rand(T, 4, device=DEV), rand((T, H), 6, torch.float16)
+    for flags in paths(q, T):
+        for c in range(4):
+            rest = [j for j in range(4) if j != c]
+            holed = idx.clone()
+            holed[:, c] = -1
+            y = q.moe_layer_fwd_given(good, H, I, holed, w, x, flags=flags)
+            want = q.moe_layer_fwd_given(good, H, I, idx[:, rest].contiguous(), w[:, rest].contiguous(), x, flags=flags)
+            assert torch.equal(y, want), (flags, c)
