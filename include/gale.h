@@ -486,7 +486,8 @@ int gale_mx_gemm(int32_t m, int32_t n, int32_t k, const uint8_t* a_codes, const 
  * x, residual: [rows] rows of dtype (GALE_F16, GALE_BF16, GALE_F32), x_stride and residual_stride elements
  * apart; weight: [cols] of weight_dtype, or NULL for ones; sum_out and y: rows back to back.
  * sum_out may be x or residual itself when that is stored back to back, and y the other of
- * the two when it also has dtype.  1 <= cols <= GALE_MAX_COLS,
+ * the two when it also has dtype; outputs that overlap an input or each other in any other way are
+ * refused.  1 <= cols <= GALE_MAX_COLS,
  * eps >= 0; rows may be 0. */
 int gale_add_rms_norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride, int32_t dtype,
                       int64_t rows, int32_t cols, const void* weight, int32_t weight_dtype, float eps, void* sum_out,

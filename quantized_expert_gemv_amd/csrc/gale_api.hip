@@ -846,6 +846,31 @@ static inline bool dtype3_ok(int d) { return dtype_ok(d) || d == GALE_BF16; }
 static inline int dsize3(int d) { return d == GALE_F32 ? 4 : 2; }
 static inline bool mx_fmt_ok(int f) { return f == GALE_MX_E2M1 || f == GALE_MX_E4M3; }
 
+// Memory of rows of `len` bytes, `stride` bytes apart; rows that lie back to back are one.
+struct RowBytes {
+  intptr_t at;
+  int64_t rows, stride, len;
+  RowBytes(const void* p, int64_t n, int64_t s, int64_t l) : at((intptr_t)p), rows(p ? n : 0), stride(s), len(l) {
+    if (rows > 0 && s == l) {
+      len *= rows;
+      rows = 1;
+    }
+    if (rows <= 1) stride = 1;      // not used, but divided by
+  }
+};
+
+// Whether two sets of rows share a byte.
+static bool meet(const RowBytes& a, const RowBytes& b) {
+  if (a.rows > b.rows) return meet(b, a);
+  for (int64_t i = 0; i < a.rows; ++i) {
+    const intptr_t lo = a.at + i * a.stride, hi = lo + a.len;
+    // the first row of b that ends behind lo
+    const int64_t r = b.at + b.len <= lo ? (lo - b.at - b.len) / b.stride + 1 : 0;
+    if (r < b.rows && b.at + r * b.stride < hi) return true;
+  }
+  return false;
+}
+
 extern "C" int gale_route_scored(const void* logits, int32_t logits_dtype, int64_t logits_stride, int32_t n_tok,
                                  int32_t n_experts, const float* bias, int32_t score, int32_t n_groups,
                                  int32_t keep_groups, int32_t group_rule, int32_t top_k, int32_t renormalize,
@@ -985,6 +1010,24 @@ extern "C" int gale_add_rms_norm(const void* x, int64_t x_stride, const void* re
       !aligned(y, dsize3(y_dtype)) || !aligned(codes, 16) || !aligned(scales, 4)) {
     set_error("%s: rows need their element's, codes 16-byte, scales 4-byte alignment", fn);
     return GALE_ERR_ALIGN;
+  }
+  // An output may take the place of x or the residual, row by row and element by element; any other overlap would be
+  // read after it is written.
+  const int ys = dsize3(y_dtype);
+  const RowBytes in[3] = {{x, rows, x_stride * es, (int64_t)cols * es},
+                          {residual, rows, residual_stride * es, (int64_t)cols * es},
+                          {weight, 1, 0, (int64_t)cols * dsize3(weight_dtype)}};
+  const RowBytes out[4] = {{sum_out, 1, 0, rows * cols * es}, {y, 1, 0, rows * cols * ys},
+                           {codes, 1, 0, codes ? rows * mx_code_row(mx_fmt, cols) : 0}, {scales, 1, 0, rows * mx_scale_row(cols)}};
+  for (int o = 0; o < 4; ++o) {
+    const bool in_place = o == 0 || (o == 1 && y_dtype == dtype);
+    for (int i = 0; i < 3; ++i)
+      if (meet(in[i], out[o]) && !(in_place && i < 2 && in[i].at == out[o].at && in[i].len == out[o].len)) {
+        set_error("%s: an output overlaps an input other than in place", fn);
+        return GALE_ERR_SHAPE;
+      }
+    for (int i = 0; i < o; ++i)
+      if (meet(out[i], out[o])) { set_error("%s: two outputs overlap", fn); return GALE_ERR_SHAPE; }
   }
   return hip_status(fn, launch_add_rms_norm(x, x_stride, residual, residual_stride, dtype, rows, cols, weight,
                                             weight_dtype, eps, sum_out, y, y_dtype, mx_fmt, codes, scales, stream));
