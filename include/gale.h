@@ -470,7 +470,7 @@ int gale_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t fmt,
  * fp32, one rounding to y_dtype, at every m.  A: m MX rows of k columns of a_fmt (activations); W:
  * n MX rows of k columns of GALE_MX_E2M1 (a weight matrix [out, in]).  y: [m] rows of n values of
  * y_dtype (GALE_F16, GALE_BF16, GALE_F32), y_stride elements apart; add: the same type, add_stride apart,
- * or NULL; add may be y itself with the same stride.  A NaN block makes every y that reads it
+ * or NULL; add may be y itself with the same stride, and y overlaps no input otherwise.  A NaN block makes every y that reads it
  * NaN.  m <= GALE_MAX_ROWS (0: nothing is enqueued), 1 <= n <= GALE_MAX_ROWS,
  * 1 <= k <= GALE_MX_MAX_COLS.  A row of y hangs on its own row of A only, and equal calls give
  * equal bits; the order of the fp32 sums depends on m, n and k. */

@@ -862,6 +862,12 @@ struct RowBytes {
 // Whether two sets of rows share a byte.
 static bool meet(const RowBytes& a, const RowBytes& b) {
   if (a.rows > b.rows) return meet(b, a);
+  if (a.rows > 1 && a.stride == b.stride) {
+    // row i of a and row i + k of b lie d + k stride apart: the smallest k from which on b's end lies behind a's start
+    const int64_t d = b.at - a.at, s = a.stride, t = -b.len - d;
+    const int64_t k = std::max((t >= 0 ? t / s : -((-t + s - 1) / s)) + 1, 1 - a.rows);
+    return k < b.rows && d + k * s < a.len;
+  }
   for (int64_t i = 0; i < a.rows; ++i) {
     const intptr_t lo = a.at + i * a.stride, hi = lo + a.len;
     // the first row of b that ends behind lo
@@ -976,7 +982,14 @@ extern "C" int gale_mx_gemm(int32_t m, int32_t n, int32_t k, const uint8_t* a_co
   if (st) return st;
   st = mx_pointers(fn, y, y_dtype, w_codes, w_scales);
   if (st) return st;
-  if (!aligned(add, dsize3(y_dtype))) { set_error("%s: misaligned add", fn); return GALE_ERR_ALIGN; }
+  const int64_t es = dsize3(y_dtype);
+  if (!aligned(add, es)) { set_error("%s: misaligned add", fn); return GALE_ERR_ALIGN; }
+  const RowBytes yb = {y, m, y_stride * es, n * es};
+  const RowBytes in[5] = {{a_codes, 1, 0, (int64_t)m * mx_code_row(a_fmt, k)}, {a_scales, 1, 0, (int64_t)m * mx_scale_row(k)},
+                          {w_codes, 1, 0, (int64_t)n * mx_code_row(GALE_MX_E2M1, k)}, {w_scales, 1, 0, (int64_t)n * mx_scale_row(k)},
+                          {add == y ? nullptr : add, m, add_stride * es, n * es}};
+  for (const RowBytes& i : in)
+    if (meet(i, yb)) { set_error("%s: y overlaps an input other than add in place", fn); return GALE_ERR_SHAPE; }
   return hip_status(fn, launch_mx_gemm(m, n, k, a_codes, a_scales, a_fmt, w_codes, w_scales, add, add_stride, y, y_dtype,
                                        y_stride, stream));
 }

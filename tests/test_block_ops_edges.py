@@ -1,5 +1,7 @@
 """Refusals of overlapping buffers by the operators around the routed layer, on the CPU: every bad call ends before any GPU
 work, and the good ones have no rows."""
+import random
+
 import pytest
 
 import quantized_expert_gemv_amd as q
@@ -45,3 +47,48 @@ def test_norm_refuses_overlaps(change):
 
 def test_norm_overlaps_of_no_rows_are_none():
     assert norm(rows=0, y=F, sum=F)[0] == 0
+
+
+M, N, K = 5, 64, 256
+
+
+def gemm(**change):
+    """gale_mx_gemm of fp16 results on buffers 1 MiB apart, y and add in rows of 200."""
+    a = {"m": M, "n": N, "k": K, "a": F, "as": F + (1 << 20), "a_fmt": 2, "w": F + (2 << 20), "ws": F + (3 << 20),
+         "add": F + (4 << 20), "add_stride": 200, "y": F + (5 << 20), "y_dtype": F16, "y_stride": 200}
+    a.update(change)
+    st = q.lib().gale_mx_gemm(*a.values(), None)
+    return st, q.lib().gale_last_error().decode()
+
+
+Y = F + (4 << 20)        # add's place
+
+
+@pytest.mark.parametrize("change", [
+    {"y": Y + 2}, {"y": Y - 2}, {"y": Y + 2 * (N - 1)}, {"y": Y - 2 * (N - 1)},          # the same stride, columns in common
+    {"y": Y + 2 * 400 + 2 * 63}, {"y": Y + 2 * 200 - 2}, {"y": Y + 2 * 800}, {"y": Y - 2 * 800 + 126},
+    {"y": Y, "y_stride": 201}, {"y": Y + 2 * 64, "y_stride": 250}, {"y": Y + 2 * 130, "y_stride": 64},   # other strides
+    {"y": Y - 2 * 64, "y_stride": 264}, {"add": None, "y": F}, {"y": F + M * 256 - 2}, {"y": F + (1 << 20) + 16},
+    {"y": F + (2 << 20) + N * 128 - 2}, {"y": F + (3 << 20) - 2 * 200 - 2}, {"m": 1, "y": Y + 126}, {"m": 1, "y": Y - 126},
+])
+def test_gemm_refuses_overlaps(change):
+    st, error = gemm(**change)
+    assert st == SHAPE and ("overlaps" in error or "in place" in error), change
+
+
+def test_overlaps_are_found_as_element_by_element():
+    """Random rows of add and y, of one stride or two, against the sets of their elements: where these meet, the call is
+    refused."""
+    rng, met = random.Random(5), 0
+    for _ in range(4000):
+        n, sx, sy = rng.randint(1, 6), rng.randint(6, 20), rng.randint(6, 20)
+        sy = sx if rng.random() < 0.5 else sy
+        rows, at = rng.randint(1, 5), rng.randint(-60, 60)
+        x = {r * sx + c for r in range(rows) for c in range(n)}
+        y = {at + r * sy + c for r in range(rows) for c in range(n)}
+        if at == 0 or not x & y:
+            continue
+        met += 1
+        st, error = gemm(m=rows, n=n, y=Y + 2 * at, add_stride=sx, y_stride=sy)
+        assert st == SHAPE and "overlaps" in error, (rows, n, sx, sy, at)
+    assert met > 500

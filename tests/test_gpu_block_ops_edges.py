@@ -173,6 +173,39 @@ def test_gemm_of_more_rows_than_a_launch_takes(q, fmt):
     assert ((y.double() - want).abs() <= t * want.abs() + MFMA * size * (1 + t) + subnormal(torch.float16)).all()
 
 
+def test_gemm_of_interleaved_rows(q):
+    """add and y in one buffer whose rows do not meet, of one stride or two: nothing is refused, and nothing else written."""
+    rng = np.random.default_rng(3)
+    done = 0
+    while done < 60:
+        m, n = int(rng.integers(1, 50)), int(rng.integers(1, 40))
+        sx, sy = (int(v) for v in rng.integers(n, 3 * n + 8, 2))
+        sy = sx if rng.random() < 0.6 else sy
+        at = int(rng.integers(0, 4 * n + 8))
+        x = np.arange(m)[:, None] * sx + np.arange(n)
+        y = at + np.arange(m)[:, None] * sy + np.arange(n)
+        if np.intersect1d(x, y).size:
+            continue
+        done += 1
+        buf = rand((50 * 130 + 400,), done, torch.float16)
+        a, w = operand(q, m, 200, 1 + done % 2, 1), operand(q, n, 200, 1, 2)
+        add, out = buf.as_strided((m, n), (sx, 1)), buf.as_strided((m, n), (sy, 1), at)
+        want, kept = q.mx_gemm(a, w, add=add.clone()), buf.clone()
+        q.mx_gemm(a, w, add=add, out=out)
+        kept.as_strided((m, n), (sy, 1), at).copy_(want)
+        assert torch.equal(buf, kept), (m, n, sx, sy, at)
+
+
+def test_norm_of_rows_around_its_outputs(q):
+    """Outputs in the gap between the rows of x."""
+    buf = rand((2, 4000), 1, torch.float16)
+    x, flat = buf[:, :300], buf.view(-1)
+    want = q.add_rms_norm(x.clone(), None, residual=x.clone(), mx_fmt=2)
+    y, s = flat[300:900].view(2, 300), flat[1000:1600].view(2, 300)
+    got = q.add_rms_norm(x, None, residual=x, out=y, sum_out=s, mx_fmt=2)
+    assert torch.equal(y, want[0]) and torch.equal(s, want[1]) and torch.equal(got[2].codes, want[2].codes)
+
+
 # ---- norm --------------------------------------------------------------------------------------------------------
 def check_norm(q, x, w, fmt, eps=0.0):
     """y and, with fmt, the codes of the exact numbers; what fp32 does not hold is infinite, and its block NaN."""
