@@ -409,9 +409,7 @@ hipError_t launch_route_scored(const void* logits, int dtype, int64_t stride, in
   int lg = 0;
   while ((1 << lg) < G) ++lg;
   ScoredParams p;
-  p.logits = logits;
   p.stride = stride;
-  p.n_tok = n_tok;
   p.E = E;
   p.k = k;
   p.bias = bias;
@@ -423,11 +421,18 @@ hipError_t launch_route_scored(const void* logits, int dtype, int64_t stride, in
   p.log2L = 6 - lg;
   p.renorm = renorm;
   p.scale = scale;
-  p.idx = idx;
-  p.w = w;
-  if (dtype == GALE_F16) return launch_scored_t<F16>(p, s);
-  if (dtype == GALE_BF16) return launch_scored_t<BF16>(p, s);
-  return launch_scored_t<F32>(p, s);
+  // a grid has fewer than 2^32 threads, 64 for a token: four million tokens per launch
+  for (int64_t t = 0; t < n_tok; t += 1 << 22) {
+    p.n_tok = (int)std::min<int64_t>(n_tok - t, 1 << 22);
+    p.logits = (const char*)logits + t * stride * (dtype == GALE_F32 ? 4 : 2);
+    p.idx = idx + t * k;
+    p.w = w + t * k;
+    const hipError_t e = dtype == GALE_F16    ? launch_scored_t<F16>(p, s)
+                         : dtype == GALE_BF16 ? launch_scored_t<BF16>(p, s)
+                                              : launch_scored_t<F32>(p, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace gale

@@ -246,6 +246,19 @@ def test_norm_of_extreme_rows_and_weights(q, fmt, dtype, scale, weight, cols):
     check_norm(q, x, w, fmt)
 
 
+# ---- routing -----------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+def test_route_of_more_tokens_than_a_grid_takes(q, dtype):
+    """2^26 tokens and a few, in several launches: the tokens at their ends are those of a small call."""
+    T = (1 << 26) + 11
+    lg = torch.randint(-8, 8, (T, 3), dtype=torch.int8, device=DEV, generator=torch.Generator(DEV).manual_seed(1)).to(dtype)
+    idx, w = q.route_scored(lg, 2, score="sigmoid")
+    pick = torch.tensor([0, 1, (1 << 22) - 1, 1 << 22, (1 << 25) + 3, (1 << 26) - 1, 1 << 26, T - 1], device=DEV)
+    want_i, want_w = q.route_scored(lg[pick], 2, score="sigmoid")
+    assert torch.equal(idx[pick], want_i) and torch.equal(w[pick], want_w)
+    assert (idx >= 0).all() and (w.sum(1) - 1).abs().max() <= 2.0 ** -22
+
+
 # ---- the routed layer with slots that have no expert ------------------------------------------------------------
 @pytest.fixture(scope="module")
 def two_tables(q):
