@@ -488,7 +488,7 @@ int gale_mx_gemm(int32_t m, int32_t n, int32_t k, const uint8_t* a_codes, const 
  * sum_out may be x or residual itself when that is stored back to back, and y the other of
  * the two when it also has dtype; outputs that overlap an input or each other in any other way are
  * refused.  1 <= cols <= GALE_MAX_COLS,
- * eps >= 0; rows may be 0. */
+ * eps >= 0 and finite; rows may be 0. */
 int gale_add_rms_norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride, int32_t dtype,
                       int64_t rows, int32_t cols, const void* weight, int32_t weight_dtype, float eps, void* sum_out,
                       void* y, int32_t y_dtype, int32_t mx_fmt, uint8_t* codes, uint8_t* scales, hipStream_t stream);

@@ -1010,7 +1010,7 @@ extern "C" int gale_add_rms_norm(const void* x, int64_t x_stride, const void* re
               (long long)residual_stride);
     return GALE_ERR_SHAPE;
   }
-  if (!(eps >= 0.f)) { set_error("%s: eps must not be negative", fn); return GALE_ERR_SHAPE; }
+  if (!(eps >= 0.f && eps < INFINITY)) { set_error("%s: eps must be finite and not negative", fn); return GALE_ERR_SHAPE; }
   if ((codes == nullptr) != (scales == nullptr)) { set_error("%s: codes and scales go together", fn); return GALE_ERR_NULL; }
   if (rows == 0) return GALE_OK;
   if (!x || (!y && !codes)) { set_error("%s: NULL pointer", fn); return GALE_ERR_NULL; }

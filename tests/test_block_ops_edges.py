@@ -92,3 +92,8 @@ def test_overlaps_are_found_as_element_by_element():
         st, error = gemm(m=rows, n=n, y=Y + 2 * at, add_stride=sx, y_stride=sy)
         assert st == SHAPE and "overlaps" in error, (rows, n, sx, sy, at)
     assert met > 500
+
+
+def test_norm_refuses_an_infinite_eps():
+    st, error = norm(eps=float("inf"))
+    assert st == SHAPE and "eps" in error

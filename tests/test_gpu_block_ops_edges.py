@@ -317,3 +317,24 @@ def test_given_empty_slots_are_as_if_absent(q, two_tables, T):
             y = q.moe_layer_fwd_given(good, H, I, holed, w, x, flags=flags)
             want = q.moe_layer_fwd_given(good, H, I, idx[:, rest].contiguous(), w[:, rest].contiguous(), x, flags=flags)
             assert torch.equal(y, want), (flags, c)
+
+
+@pytest.mark.parametrize("T", [1, 40, 300])
+def test_masked_tokens_through_router_and_layer(q, two_tables, T):
+    """Tokens whose logits leave nothing, or fewer experts than slots, go from the router into the layer: the first are
+    zero, and the others' empty slots add nothing."""
+    H, I, E, good, bad = two_tables
+    lg = rand((T, E), 7)
+    lg[:, 0] = -math.inf                           # expert 0, whose numbers are NaN in `bad`, is masked
+    lg[0] = -math.inf
+    if T > 1:
+        lg[1, 2:] = -math.inf                      # one expert
+        lg[2, 5:] = math.nan                       # four
+    idx, w = q.route_scored(lg, 6, score="sigmoid", n_groups=2, keep_groups=2)
+    assert (idx[0] == -1).all()
+    x = rand((T, H), 8, torch.float16)
+    y = q.moe_layer_fwd_given(good, H, I, idx, w, x)
+    assert (y[0] == 0).all() and y.isfinite().all()
+    assert torch.equal(q.moe_layer_fwd_given(bad, H, I, idx, w, x), y)
+    if T > 1:
+        assert (idx[1] == torch.tensor([1, -1, -1, -1, -1, -1], device=DEV)).all() and (y[1] != 0).any()
