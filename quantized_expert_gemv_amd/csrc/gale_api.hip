@@ -862,6 +862,7 @@ struct RowBytes {
 // Whether two sets of rows share a byte.
 static bool meet(const RowBytes& a, const RowBytes& b) {
   if (a.rows > b.rows) return meet(b, a);
+  if (a.rows == 0 || a.at + (a.rows - 1) * a.stride + a.len <= b.at || b.at + (b.rows - 1) * b.stride + b.len <= a.at) return false;
   if (a.rows > 1 && a.stride == b.stride) {
     // row i of a and row i + k of b lie d + k stride apart: the smallest k from which on b's end lies behind a's start
     const int64_t d = b.at - a.at, s = a.stride, t = -b.len - d;

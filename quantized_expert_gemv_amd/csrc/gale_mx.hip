@@ -51,23 +51,29 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(const typename T::bits
   for (int k = 0; k < U; ++k) {
     if (blockIdx.x * (256u * U) + 256u * k + threadIdx.x >= n_units) return;
     if constexpr (SWIGLU) {
-      float g[8], least = INFINITY;
+      float g[8], a[8], least = INFINITY;
       uint32_t near = 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         g[j] = v[k][j];
-        const float a = silu(g[j]);
-        v[k][j] = a * up[k][j];
-        least = fminf(least, fminf(fabsf(a), fabsf(v[k][j])));
+        a[j] = silu(g[j]);
+        v[k][j] = a[j] * up[k][j];
+        least = fminf(least, fminf(fabsf(a[j]), fabsf(v[k][j])));
         // off by less than 16 of its last place; borders between elements and between scales end in 19 zero bits
         near |= ((__float_as_uint(v[k][j]) + 16u) & 0x7FFFFu) <= 32u && v[k][j] != 0.f ? 1u << j : 0u;
+      }
+      if (least < 0x1p-120f) {         // zeros do not count
+        least = INFINITY;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          least = fminf(least, fminf(fabsf(g[j]), fabsf(up[k][j])) == 0.f ? 1.f : fminf(fabsf(a[j]), fabsf(v[k][j])));
       }
       if (least < 0x1p-120f) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           // below g = -200 no up value brings the product back; a product rounded to zero lies far below half of the
           // smallest element, 2^-137
-          const bool lost = fabsf(silu(g[j])) < 0x1p-120f && fabsf(up[k][j]) > 1.f && g[j] != 0.f && g[j] > -200.f;
+          const bool lost = fabsf(a[j]) < 0x1p-120f && g[j] > -200.f && g[j] != 0.f && fabsf(up[k][j]) > 1.f;
           near |= lost || (v[k][j] != 0.f && fabsf(v[k][j]) < 0x1p-126f) ? 1u << j : 0u;
         }
       }

@@ -106,6 +106,8 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(const NormParams p) 
   inv = fma(inv * 0.5, fma(-ms * inv, inv, 1.0), inv);
   if (!ordinary) inv = 1.0 / sqrt(ms);
   const float ih = (float)inv, il = (float)(inv - (double)ih);
+  const float tiny = 0x1p-100f * fmaxf(1.f, 1.f / ih);    // |p| from here on has p and p / rms above 2^-100
+  const bool by_32 = ordinary || (sq == 0.0 && p.eps > 0.f);      // also rows of zeros
 #pragma unroll
   for (int k = 0; k < U; ++k) {
     const int u = (int)(threadIdx.x + k * blockDim.x), c = 8 * u;
@@ -117,26 +119,31 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(const NormParams p) 
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[i] = 1.0f;
     }
-    float y[8], least = INFINITY, most = 0.f;
+    float y[8];
     uint32_t low = 0xFFFFFFFFu;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float pr = v[k][i] * w[i], q = fmaf(v[k][i], w[i], -pr);
-      y[i] = fmaf(pr, ih, fmaf(pr, il, q * ih));
-      least = fminf(least, fminf(fabsf(pr), fabsf(y[i])));
-      most = fmaxf(most, fabsf(pr));
-      if constexpr (FMT != 0) low = min(low, __float_as_uint(y[i]) & 0x7FFFFu);
-    }
-    // Products and results near the ends of 32 bits, where p + q or t are not whole, go by 64.  A zero factor needs neither: its
-    // product is y, with its sign.
-    bool far = !ordinary;
-    if (least < 0x1p-100f || most > 0x1p126f) {
+    bool far = !by_32;
+    if (by_32) {
+      float least = INFINITY, most = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float pr = v[k][i] * w[i];
-        const bool zero = v[k][i] == 0.f || w[i] == 0.f;
-        far = far || fabsf(pr) > 0x1p126f || (fminf(fabsf(pr), fabsf(y[i])) < 0x1p-100f && !zero);
-        y[i] = zero ? pr : y[i];
+        const float pr = v[k][i] * w[i], q = fmaf(v[k][i], w[i], -pr);
+        y[i] = fmaf(pr, ih, fmaf(pr, il, q * ih));
+        least = fminf(least, fabsf(pr));
+        most = fmaxf(most, fabsf(pr));
+        if constexpr (FMT != 0) low = min(low, __float_as_uint(y[i]) & 0x7FFFFu);
+      }
+      // Products and results near the ends of 32 bits, where p + q or t are not whole, go by 64.  Those of a zero factor
+      // need not: y is the product, with its sign.
+      if (least < tiny || most > 0x1p126f) {
+        least = INFINITY;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float pr = v[k][i] * w[i];
+          const bool zero = fminf(fabsf(v[k][i]), fabsf(w[i])) == 0.f;
+          least = fminf(least, zero ? 1.f : fabsf(pr));
+          y[i] = zero ? pr : y[i];
+        }
+        far = least < tiny || most > 0x1p126f;
       }
     }
     uint32_t odd = 0;                 // two bits per column: the step of its rounding to odd, and one
@@ -157,7 +164,7 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(const NormParams p) 
       if (far) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = __uint_as_float(__float_as_uint(y[i]) + ((odd >> (2 * i)) & 3u) - 1u);
-      } else if (low == 0) {
+      } else if (low == 0 && ordinary) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float pr = v[k][i] * w[i], q = fmaf(v[k][i], w[i], -pr);
