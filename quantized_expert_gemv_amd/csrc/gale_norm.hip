@@ -3,14 +3,15 @@
 // s = x + r (rounded to the rows' type), y = s / sqrt(mean(s^2) + eps) * w.  One pass over memory: a workgroup
 // holds its row in registers between the sum of squares and the outputs.
 //
-// The 8- or 4-bit form of y is that of the exact number (to a few 2^-30): with plain 32-bit arithmetic a few elements in a million
-// took the neighbouring code and two blocks in a million the other of two scales, as the last bit of y fell.  The squares of eight
-// columns are added in 32 bits and the eights in 64, 1 / rms is held as two floats ih + il, and s w as p + q: y = p ih + t,
+// The 8- or 4-bit form of y is that of the exact number (to a few 2^-45): with plain 32-bit arithmetic a few elements in a million
+// took the neighbouring code and two blocks in a million the other of two scales, as the last bit of y fell.  The squares are
+// added in 64 bits (in 32 by eights, one element in ten million was on the wrong side of a border, at the same time: 112 us
+// for 16,384 x 4,096 bf16 with an 8-bit output), 1 / rms is held as two floats ih + il, and s w as p + q: y = p ih + t,
 // t = p il + q ih, is rounded once.  A second rounding, to the element, differs from that of the exact number only where y
 // fell on a border: halfway between two elements, or the largest number at a scale.  All borders end in 19 zero bits, which
-// one element in 2^19 does: for those the rest p ih + t - y pushes y off the border, to the side it came from.  (All in 64
-// bits the arithmetic, not HBM, bounds the kernel: 123 us for 16,384 x 4,096 bf16 with an 8-bit output.)  Rows whose squares or rms 32
-// bits do not hold well are computed in 64, and so are eights of columns with a product or result near the ends of 32 bits.
+// one element in 2^19 does: for those the rest p ih + t - y pushes y off the border, to the side it came from.  (With y in 64
+// bits too the arithmetic, not HBM, bounds the kernel: 123 us.)  Rows whose sum or rms is near the ends of 32 bits are computed in
+// 64, and so are eights of columns with such a product or result.
 #include "gale_mx.h"
 #include "gale_lanes.h"
 
@@ -83,23 +84,12 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(const NormParams p) 
   double sq = 0.0;
 #pragma unroll
   for (int k = 0; k < U; ++k) {
-    float e = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e = fmaf(v[k][i], v[k][i], e);
-    sq += (double)e;
+    for (int i = 0; i < 8; ++i) sq = fma((double)v[k][i], (double)v[k][i], sq);
   }
   sq = block_sum(sq, s_wave);
-  // the same for the whole workgroup: squares near the ends of 32 bits, or rows without a finite sum
+  // the same for the whole workgroup: p, ih and il are far from the ends of 32 bits, or rows without a finite sum
   const bool ordinary = sq > 1e-20 && sq < 1e35;
-  if (!ordinary) {
-    __syncthreads();
-    sq = 0.0;
-#pragma unroll
-    for (int k = 0; k < U; ++k)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sq = fma((double)v[k][i], (double)v[k][i], sq);
-    sq = block_sum(sq, s_wave);
-  }
   const double ms = sq / p.cols + (double)p.eps;
   // 1 / sqrt(ms): the hardware's estimate and one Newton step, or as written for rows out of the ordinary
   double inv = __builtin_amdgcn_rsq(ms);
@@ -150,7 +140,9 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(const NormParams p) 
     if (far) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const double d = (double)v[k][i] * inv * (double)w[i];
+        float x = v[k][i];
+        asm volatile("" : "+v"(x));            // not the 64-bit numbers of the squares: they would stay in registers
+        const double d = (double)x * inv * (double)w[i];
         y[i] = (float)d;
         if constexpr (FMT != 0) odd |= (uint32_t)(odd_step(d, y[i]) + 1) << (2 * i);
         __builtin_amdgcn_sched_barrier(0);     // one after the other: registers for eight at once would cost occupancy

@@ -246,6 +246,33 @@ def test_norm_of_extreme_rows_and_weights(q, fmt, dtype, scale, weight, cols):
     check_norm(q, x, w, fmt)
 
 
+@pytest.mark.parametrize("fmt", [1, 2])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("cols", [4096, 16384])
+def test_norm_codes_next_to_borders(q, fmt, dtype, cols):
+    """Weights that put every result within 2^-22 of a border between two elements, in rows of one large number and seven small
+    ones each eight, whose squares a sum in 32 bits would lose."""
+    g = torch.Generator().manual_seed(cols)
+    x = torch.rand(cols, generator=g, dtype=torch.float64) * 0.2 + 0.9
+    x[::8] = x[::8] * 1.5
+    small = torch.ones(cols, dtype=torch.bool)
+    small[::8] = False
+    x = (torch.where(small, x * 2.0 ** -12.4, x) * (1 - 2 * torch.randint(0, 2, (cols,), generator=g))).to(dtype)
+    rms = math.sqrt(float((x.double() ** 2).mean()) + 1e-6)
+    # halfway between elements of the two octaves below the largest, which stays clear of borders
+    table = torch.from_numpy(O.TABLE[fmt])
+    mid = ((table[1:] + table[:-1]) / 2)[-17 if fmt == 2 else -5:-1]
+    y = mid[torch.randint(0, len(mid), (cols,), generator=g)]
+    y[::32] = float(table[-1]) * 0.98
+    w = (y * rms / x.double()).float()
+    w = w * (1 + torch.randint(-2, 3, (cols,), generator=g) * 2.0 ** -23)
+    _, _, mx = q.add_rms_norm(x[None].to(DEV), w.float().to(DEV), eps=1e-6, mx_fmt=fmt)
+    exact = O.rms_norm(x[None].double().numpy(), w.double().numpy(), float(np.float32(1e-6)))
+    want_c, want_s = O.mx_quantize(exact, fmt)
+    codes, scales = elements(mx)
+    assert np.array_equal(scales, want_s) and np.array_equal(codes, want_c)
+
+
 # ---- routing -----------------------------------------------------------------------------------------------------
 @pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
 def test_route_of_more_tokens_than_a_grid_takes(q, dtype):
