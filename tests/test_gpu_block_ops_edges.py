@@ -68,6 +68,28 @@ def test_swiglu_of_subnormal_products(q, fmt, dtype):
     assert np.array_equal(scales, want_s) and np.array_equal(codes, want_c)
 
 
+@pytest.mark.parametrize("fmt", [1, 2])
+def test_swiglu_codes_next_to_borders(q, fmt):
+    """Up values that put every product within 2^-22 of a border between two elements, for gates from -200 to 200."""
+    g = torch.Generator().manual_seed(9)
+    rows, cols = 48, 4096
+    gate = torch.randn(rows, cols, generator=g) * torch.exp2(torch.randint(-6, 7, (rows, 1), generator=g).float())
+    gate[::3] = 400 * torch.rand(rows // 3, cols, generator=g) - 200
+    gate[1::3, ::5] = -78 - 12 * torch.rand(rows // 3, len(range(0, cols, 5)), generator=g)
+    gate = torch.where(gate.abs() < 2.0 ** -20, torch.ones(()), gate)
+    silu = gate.double() / (1 + torch.exp(-gate.double()))
+    # halfway between elements of the two octaves below the largest, which stays clear of borders
+    table = torch.from_numpy(O.TABLE[fmt])
+    mid = ((table[1:] + table[:-1]) / 2)[-17 if fmt == 2 else -5:-1]
+    y = mid[torch.randint(0, len(mid), (rows, cols), generator=g)]
+    y[:, ::32] = float(table[-1]) * 0.98
+    up = (y / silu).clamp(-3e38, 3e38).float() * (1 + torch.randint(-2, 3, (rows, cols), generator=g) * 2.0 ** -23)
+    x = torch.cat((gate, up.float()), 1)
+    codes, scales = elements(q.mx_swiglu_quantize(x.to(DEV), fmt))
+    want_c, want_s = O.mx_quantize(O.swiglu(x.double().numpy()), fmt)
+    assert np.array_equal(scales, want_s) and np.array_equal(codes, want_c)
+
+
 def test_swiglu_repeats_itself(q):
     x = rand((2048, 4096), 21, torch.float16, 3.0)
     a = q.mx_swiglu_quantize(x, 2)
