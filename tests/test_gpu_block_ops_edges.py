@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from oracle import block_oracle as O
-from tests.test_gpu_block_ops import (DEV, DTS, MFMA, WORK, elements, f64, half_step, operand, q, rand,  # noqa: F401
+from tests.test_gpu_block_ops import (DEV, DTS, MFMA, WORK, check_route, elements, f64, half_step, operand, q, rand,  # noqa: F401
                                       subnormal)
 
 pytestmark = pytest.mark.gpu
@@ -306,6 +306,21 @@ def test_route_of_more_tokens_than_a_grid_takes(q, dtype):
     want_i, want_w = q.route_scored(lg[pick], 2, score="sigmoid")
     assert torch.equal(idx[pick], want_i) and torch.equal(w[pick], want_w)
     assert (idx >= 0).all() and (w.sum(1) - 1).abs().max() <= 2.0 ** -22
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("spread", [2.0 ** -14, 2.0 ** -17, 2.0 ** -18, 2.0 ** -19, 2.0 ** -21, 2.0 ** -24])
+def test_route_of_sums_within_the_margins(q, score, spread):
+    """Biases that bring all sums within `spread` of each other, around the margins that 32 bits are trusted with: the choice is
+    that of 64 bits, with groups and without."""
+    g = torch.Generator().manual_seed(11)
+    for E, G, keep in ((256, 1, 1), (256, 8, 3), (96, 4, 2)):
+        for _ in range(6):
+            lg = 3 * torch.randn(1, E, generator=g)
+            s = torch.softmax(lg.double(), 1) if score == "softmax" else torch.sigmoid(lg.double())
+            bias = (1 - s[0] + spread * torch.randn(E, generator=g).double()).float().to(DEV)
+            for rule in ("max", "top2"):
+                check_route(q, lg.to(DEV), 8, score=score, bias=bias, n_groups=G, keep_groups=keep, group_score=rule)
 
 
 # ---- the routed layer with slots that have no expert ------------------------------------------------------------
