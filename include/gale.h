@@ -461,7 +461,7 @@ int gale_mx_quantize(const void* x, int32_t x_dtype, int64_t x_stride, int64_t r
 int gale_mx_swiglu_quantize(const void* x, int32_t x_dtype, int64_t x_stride, int64_t rows, int32_t cols,
                             int32_t fmt, uint8_t* codes, uint8_t* scales, hipStream_t stream);
 
-/* MX -> the numbers, rounded once to y_dtype (exact in fp32).  y: [rows] rows of cols values,
+/* MX -> the numbers, rounded once to y_dtype (exact in fp32 up to its largest number).  y: [rows] rows of cols values,
  * y_stride elements apart. */
 int gale_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t fmt, int64_t rows, int32_t cols,
                        void* y, int32_t y_dtype, int64_t y_stride, hipStream_t stream);

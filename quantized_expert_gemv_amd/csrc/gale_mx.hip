@@ -12,7 +12,7 @@ namespace gale {
 // x into a relative one.  With the library's exponential and division the arithmetic bounds the kernel
 // (4096 x 2048 fp16 into 8 bits: 12.2 us against 10.2 with two units per thread).  The codes are made those of 64-bit arithmetic: where the result
 // lies so near a border of the rounding that its error matters, one element in 16,000, it is computed in 64 bits
-// (together 10.7 us, one unit per thread).  So are the results that 32 bits hold with fewer bits: subnormal products, and those
+// (together 11.1 us, one unit per thread).  So are the results that 32 bits hold with fewer bits: subnormal products, and those
 // of a silu below 2^-120 (g under -87 or next to 0) and an up value above 1, which may bring it back among the normal numbers.
 __device__ __forceinline__ float silu(float g) {
   const float a = fabsf(g), kHi = 0.72134752044448170f, kLo = 9.62981496e-9f;   // log2(e) / 2 = kHi + kLo
