@@ -443,7 +443,8 @@ int gale_route_scored(const void* logits, int32_t logits_dtype, int64_t logits_s
  * Rows are stored back to back, padded to whole groups of GALE_MX_GROUP = 128 columns: codes
  * [rows][gale_mx_code_bytes(fmt, cols)], scales [rows][gale_mx_scale_bytes(cols)].  Codes and scales
  * behind column cols are zero bytes: every writer below stores them, and gale_mx_gemm relies on it.
- * codes are 16-byte, scales 4-byte aligned. */
+ * codes are 16-byte, scales 4-byte aligned.  No output of a call below shares memory with an input or
+ * another output but where its text allows it. */
 size_t gale_mx_code_bytes(int32_t fmt, int32_t cols);    /* bytes of a row of codes (0: bad arguments) */
 size_t gale_mx_scale_bytes(int32_t cols);                /* bytes of a row of scales */
 

@@ -904,6 +904,13 @@ extern "C" int gale_route_scored(const void* logits, int32_t logits_dtype, int64
     set_error("%s: misaligned pointer", fn);
     return GALE_ERR_ALIGN;
   }
+  const int64_t es = dsize3(logits_dtype), slots = 4 * (int64_t)n_tok * top_k;
+  const RowBytes in[2] = {{logits, n_tok, logits_stride * es, n_experts * es}, {bias, 1, 0, 4 * (int64_t)n_experts}};
+  const RowBytes idx = {topk_idx, 1, 0, slots}, w = {topk_w, 1, 0, slots};
+  if (meet(in[0], idx) || meet(in[0], w) || meet(in[1], idx) || meet(in[1], w) || meet(idx, w)) {
+    set_error("%s: an output overlaps another buffer", fn);
+    return GALE_ERR_SHAPE;
+  }
   return hip_status(fn, launch_route_scored(logits, logits_dtype, logits_stride, n_tok, n_experts, bias, score, n_groups,
                                             keep_groups, group_rule, top_k, renormalize ? 1 : 0, scale, topk_idx, topk_w,
                                             stream));
@@ -938,11 +945,23 @@ static int mx_pointers(const char* fn, const void* rows, int32_t dtype, const ui
   return GALE_OK;
 }
 
+// Rows of numbers and the MX numbers made of them, or the other way round, must not share memory.
+static int mx_apart(const char* fn, const void* rows, int32_t dtype, int64_t stride, int64_t n, int64_t len, const uint8_t* codes,
+                    const uint8_t* scales, int32_t fmt, int32_t cols) {
+  const int64_t es = dsize3(dtype);
+  const RowBytes x = {rows, n, stride * es, len * es}, c = {codes, 1, 0, n * mx_code_row(fmt, cols)},
+                 s = {scales, 1, 0, n * mx_scale_row(cols)};
+  if (meet(x, c) || meet(x, s) || meet(c, s)) { set_error("%s: an output overlaps another buffer", fn); return GALE_ERR_SHAPE; }
+  return GALE_OK;
+}
+
 static int mx_quantize(const char* fn, const void* x, int32_t x_dtype, int64_t x_stride, int64_t rows, int32_t cols,
                        int32_t fmt, bool swiglu, uint8_t* codes, uint8_t* scales, hipStream_t stream) {
   int st = mx_check(fn, fmt, x_dtype, x_stride, (swiglu ? 2 : 1) * (int64_t)cols, rows, cols);
   if (st || rows == 0) return st;
   st = mx_pointers(fn, x, x_dtype, codes, scales);
+  if (st) return st;
+  st = mx_apart(fn, x, x_dtype, x_stride, rows, (swiglu ? 2 : 1) * (int64_t)cols, codes, scales, fmt, cols);
   if (st) return st;
   return hip_status(fn, launch_mx_quantize(x, x_dtype, x_stride, rows, cols, fmt, swiglu, codes, scales, stream));
 }
@@ -963,6 +982,8 @@ extern "C" int gale_mx_dequantize(const uint8_t* codes, const uint8_t* scales, i
   int st = mx_check(fn, fmt, y_dtype, y_stride, cols, rows, cols);
   if (st || rows == 0) return st;
   st = mx_pointers(fn, y, y_dtype, codes, scales);
+  if (st) return st;
+  st = mx_apart(fn, y, y_dtype, y_stride, rows, cols, codes, scales, fmt, cols);
   if (st) return st;
   return hip_status(fn, launch_mx_dequantize(codes, scales, fmt, rows, cols, y, y_dtype, y_stride, stream));
 }

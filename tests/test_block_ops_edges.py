@@ -97,3 +97,25 @@ def test_overlaps_are_found_as_element_by_element():
 def test_norm_refuses_an_infinite_eps():
     st, error = norm(eps=float("inf"))
     assert st == SHAPE and "eps" in error
+
+
+@pytest.mark.parametrize("name,two", [("gale_mx_quantize", 1), ("gale_mx_swiglu_quantize", 2)])
+@pytest.mark.parametrize("codes,scales", [(F, F + (2 << 20)), (F + 16, F + (2 << 20)), (F - 3 * 64 - 16, F + (2 << 20)),
+                                          (F + (2 << 20), F + 8), (F + (2 << 20), F + (2 << 20) + 4), (F + (2 << 20), F - 12)])
+def test_quantisers_refuse_overlaps(name, two, codes, scales):
+    st = getattr(q.lib(), name)(F, F16, 300 * two, 4, 128, 1, codes, scales, None)
+    assert st == SHAPE and "overlaps" in q.lib().gale_last_error().decode()
+
+
+@pytest.mark.parametrize("y", [F, F + 3 * 64, F - 3 * 600 - 254, F + (1 << 20), F + (1 << 20) + 12])
+def test_dequantiser_refuses_overlaps(y):
+    st = q.lib().gale_mx_dequantize(F, F + (1 << 20), 1, 4, 128, y, F16, 300, None)
+    assert st == SHAPE and "overlaps" in q.lib().gale_last_error().decode()
+
+
+@pytest.mark.parametrize("bias,idx,w", [
+    (None, F, F + (2 << 20)), (None, F + (1 << 20), F + 3 * 1200 + 1020), (None, F + (1 << 20), F + (1 << 20) + 124),
+    (F + (3 << 20), F + (3 << 20) + 1020, F + (1 << 20)), (F + (3 << 20), F + (1 << 20), F + (3 << 20) - 124)])
+def test_router_refuses_overlaps(bias, idx, w):
+    st = q.lib().gale_route_scored(F, F32, 300, 4, 256, bias, 2, 8, 4, 2, 8, 1, 1.0, idx, w, None)
+    assert st == SHAPE and "overlaps" in q.lib().gale_last_error().decode()

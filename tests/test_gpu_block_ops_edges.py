@@ -232,7 +232,7 @@ def test_norm_of_rows_around_its_outputs(q):
 def check_norm(q, x, w, fmt, eps=0.0):
     """y and, with fmt, the codes of the exact numbers; what fp32 does not hold is infinite, and its block NaN."""
     y, _, mx = q.add_rms_norm(x, w, eps=eps, out_dtype=torch.float32, mx_fmt=fmt)
-    exact = O.rms_norm(f64(x), f64(w), eps)
+    exact = O.rms_norm(f64(x), f64(w), float(np.float32(eps)))
     with np.errstate(over="ignore"):
         near = exact.astype(np.float32).astype(np.float64)
     held = np.isfinite(near)
@@ -266,6 +266,17 @@ def test_norm_of_extreme_rows_and_weights(q, fmt, dtype, scale, weight, cols):
     x, w = rand((40, cols), 1, dtype, scale), (rand((cols,), 2).double() * weight).clamp(-3e38, 3e38).float()
     x[:, 5], w[7] = 0, 0
     check_norm(q, x, w, fmt)
+
+
+@pytest.mark.parametrize("fmt", [None, 1, 2])
+@pytest.mark.parametrize("dtype", DTS)
+@pytest.mark.parametrize("rows", [3, 600])
+def test_norm_of_weights_extreme_in_places(q, fmt, dtype, rows):
+    """Eights of columns that go by 64 bits next to ordinary ones of the same blocks."""
+    x, w = rand((rows, 1000), 1, dtype), rand((1000,), 2)
+    for first, by in ((8, 1e-37), (40, 1e37), (203, 0.0), (320, 1e-30), (701, 1e-33)):
+        w[first:first + 8] *= by
+    check_norm(q, x, w, fmt, eps=1e-6)
 
 
 @pytest.mark.parametrize("fmt", [1, 2])
