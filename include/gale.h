@@ -494,6 +494,107 @@ int gale_add_rms_norm(const void* x, int64_t x_stride, const void* residual, int
                       int64_t rows, int32_t cols, const void* weight, int32_t weight_dtype, float eps, void* sum_out,
                       void* y, int32_t y_dtype, int32_t mx_fmt, uint8_t* codes, uint8_t* scales, hipStream_t stream);
 
+/* ---- latent attention over a paged cache ------------------------------------------ */
+
+/* A token's key and value, for all heads, are one latent vector c of GALE_LATENT_DIM numbers and the position part r of
+ * its key, GALE_LATENT_ROPE numbers (rotated by the caller).  The cache holds them in n_blocks blocks of block_size
+ * slots (a power of two up to GALE_MAX_BLOCK_SIZE); slot i is row i of `latent` and of `rope`.  Request r's token at
+ * position p lives in slot block_table[r][p / block_size] * block_size + p % block_size.
+ *   dtype: GALE_F16 or GALE_BF16, of rope, of 16-bit latents and of the queries that read them.
+ *   fmt 0: latent rows hold GALE_LATENT_DIM values of dtype, latent_stride elements apart; scales is NULL.
+ *   fmt GALE_MX_E2M1: latent holds MX codes back to back ([slots][256] bytes) and scales their scales ([slots][16]), the
+ *         layout of gale_mx_quantize with GALE_LATENT_DIM columns, so gale_mx_dequantize reads it; latent_stride is
+ *         not used.
+ *   rope: rows of GALE_LATENT_ROPE values of dtype, rope_stride elements apart.
+ * latent and rope are 16-byte aligned with strides of whole 16 bytes; n_blocks * block_size < 2^31.  The struct itself is
+ * in host memory and is read during the call only. */
+#define GALE_LATENT_DIM      512
+#define GALE_LATENT_ROPE      64
+#define GALE_HEAD_NOPE       128   /* expanded keys: a head's own part */
+#define GALE_HEAD_VALUE      128   /* expanded values */
+#define GALE_MAX_BLOCK_SIZE 1024
+#define GALE_MAX_REQUESTS  65536
+#define GALE_MAX_HEADS      1024
+
+typedef struct {
+  void* latent;
+  uint8_t* scales;
+  void* rope;
+  int64_t latent_stride, rope_stride;
+  int32_t dtype, fmt;
+  int32_t n_blocks, block_size;
+} gale_latent_cache;
+
+/* Block tables and slot maps of a batch, from the requests' lengths, on the GPU.  Request r has past_lens[r] tokens in the
+ * cache, in the blocks that its row of block_table names, and new_lens[r] tokens in this batch; the batch holds the
+ * requests' new tokens one request after the other, and has room for n_tok (negative lengths count as 0).  For each request:
+ *   q_starts[r] = the sum of the new lengths before it, at most n_tok; q_starts[n_req] = the sum of all, likewise;
+ *   it is refused if its blocks ceil((past + new) / block_size) pass max_blocks, or its tokens n_tok;
+ *   the others need ceil((past + new) / block_size) - ceil(past / block_size) more blocks.  They take them from free_blocks in
+ *         the order of the requests; those whose need is not met by the *n_free (at most free_cap) entries are refused;
+ *         a request that needs none is not;
+ *   kv_lens[r] = past + new, or past for a refused request;  the new blocks' ids are put into its row of block_table, the
+ *         table's other entries stay as they are.
+ * slots[t], for each of the n_tok places of the batch, is where token t goes: -1 behind the last token, for the tokens of
+ * refused requests, and where the table holds a negative id.  taken[0] = the number of entries of free_blocks that were
+ * used, from its front.
+ * past_lens, new_lens, kv_lens: int32 [n_req]; free_blocks: int32 [free_cap]; n_free, taken: int32 [1]; block_table: int32
+ * [n_req] rows of max_blocks, table_stride elements apart; slots: int64 [n_tok]; q_starts: int32 [n_req + 1].  All are
+ * device memory; no output overlaps another or an input.  n_req and n_tok may be 0. */
+int gale_paged_plan(const int32_t* past_lens, const int32_t* new_lens, int32_t n_req, int32_t block_size,
+                    const int32_t* free_blocks, int32_t free_cap, const int32_t* n_free, int32_t* block_table,
+                    int64_t table_stride, int32_t max_blocks, int32_t n_tok, int64_t* slots, int32_t* q_starts,
+                    int32_t* kv_lens, int32_t* taken, hipStream_t stream);
+
+/* Writes n_tok tokens into the cache: row slots[t] of the cache becomes token t's latent (GALE_LATENT_DIM values of the
+ * cache's dtype; into a 4-bit cache as gale_mx_quantize rounds them) and rope (GALE_LATENT_ROPE values, already rotated).
+ * Slots outside [0, n_blocks * block_size) are skipped (padding).  The slots of a call are distinct, as
+ * gale_paged_plan's are: a row whose slot is given twice ends as a mix of the two.  Rows are latent_stride and rope_stride
+ * elements apart, 16-byte aligned; they do not overlap the cache.  n_tok may be 0. */
+int gale_latent_append(const gale_latent_cache* cache, const void* latent, int64_t latent_stride, const void* rope,
+                       int64_t rope_stride, const int64_t* slots, int32_t n_tok, hipStream_t stream);
+
+/* Workspace bytes for gale_latent_attention (0 for arguments that it refuses). */
+size_t gale_latent_workspace_bytes(int32_t n_tok, int32_t n_req, int32_t n_heads);
+
+/* Latent attention, absorbed form: queries against the cached vectors themselves, for decode and drafted tokens.  Request r's
+ * queries are tokens q_starts[r] .. q_starts[r + 1] - 1, the last of its kv_lens[r] tokens.  For a query x (of one token
+ * and head) and key j, with x = (a, b), a of GALE_LATENT_DIM and b of GALE_LATENT_ROPE numbers,
+ *   s_j = scale * (a . c_j + b . r_j),   w = softmax(s),   out = sum_j w_j c_j,   lse = log(sum_j exp(s_j)).
+ * Query i of a request's n sees keys j <= kv_len - n + i when causal != 0, else all kv_len.  A key whose block id is outside
+ * [0, n_blocks) is not seen.  What a query does not see has no influence on it, NaN included; a query that sees no key
+ * gets out = 0 and lse = -infinity.  kv_lens outside [0, max_blocks * block_size] are clamped to it.  Products are exact and
+ * summed in fp32; the weights are rounded to the queries' type for the second product, relative to a running maximum,
+ * and normalised in fp32 (sums of weights times values past fp32's range, values above 2^90, are infinite); 4-bit latents are
+ * read as numbers of the queries' type, gale_mx_dequantize's rounding.
+ * q: [n_tok] tokens, q_stride elements apart, of n_heads rows of GALE_LATENT_DIM + GALE_LATENT_ROPE values of the cache's
+ * dtype; out: [n_tok] tokens, out_stride elements apart, of n_heads rows of GALE_LATENT_DIM; both 16-byte aligned with
+ * strides of whole 16 bytes.  lse: fp32 [n_tok][n_heads], or NULL.  block_table: as gale_paged_plan's; q_starts: int32
+ * [n_req + 1], ascending from 0, values outside [0, n_tok] are clamped; tokens from q_starts[n_req] on are left as they
+ * were.  n_heads <= GALE_MAX_HEADS, n_tok * n_heads < 2^31, n_req <= GALE_MAX_REQUESTS; n_req and n_tok may be 0.  ws: 256-byte
+ * aligned; nothing in it lives from call to call.  Equal calls give equal bits. */
+int gale_latent_attention(const gale_latent_cache* cache, const int32_t* block_table, int64_t table_stride,
+                          int32_t max_blocks, const int32_t* kv_lens, const int32_t* q_starts, int32_t n_req,
+                          const void* q, int64_t q_stride, int32_t n_tok, int32_t n_heads, float scale, int32_t causal,
+                          void* out, int64_t out_stride, float* lse, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Latent attention, expanded form, for prompts: the latent vectors have been taken to a key part k and a value v for every
+ * head (one product with the up-projection gives both).  s_j = scale * (a . k_j + b . r_j) with x = (a, b), a of
+ * GALE_HEAD_NOPE and b of GALE_LATENT_ROPE numbers; out = sum_j softmax(s)_j v_j; the rest as above.  Request r's queries are tokens
+ * q_starts[r] .. q_starts[r + 1] - 1 of q, its keys rows kv_starts[r] .. kv_starts[r + 1] - 1 of k, k_rope and v.
+ * q: [n_tok] tokens, q_stride apart, of n_heads rows of GALE_HEAD_NOPE + GALE_LATENT_ROPE; k and v: [n_kv] tokens,
+ * k_stride and v_stride apart, of n_heads rows of GALE_HEAD_NOPE and GALE_HEAD_VALUE values, k_head_stride and v_head_stride apart
+ * (both may lie in one product's output); k_rope: [n_kv] rows of GALE_LATENT_ROPE; out: [n_tok] tokens of
+ * n_heads rows of GALE_HEAD_VALUE; all of dtype (GALE_F16 or GALE_BF16), strides in elements, 16-byte aligned with strides of
+ * whole 16 bytes.  lse: fp32 [n_tok][n_heads], or NULL.  q_starts, kv_starts: int32 [n_req + 1], ascending from 0, clamped
+ * to [0, n_tok] and [0, n_kv]; tokens from q_starts[n_req] on are left as they were. */
+int gale_latent_attention_expanded(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                   int64_t k_head_stride, const void* k_rope, int64_t k_rope_stride, const void* v,
+                                   int64_t v_stride, int64_t v_head_stride, int32_t dtype, int32_t n_tok, int32_t n_kv,
+                                   int32_t n_heads, const int32_t* q_starts, const int32_t* kv_starts, int32_t n_req,
+                                   float scale, int32_t causal, void* out, int64_t out_stride, float* lse,
+                                   hipStream_t stream);
+
 /* Diagnostic, not a step of the method: reads `bytes` bytes at device pointer src (16-byte
  * aligned, a positive multiple of 16) once with a plain streaming kernel, 16 bytes per lane per
  * step, on `stream`, and writes one folded word per workgroup to the device array sink

@@ -23,6 +23,8 @@ GALE_MX_E2M1, GALE_MX_E4M3 = 1, 2
 GALE_MX_BLOCK, GALE_MX_GROUP = 32, 128
 GALE_SCORE_SOFTMAX, GALE_SCORE_SIGMOID = 1, 2
 GALE_GROUP_MAX, GALE_GROUP_TOP2 = 1, 2
+GALE_LATENT_DIM, GALE_LATENT_ROPE, GALE_HEAD_NOPE, GALE_HEAD_VALUE = 512, 64, 128, 128
+GALE_MAX_BLOCK_SIZE = 1024
 GALE_X_ROTATED = 0x1
 GALE_X_PREPARED = 0x2
 GALE_PATH_DECODE = 0x10
@@ -91,6 +93,12 @@ class gale_layer_io(ctypes.Structure):
                 ("topk_idx", ctypes.c_void_p), ("topk_w", ctypes.c_void_p)]
 
 
+class gale_latent_cache(ctypes.Structure):
+    _fields_ = [("latent", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rope", ctypes.c_void_p),
+                ("latent_stride", ctypes.c_int64), ("rope_stride", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("fmt", ctypes.c_int32), ("n_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32)]
+
+
 class gale_sizes(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in
                 ("signs", "block_scales", "row_scales", "row_ptr", "out_cols", "out_vals", "format_bytes")]
@@ -133,6 +141,13 @@ _SIGS = {
     "gale_mx_gemm": (_I32, [_I32, _I32, _I32, _P, _P, _I32, _P, _P, _P, _I64, _P, _I32, _I64, _P]),
     "gale_add_rms_norm": (_I32, [_P, _I64, _P, _I64, _I32, _I64, _I32, _P, _I32, ctypes.c_float, _P, _P, _I32, _I32,
                                  _P, _P, _P]),
+    "gale_paged_plan": (_I32, [_P, _P, _I32, _I32, _P, _I32, _P, _P, _I64, _I32, _I32, _P, _P, _P, _P, _P]),
+    "gale_latent_append": (_I32, [ctypes.POINTER(gale_latent_cache), _P, _I64, _P, _I64, _P, _I32, _P]),
+    "gale_latent_workspace_bytes": (_SZ, [_I32, _I32, _I32]),
+    "gale_latent_attention": (_I32, [ctypes.POINTER(gale_latent_cache), _P, _I64, _I32, _P, _P, _I32, _P, _I64, _I32, _I32,
+                                     ctypes.c_float, _I32, _P, _I64, _P, _P, _SZ, _P]),
+    "gale_latent_attention_expanded": (_I32, [_P, _I64, _P, _I64, _I64, _P, _I64, _P, _I64, _I64, _I32, _I32, _I32, _I32,
+                                              _P, _P, _I32, ctypes.c_float, _I32, _P, _I64, _P, _P]),
     "gale_decode_stack_workspace_bytes": (_SZ, [_I32, _I32, _I32]),
     "gale_moe_decode_stack": (_I32, [_I32, _I32, _I32, _I32, _I32, _P, _P, _SZ, _U32, _P]),
     "gale_moe_decode_stack_static": (_I32, [_I32, _I32, _I32, _I32, _I32, _P, _U32, _P]),
@@ -825,3 +840,195 @@ def moe_layer_fwd_given(table: DescriptorTable, hidden: int, inter: int, topk_id
              topk_w.data_ptr(), top_k, x.data_ptr(), n_tok, y.data_ptr(), ws.data_ptr(), ws.numel(),
              _with_stage(flags, table))
     return y
+
+
+# ----------------------------------------------------------------------------
+# latent attention over a paged cache
+# ----------------------------------------------------------------------------
+def _int32_vector(name: str, t: torch.Tensor, n: int) -> None:
+    if t.dtype is not torch.int32 or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor [{n}]")
+
+
+def _int32_table(name: str, t: torch.Tensor, n_req: int) -> int:
+    """Row stride of a block table [n_req, max_blocks]."""
+    if t.dtype is not torch.int32 or t.dim() != 2 or t.shape[0] != n_req or \
+            (n_req and t.shape[1] > 1 and t.stride(1) != 1) or (n_req > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{name} must be an int32 tensor [{n_req}, max_blocks] of whole rows")
+    return t.stride(0) if n_req > 1 else t.shape[1]
+
+
+class LatentCache:
+    """A paged cache of latent vectors: slot i is row i of `latent` and of `rope`.
+
+    latent: a 16-bit tensor [slots, 512], or an MXTensor of 512 columns in GALE_MX_E2M1; rope: a 16-bit tensor [slots, 64]
+    of the latent's type (with 4-bit latents: of the queries').  slots is a multiple of block_size, a power of two."""
+    __slots__ = ("latent", "rope", "block_size", "n_blocks", "dtype", "desc", "device_index")
+
+    def __init__(self, latent, rope: torch.Tensor, block_size: int):
+        mx = isinstance(latent, MXTensor)
+        rows = latent.codes if mx else latent
+        if rope.dtype not in (torch.float16, torch.bfloat16) or rope.dim() != 2 or rope.shape[1] != GALE_LATENT_ROPE or \
+                rope.stride(1) != 1:
+            raise ValueError(f"rope must be a 16-bit tensor [slots, {GALE_LATENT_ROPE}] of whole rows")
+        slots = rope.shape[0]
+        if mx:
+            if latent.fmt != GALE_MX_E2M1 or latent.cols != GALE_LATENT_DIM or latent.rows != slots:
+                raise ValueError(f"latent must hold {slots} rows of {GALE_LATENT_DIM} columns in GALE_MX_E2M1")
+        elif latent.dtype is not rope.dtype or latent.shape != (slots, GALE_LATENT_DIM) or latent.stride(1) != 1:
+            raise ValueError(f"latent must be [{slots}, {GALE_LATENT_DIM}] of rope's type, of whole rows")
+        if block_size < 1 or slots < block_size or slots % block_size:
+            raise ValueError("the slots must be whole blocks")
+        _same_device(rope.get_device(), rows)
+        self.latent, self.rope, self.block_size, self.n_blocks = latent, rope, block_size, slots // block_size
+        self.dtype, self.device_index = rope.dtype, rope.get_device()
+        self.desc = gale_latent_cache(rows.data_ptr(), latent.scales.data_ptr() if mx else None, rope.data_ptr(),
+                                      0 if mx else latent.stride(0), rope.stride(0), _dt3(rope),
+                                      GALE_MX_E2M1 if mx else 0, self.n_blocks, block_size)
+
+    @classmethod
+    def empty(cls, n_blocks: int, block_size: int, dtype=torch.bfloat16, mx: bool = False, device="cuda") -> "LatentCache":
+        slots = n_blocks * block_size
+        latent = MXTensor.empty(slots, GALE_LATENT_DIM, GALE_MX_E2M1, device) if mx else \
+            torch.empty(slots, GALE_LATENT_DIM, dtype=dtype, device=device)
+        return cls(latent, torch.empty(slots, GALE_LATENT_ROPE, dtype=dtype, device=device), block_size)
+
+
+def paged_plan(past_lens: torch.Tensor, new_lens: torch.Tensor, free_blocks: torch.Tensor, n_free: torch.Tensor,
+               block_table: torch.Tensor, block_size: int, n_tok: int, out=None):
+    """(slots int64 [n_tok], q_starts int32 [R + 1], kv_lens int32 [R], taken int32 [1]) of a batch of R requests with
+    past_lens tokens in the cache and new_lens in the batch (int32 [R]); new blocks come from the front of free_blocks
+    (int32, the first n_free[0] of them) and are put into block_table (int32 [R, max_blocks]) in place.  Refused requests
+    (no room in the table, the batch or the free blocks) keep kv_lens = past_lens and get slots of -1.  out: the four
+    outputs' tensors."""
+    R, dev = past_lens.shape[0] if past_lens.dim() else 0, past_lens.get_device()
+    _int32_vector("past_lens", past_lens, R)
+    _int32_vector("new_lens", new_lens, R)
+    _int32_vector("free_blocks", free_blocks, free_blocks.numel())
+    _int32_vector("n_free", n_free, 1)
+    stride = _int32_table("block_table", block_table, R)
+    if out is None:
+        out = (torch.empty(n_tok, dtype=torch.int64, device=past_lens.device),
+               *(torch.empty(n, dtype=torch.int32, device=past_lens.device) for n in (R + 1, R, 1)))
+    slots, q_starts, kv_lens, taken = out
+    if slots.dtype is not torch.int64 or slots.shape != (n_tok,) or not slots.is_contiguous():
+        raise ValueError(f"slots must be a contiguous int64 tensor [{n_tok}]")
+    _int32_vector("q_starts", q_starts, R + 1)
+    _int32_vector("kv_lens", kv_lens, R)
+    _int32_vector("taken", taken, 1)
+    _same_device(dev, new_lens, free_blocks, n_free, block_table, *out)
+    _enqueue("gale_paged_plan", dev, past_lens.data_ptr(), new_lens.data_ptr(), R, block_size, free_blocks.data_ptr(),
+             free_blocks.numel(), n_free.data_ptr(), block_table.data_ptr(), stride, block_table.shape[1], n_tok,
+             slots.data_ptr(), q_starts.data_ptr(), kv_lens.data_ptr(), taken.data_ptr())
+    return slots, q_starts, kv_lens, taken
+
+
+def _aligned_rows(t: torch.Tensor, cols: int, dtype) -> torch.Tensor:
+    """t [n, cols] of dtype itself where its rows are whole, 16-byte aligned and whole 16 bytes apart, else a copy."""
+    if t.dim() != 2 or t.shape[1] != cols or t.dtype is not dtype:
+        raise ValueError(f"rows of {cols} values of {dtype} are needed")
+    if t.stride(1) != 1 or (t.shape[0] > 1 and (t.stride(0) < cols or t.stride(0) % 8)) or t.data_ptr() % 16:
+        t = t.clone(memory_format=torch.contiguous_format)
+    return t
+
+
+def latent_append(cache: LatentCache, latent: torch.Tensor, rope: torch.Tensor, slots: torch.Tensor) -> LatentCache:
+    """Writes tokens into the cache: latent [T, 512] and rope [T, 64] (the cache's type) go to rows slots (int64 [T],
+    paged_plan's; others than the cache's are skipped)."""
+    T, dev = slots.numel(), cache.device_index
+    latent = _aligned_rows(latent, GALE_LATENT_DIM, cache.dtype)
+    rope = _aligned_rows(rope, GALE_LATENT_ROPE, cache.dtype)
+    if slots.dtype is not torch.int64 or slots.dim() != 1 or not slots.is_contiguous() or latent.shape[0] != T or \
+            rope.shape[0] != T:
+        raise ValueError("slots must be a contiguous int64 tensor with an entry for each row of latent and rope")
+    _same_device(dev, latent, rope, slots)
+    _enqueue("gale_latent_append", dev, cache.desc, latent.data_ptr(), latent.stride(0) if T > 1 else GALE_LATENT_DIM,
+             rope.data_ptr(), rope.stride(0) if T > 1 else GALE_LATENT_ROPE, slots.data_ptr(), T)
+    return cache
+
+
+def latent_workspace_bytes(n_tok: int, n_req: int, n_heads: int) -> int:
+    return int(lib().gale_latent_workspace_bytes(n_tok, n_req, n_heads))
+
+
+def _head_rows(name: str, t: torch.Tensor, cols: int, dtype, apart: bool) -> torch.Tensor:
+    """t [tokens, heads, cols] of dtype: itself where its heads are whole, 16-byte aligned rows (back to back unless
+    `apart`), else a copy."""
+    if t.dim() != 3 or t.shape[2] != cols or t.dtype is not dtype or not t.shape[1]:
+        raise ValueError(f"{name} must be [tokens, heads, {cols}] of {dtype}")
+    n, h, _ = t.shape
+    s0, s1, s2 = t.stride()
+    fine = s2 == 1 and t.data_ptr() % 16 == 0 and (h == 1 or (s1 >= cols and s1 % 8 == 0 if apart else s1 == cols)) and \
+        (n <= 1 or (s0 >= (h - 1) * (s1 if h > 1 else 0) + cols and s0 % 8 == 0))
+    return t if fine else t.clone(memory_format=torch.contiguous_format)
+
+
+def _strides(t: torch.Tensor):
+    """(token stride, head stride) of [tokens, heads, cols], also where a dimension of one leaves them open."""
+    n, h, cols = t.shape
+    head = t.stride(1) if h > 1 else cols
+    return (t.stride(0) if n > 1 else (h - 1) * head + cols), head
+
+
+def _attention_out(q: torch.Tensor, cols: int, out, lse):
+    n, h = q.shape[:2]
+    if out is None:
+        out = torch.empty(n, h, cols, dtype=q.dtype, device=q.device)
+    elif out.shape != (n, h, cols) or out.dtype is not q.dtype or out.stride(2) != 1 or (h > 1 and out.stride(1) != cols) or \
+            (n > 1 and out.stride(0) < h * cols):
+        raise ValueError(f"out must be [{n}, {h}, {cols}] of q's type, a token's heads back to back")
+    if lse is None:
+        lse = torch.empty(n, h, dtype=torch.float32, device=q.device)
+    elif lse.shape != (n, h) or lse.dtype is not torch.float32 or not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous fp32 tensor [{n}, {h}]")
+    return out, lse
+
+
+def latent_attention(q: torch.Tensor, cache: LatentCache, block_table: torch.Tensor, q_starts: torch.Tensor,
+                     kv_lens: torch.Tensor, scale: float, causal: bool = True, out: Optional[torch.Tensor] = None,
+                     lse: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
+    """(out [T, H, 512], lse fp32 [T, H]): absorbed latent attention of q [T, H, 576] over the cached vectors of each
+    request (block_table int32 [R, max_blocks]; q_starts int32 [R + 1] and kv_lens int32 [R] as paged_plan gives them).
+    Query i of a request's n sees its first kv_len - n + i + 1 keys, or all with causal=False."""
+    R, dev = kv_lens.shape[0] if kv_lens.dim() else 0, cache.device_index
+    q = _head_rows("q", q, GALE_LATENT_DIM + GALE_LATENT_ROPE, cache.dtype, False)
+    T, H = q.shape[:2]
+    _int32_vector("kv_lens", kv_lens, R)
+    _int32_vector("q_starts", q_starts, R + 1)
+    stride = _int32_table("block_table", block_table, R)
+    out, lse = _attention_out(q, GALE_LATENT_DIM, out, lse)
+    if ws is None:
+        ws = _workspace(latent_workspace_bytes(T, R, H), q.device)
+    _same_device(dev, q, block_table, q_starts, kv_lens, out, lse, ws)
+    _enqueue("gale_latent_attention", dev, cache.desc, block_table.data_ptr(), stride, block_table.shape[1],
+             kv_lens.data_ptr(), q_starts.data_ptr(), R, q.data_ptr(), _strides(q)[0], T, H, scale, int(bool(causal)),
+             out.data_ptr(), _strides(out)[0], lse.data_ptr(), ws.data_ptr(), ws.numel())
+    return out, lse
+
+
+def latent_attention_expanded(q: torch.Tensor, k: torch.Tensor, k_rope: torch.Tensor, v: torch.Tensor,
+                              q_starts: torch.Tensor, kv_starts: torch.Tensor, scale: float, causal: bool = True,
+                              out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None):
+    """(out [T, H, 128], lse fp32 [T, H]): latent attention of prompts with keys and values of every head, q [T, H, 192],
+    k [S, H, 128], k_rope [S, 64] (shared by the heads), v [S, H, 128]; k and v may be halves of one product's output
+    [S, H, 256].  Request r's queries are tokens q_starts[r] .. q_starts[r + 1] - 1, its keys kv_starts[r] .. likewise
+    (int32 [R + 1]); query i of n sees the first n_keys - n + i + 1 of them, or all with causal=False."""
+    R, dev = q_starts.numel() - 1, q.get_device()
+    code = _dt3(q)
+    q = _head_rows("q", q, GALE_HEAD_NOPE + GALE_LATENT_ROPE, q.dtype, False)
+    k = _head_rows("k", k, GALE_HEAD_NOPE, q.dtype, True)
+    v = _head_rows("v", v, GALE_HEAD_VALUE, q.dtype, True)
+    k_rope = _aligned_rows(k_rope, GALE_LATENT_ROPE, q.dtype)
+    T, H = q.shape[:2]
+    S = k.shape[0]
+    if R < 0 or k.shape[1] != H or v.shape[:2] != (S, H) or k_rope.shape[0] != S:
+        raise ValueError("q, k, k_rope and v must agree on heads and keys, and q_starts hold R + 1 entries")
+    _int32_vector("q_starts", q_starts, R + 1)
+    _int32_vector("kv_starts", kv_starts, R + 1)
+    out, lse = _attention_out(q, GALE_HEAD_VALUE, out, lse)
+    _same_device(dev, k, k_rope, v, q_starts, kv_starts, out, lse)
+    (ks, kh), (vs, vh) = _strides(k), _strides(v)
+    _enqueue("gale_latent_attention_expanded", dev, q.data_ptr(), _strides(q)[0], k.data_ptr(), ks, kh, k_rope.data_ptr(),
+             k_rope.stride(0) if S > 1 else GALE_LATENT_ROPE, v.data_ptr(), vs, vh, code, T, S, H, q_starts.data_ptr(),
+             kv_starts.data_ptr(), R, scale, int(bool(causal)), out.data_ptr(), _strides(out)[0], lse.data_ptr())
+    return out, lse

@@ -1067,3 +1067,207 @@ extern "C" int gale_add_rms_norm(const void* x, int64_t x_stride, const void* re
   return hip_status(fn, launch_add_rms_norm(x, x_stride, residual, residual_stride, dtype, rows, cols, weight,
                                             weight_dtype, eps, sum_out, y, y_dtype, mx_fmt, codes, scales, stream));
 }
+
+// ---------------------------------------------------------------------------
+// Latent attention and its paged cache
+// ---------------------------------------------------------------------------
+static int block_shift(int32_t block_size) {
+  if (block_size < 1 || block_size > GALE_MAX_BLOCK_SIZE || (block_size & (block_size - 1))) return -1;
+  return __builtin_ctz((unsigned)block_size);
+}
+
+extern "C" int gale_paged_plan(const int32_t* past_lens, const int32_t* new_lens, int32_t n_req, int32_t block_size,
+                               const int32_t* free_blocks, int32_t free_cap, const int32_t* n_free, int32_t* block_table,
+                               int64_t table_stride, int32_t max_blocks, int32_t n_tok, int64_t* slots, int32_t* q_starts,
+                               int32_t* kv_lens, int32_t* taken, hipStream_t stream) {
+  const char* fn = "gale_paged_plan";
+  const int shift = block_shift(block_size);
+  if (n_req < 0 || n_req > GALE_MAX_REQUESTS || shift < 0 || free_cap < 0 || max_blocks < 0 ||
+      table_stride < max_blocks || n_tok < 0) {
+    set_error("%s: n_req=%d block_size=%d free_cap=%d max_blocks=%d table_stride=%lld n_tok=%d", fn, n_req, block_size,
+              free_cap, max_blocks, (long long)table_stride, n_tok);
+    return GALE_ERR_SHAPE;
+  }
+  if ((n_req && (!past_lens || !new_lens || !kv_lens)) || (free_cap && !free_blocks) || !n_free ||
+      (n_req && max_blocks && !block_table) || (n_tok && !slots) || !q_starts || !taken) {
+    set_error("%s: NULL pointer", fn);
+    return GALE_ERR_NULL;
+  }
+  if (!aligned(past_lens, 4) || !aligned(new_lens, 4) || !aligned(free_blocks, 4) || !aligned(n_free, 4) ||
+      !aligned(block_table, 4) || !aligned(slots, 8) || !aligned(q_starts, 4) || !aligned(kv_lens, 4) || !aligned(taken, 4)) {
+    set_error("%s: misaligned pointer", fn);
+    return GALE_ERR_ALIGN;
+  }
+  const int64_t r4 = 4 * (int64_t)n_req;
+  const RowBytes in[4] = {{past_lens, n_req ? 1 : 0, 0, r4}, {new_lens, n_req ? 1 : 0, 0, r4},
+                          {free_blocks, free_cap ? 1 : 0, 0, 4 * (int64_t)free_cap}, {n_free, 1, 0, 4}};
+  const RowBytes out[5] = {{block_table, max_blocks ? n_req : 0, 4 * table_stride, 4 * (int64_t)max_blocks},
+                           {slots, n_tok ? 1 : 0, 0, 8 * (int64_t)n_tok}, {q_starts, 1, 0, r4 + 4},
+                           {kv_lens, n_req ? 1 : 0, 0, r4}, {taken, 1, 0, 4}};
+  for (int o = 0; o < 5; ++o) {
+    for (const RowBytes& i : in)
+      if (meet(i, out[o])) { set_error("%s: an output overlaps an input", fn); return GALE_ERR_SHAPE; }
+    for (int i = 0; i < o; ++i)
+      if (meet(out[i], out[o])) { set_error("%s: two outputs overlap", fn); return GALE_ERR_SHAPE; }
+  }
+  return hip_status(fn, launch_paged_plan(past_lens, new_lens, n_req, shift, free_blocks, free_cap, n_free, block_table,
+                                          table_stride, max_blocks, n_tok, slots, q_starts, kv_lens, taken, stream));
+}
+
+// 16-bit rows of len values: 16-byte aligned, whole 16 bytes apart.
+static bool rows16(const void* p, int64_t stride) { return aligned(p, 16) && stride % 8 == 0; }
+
+static int check_cache(const char* fn, const gale_latent_cache* c, RowBytes (&rows)[3]) {
+  if (!c) { set_error("%s: NULL cache", fn); return GALE_ERR_NULL; }
+  if ((c->dtype != GALE_F16 && c->dtype != GALE_BF16) || (c->fmt != 0 && c->fmt != GALE_MX_E2M1)) {
+    set_error("%s: a cache of dtype %d, fmt %d", fn, c->dtype, c->fmt);
+    return GALE_ERR_DTYPE;
+  }
+  if (c->n_blocks < 1 || block_shift(c->block_size) < 0 || (int64_t)c->n_blocks * c->block_size > INT32_MAX ||
+      (c->fmt == 0 && c->latent_stride < GALE_LATENT_DIM) || c->rope_stride < GALE_LATENT_ROPE) {
+    set_error("%s: a cache of %d blocks of %d slots, strides %lld, %lld", fn, c->n_blocks, c->block_size,
+              (long long)c->latent_stride, (long long)c->rope_stride);
+    return GALE_ERR_SHAPE;
+  }
+  if (!c->latent || !c->rope || (c->fmt != 0 && !c->scales)) { set_error("%s: NULL cache pointer", fn); return GALE_ERR_NULL; }
+  if ((c->fmt == 0 ? !rows16(c->latent, c->latent_stride) : !aligned(c->latent, 16) || !aligned(c->scales, 16)) ||
+      !rows16(c->rope, c->rope_stride)) {
+    set_error("%s: cache rows need 16-byte alignment", fn);
+    return GALE_ERR_ALIGN;
+  }
+  const int64_t slots = (int64_t)c->n_blocks * c->block_size;
+  if (c->fmt == 0) {
+    rows[0] = RowBytes(c->latent, slots, c->latent_stride * 2, GALE_LATENT_DIM * 2);
+    rows[1] = RowBytes(nullptr, 0, 0, 0);
+  } else {
+    rows[0] = RowBytes(c->latent, 1, 0, slots * (GALE_LATENT_DIM / 2));
+    rows[1] = RowBytes(c->scales, 1, 0, slots * (GALE_LATENT_DIM / 32));
+  }
+  rows[2] = RowBytes(c->rope, slots, c->rope_stride * 2, GALE_LATENT_ROPE * 2);
+  return GALE_OK;
+}
+
+extern "C" int gale_latent_append(const gale_latent_cache* cache, const void* latent, int64_t latent_stride,
+                                  const void* rope, int64_t rope_stride, const int64_t* slots, int32_t n_tok,
+                                  hipStream_t stream) {
+  const char* fn = "gale_latent_append";
+  RowBytes c[3] = {{nullptr, 0, 0, 0}, {nullptr, 0, 0, 0}, {nullptr, 0, 0, 0}};
+  const int st = check_cache(fn, cache, c);
+  if (st) return st;
+  if (n_tok < 0 || latent_stride < GALE_LATENT_DIM || rope_stride < GALE_LATENT_ROPE) {
+    set_error("%s: n_tok=%d strides %lld, %lld", fn, n_tok, (long long)latent_stride, (long long)rope_stride);
+    return GALE_ERR_SHAPE;
+  }
+  if (n_tok == 0) return GALE_OK;
+  if (!latent || !rope || !slots) { set_error("%s: NULL pointer", fn); return GALE_ERR_NULL; }
+  if (!rows16(latent, latent_stride) || !rows16(rope, rope_stride) || !aligned(slots, 8)) {
+    set_error("%s: rows need 16-byte, slots 8-byte alignment", fn);
+    return GALE_ERR_ALIGN;
+  }
+  const RowBytes in[3] = {{latent, n_tok, latent_stride * 2, GALE_LATENT_DIM * 2}, {rope, n_tok, rope_stride * 2, GALE_LATENT_ROPE * 2},
+                          {slots, 1, 0, 8 * (int64_t)n_tok}};
+  for (int o = 0; o < 3; ++o) {
+    for (const RowBytes& i : in)
+      if (meet(i, c[o])) { set_error("%s: the cache overlaps an input", fn); return GALE_ERR_SHAPE; }
+    for (int i = 0; i < o; ++i)
+      if (meet(c[i], c[o])) { set_error("%s: the cache's parts overlap", fn); return GALE_ERR_SHAPE; }
+  }
+  return hip_status(fn, launch_latent_append(*cache, latent, latent_stride, rope, rope_stride, slots, n_tok, stream));
+}
+
+static bool attention_sizes_ok(int32_t n_tok, int32_t n_req, int32_t n_heads) {
+  return n_tok >= 0 && n_req >= 0 && n_req <= GALE_MAX_REQUESTS && n_heads >= 1 && n_heads <= GALE_MAX_HEADS &&
+         (int64_t)n_tok * n_heads <= INT32_MAX;
+}
+
+extern "C" size_t gale_latent_workspace_bytes(int32_t n_tok, int32_t n_req, int32_t n_heads) {
+  if (!attention_sizes_ok(n_tok, n_req, n_heads)) return 0;
+  return latent_workspace_bytes(n_tok, n_req, n_heads);
+}
+
+extern "C" int gale_latent_attention(const gale_latent_cache* cache, const int32_t* block_table, int64_t table_stride,
+                                     int32_t max_blocks, const int32_t* kv_lens, const int32_t* q_starts, int32_t n_req,
+                                     const void* q, int64_t q_stride, int32_t n_tok, int32_t n_heads, float scale,
+                                     int32_t causal, void* out, int64_t out_stride, float* lse, void* ws, size_t ws_bytes,
+                                     hipStream_t stream) {
+  const char* fn = "gale_latent_attention";
+  RowBytes c[3] = {{nullptr, 0, 0, 0}, {nullptr, 0, 0, 0}, {nullptr, 0, 0, 0}};
+  const int st = check_cache(fn, cache, c);
+  if (st) return st;
+  const int64_t ql = (int64_t)n_heads * (GALE_LATENT_DIM + GALE_LATENT_ROPE), ol = (int64_t)n_heads * GALE_LATENT_DIM;
+  if (!attention_sizes_ok(n_tok, n_req, n_heads) || max_blocks < 0 || table_stride < max_blocks || q_stride < ql ||
+      out_stride < ol) {
+    set_error("%s: n_tok=%d n_req=%d n_heads=%d max_blocks=%d strides %lld (table), %lld (q), %lld (out)", fn, n_tok, n_req,
+              n_heads, max_blocks, (long long)table_stride, (long long)q_stride, (long long)out_stride);
+    return GALE_ERR_SHAPE;
+  }
+  if (!(fabsf(scale) < INFINITY)) { set_error("%s: scale must be finite", fn); return GALE_ERR_SHAPE; }
+  if (n_tok == 0 || n_req == 0) return GALE_OK;
+  if (!q || !out || !kv_lens || !q_starts || (max_blocks && !block_table)) { set_error("%s: NULL pointer", fn); return GALE_ERR_NULL; }
+  if (!rows16(q, q_stride) || !rows16(out, out_stride) || !aligned(block_table, 4) || !aligned(kv_lens, 4) ||
+      !aligned(q_starts, 4) || !aligned(lse, 4) || !aligned(ws, 256)) {
+    set_error("%s: q and out need 16-byte rows, ws 256-byte alignment", fn);
+    return GALE_ERR_ALIGN;
+  }
+  const size_t need = latent_workspace_bytes(n_tok, n_req, n_heads);
+  if (need && (!ws || ws_bytes < need)) { set_error("%s: workspace of %zu bytes, %zu needed", fn, ws_bytes, need); return GALE_ERR_WORKSPACE; }
+  const RowBytes in[7] = {c[0], c[1], c[2], {q, n_tok, q_stride * 2, ql * 2},
+                          {block_table, max_blocks ? n_req : 0, 4 * table_stride, 4 * (int64_t)max_blocks},
+                          {kv_lens, 1, 0, 4 * (int64_t)n_req}, {q_starts, 1, 0, 4 * (int64_t)n_req + 4}};
+  const RowBytes o[3] = {{out, n_tok, out_stride * 2, ol * 2}, {lse, 1, 0, 4 * (int64_t)n_tok * n_heads},
+                         {need ? ws : nullptr, 1, 0, (int64_t)need}};
+  for (int i = 0; i < 3; ++i) {
+    for (const RowBytes& b : in)
+      if (meet(b, o[i])) { set_error("%s: an output overlaps an input", fn); return GALE_ERR_SHAPE; }
+    for (int j = 0; j < i; ++j)
+      if (meet(o[j], o[i])) { set_error("%s: two outputs overlap", fn); return GALE_ERR_SHAPE; }
+  }
+  const LatentParams p = {(const uint8_t*)cache->latent, cache->scales, (const uint8_t*)cache->rope,
+                          cache->fmt ? GALE_LATENT_DIM / 2 : 2 * cache->latent_stride, 2 * cache->rope_stride, cache->n_blocks,
+                          block_shift(cache->block_size), block_table, table_stride, max_blocks, kv_lens, q_starts, n_req,
+                          n_tok, n_heads, causal != 0, (const uint16_t*)q, q_stride, scale, (uint16_t*)out, out_stride, lse};
+  return hip_status(fn, launch_latent_attention(p, cache->dtype, cache->fmt, ws, stream));
+}
+
+extern "C" int gale_latent_attention_expanded(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                              int64_t k_head_stride, const void* k_rope, int64_t k_rope_stride,
+                                              const void* v, int64_t v_stride, int64_t v_head_stride, int32_t dtype,
+                                              int32_t n_tok, int32_t n_kv, int32_t n_heads, const int32_t* q_starts,
+                                              const int32_t* kv_starts, int32_t n_req, float scale, int32_t causal,
+                                              void* out, int64_t out_stride, float* lse, hipStream_t stream) {
+  const char* fn = "gale_latent_attention_expanded";
+  if (dtype != GALE_F16 && dtype != GALE_BF16) { set_error("%s: dtype %d", fn, dtype); return GALE_ERR_DTYPE; }
+  const int64_t ql = (int64_t)n_heads * (GALE_HEAD_NOPE + GALE_LATENT_ROPE), ol = (int64_t)n_heads * GALE_HEAD_VALUE;
+  // a token's heads, one after the other (head strides past 32 bits are refused below)
+  const int64_t kl = (n_heads - 1) * (int64_t)(int32_t)k_head_stride + GALE_HEAD_NOPE,
+                vl = (n_heads - 1) * (int64_t)(int32_t)v_head_stride + GALE_HEAD_VALUE;
+  if (!attention_sizes_ok(n_tok, n_req, n_heads) || n_kv < 0 || q_stride < ql || out_stride < ol ||
+      k_head_stride < GALE_HEAD_NOPE || v_head_stride < GALE_HEAD_VALUE || k_head_stride > INT32_MAX ||
+      v_head_stride > INT32_MAX || k_stride < kl || v_stride < vl || k_rope_stride < GALE_LATENT_ROPE) {
+    set_error("%s: n_tok=%d n_kv=%d n_req=%d n_heads=%d strides %lld (q), %lld, %lld (k), %lld (k_rope), %lld, %lld (v), %lld (out)",
+              fn, n_tok, n_kv, n_req, n_heads, (long long)q_stride, (long long)k_stride, (long long)k_head_stride,
+              (long long)k_rope_stride, (long long)v_stride, (long long)v_head_stride, (long long)out_stride);
+    return GALE_ERR_SHAPE;
+  }
+  if (!(fabsf(scale) < INFINITY)) { set_error("%s: scale must be finite", fn); return GALE_ERR_SHAPE; }
+  if (n_tok == 0 || n_req == 0) return GALE_OK;
+  if (!q || !out || !q_starts || !kv_starts || (n_kv && (!k || !k_rope || !v))) { set_error("%s: NULL pointer", fn); return GALE_ERR_NULL; }
+  if (!rows16(q, q_stride) || !rows16(out, out_stride) || !rows16(k, k_stride) || k_head_stride % 8 || !rows16(v, v_stride) ||
+      v_head_stride % 8 || !rows16(k_rope, k_rope_stride) || !aligned(q_starts, 4) || !aligned(kv_starts, 4) ||
+      !aligned(lse, 4)) {
+    set_error("%s: q, k, k_rope, v and out need 16-byte rows", fn);
+    return GALE_ERR_ALIGN;
+  }
+  const RowBytes in[6] = {{q, n_tok, q_stride * 2, ql * 2}, {k, n_kv, k_stride * 2, kl * 2}, {k_rope, n_kv, k_rope_stride * 2, GALE_LATENT_ROPE * 2},
+                          {v, n_kv, v_stride * 2, vl * 2}, {q_starts, 1, 0, 4 * (int64_t)n_req + 4},
+                          {kv_starts, 1, 0, 4 * (int64_t)n_req + 4}};
+  const RowBytes o[2] = {{out, n_tok, out_stride * 2, ol * 2}, {lse, 1, 0, 4 * (int64_t)n_tok * n_heads}};
+  for (int i = 0; i < 2; ++i)
+    for (const RowBytes& b : in)
+      if (meet(b, o[i])) { set_error("%s: an output overlaps an input", fn); return GALE_ERR_SHAPE; }
+  if (meet(o[0], o[1])) { set_error("%s: two outputs overlap", fn); return GALE_ERR_SHAPE; }
+  const PromptParams p = {(const uint16_t*)q, (const uint16_t*)k, (const uint16_t*)k_rope, (const uint16_t*)v, q_stride, k_stride,
+                          k_head_stride, k_rope_stride, v_stride, v_head_stride, n_tok, n_kv, n_heads, n_req, causal != 0,
+                          q_starts, kv_starts, scale, (uint16_t*)out, out_stride, lse};
+  return hip_status(fn, launch_prompt_attention(p, dtype, stream));
+}

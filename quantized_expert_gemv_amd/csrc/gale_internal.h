@@ -210,6 +210,45 @@ hipError_t launch_route_scored(const void* logits, int dtype, int64_t stride, in
                                int score, int G, int keep, int rule, int k, int renorm, float scale, int32_t* idx,
                                float* w, hipStream_t s);
 
+// latent attention and its paged cache
+struct LatentParams {
+  const uint8_t* latent;      // rows of 16-bit values, latent_bytes apart, or 4-bit codes
+  const uint8_t* scales;      // 4-bit codes: their scales
+  const uint8_t* rope;
+  int64_t latent_bytes, rope_bytes;
+  int n_blocks, block_shift;
+  const int32_t* table;
+  int64_t table_stride;
+  int max_blocks;
+  const int32_t* kv_lens;
+  const int32_t* q_starts;
+  int n_req, n_tok, n_heads, causal;
+  const uint16_t* q;
+  int64_t q_stride;
+  float scale;
+  uint16_t* out;
+  int64_t out_stride;
+  float* lse;
+};
+struct PromptParams {
+  const uint16_t *q, *k, *kr, *v;
+  int64_t q_stride, k_stride, k_head, kr_stride, v_stride, v_head;
+  int n_tok, n_kv, n_heads, n_req, causal;
+  const int32_t *q_starts, *kv_starts;
+  float scale;
+  uint16_t* out;
+  int64_t out_stride;
+  float* lse;
+};
+hipError_t launch_paged_plan(const int32_t* past, const int32_t* news, int n_req, int block_shift, const int32_t* free_blocks,
+                             int free_cap, const int32_t* n_free, int32_t* table, int64_t table_stride, int max_blocks,
+                             int n_tok, int64_t* slots, int32_t* q_starts, int32_t* kv_lens, int32_t* taken, hipStream_t s);
+hipError_t launch_latent_append(const gale_latent_cache& c, const void* latent, int64_t latent_stride, const void* rope,
+                                int64_t rope_stride, const int64_t* slots, int n_tok, hipStream_t s);
+size_t latent_workspace_bytes(int n_tok, int n_req, int n_heads);
+hipError_t launch_latent_attention(const LatentParams& p, int dtype, int fmt, void* ws, hipStream_t s);
+hipError_t launch_prompt_attention(const PromptParams& p, int dtype, hipStream_t s);
+
 // one-launch decode of one token through one MoE layer or a stack of layers (route, gate/up +
 // SwiGLU, rotate h, down, combine per layer); sync: kDecodeSyncBytes of synchronisation words
 // (zero-filled before the first call), h: decode_stack_h_bytes(inter, top_k) of fp32 h,
