@@ -515,6 +515,7 @@ int gale_add_rms_norm(const void* x, int64_t x_stride, const void* residual, int
 #define GALE_MAX_BLOCK_SIZE 1024
 #define GALE_MAX_REQUESTS  65536
 #define GALE_MAX_HEADS      1024
+#define GALE_MAX_KEY_STRIDE 16777208 /* elements between tokens of k, k_rope and v in the expanded form */
 
 typedef struct {
   void* latent;
@@ -586,7 +587,7 @@ int gale_latent_attention(const gale_latent_cache* cache, const int32_t* block_t
  * k_stride and v_stride apart, of n_heads rows of GALE_HEAD_NOPE and GALE_HEAD_VALUE values, k_head_stride and v_head_stride apart
  * (both may lie in one product's output); k_rope: [n_kv] rows of GALE_LATENT_ROPE; out: [n_tok] tokens of
  * n_heads rows of GALE_HEAD_VALUE; all of dtype (GALE_F16 or GALE_BF16), strides in elements, 16-byte aligned with strides of
- * whole 16 bytes.  lse: fp32 [n_tok][n_heads], or NULL.  q_starts, kv_starts: int32 [n_req + 1], ascending from 0, clamped
+ * whole 16 bytes, those between tokens of k, k_rope and v at most GALE_MAX_KEY_STRIDE.  lse: fp32 [n_tok][n_heads], or NULL.  q_starts, kv_starts: int32 [n_req + 1], ascending from 0, clamped
  * to [0, n_tok] and [0, n_kv]; tokens from q_starts[n_req] on are left as they were. */
 int gale_latent_attention_expanded(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                                    int64_t k_head_stride, const void* k_rope, int64_t k_rope_stride, const void* v,

@@ -3,6 +3,7 @@
 // between host and device; every launch goes on the caller's stream.
 #include <cstdarg>
 #include <cstdio>
+#include <algorithm>
 #include <climits>
 #include <cstring>
 
@@ -1243,7 +1244,8 @@ extern "C" int gale_latent_attention_expanded(const void* q, int64_t q_stride, c
                 vl = (n_heads - 1) * (int64_t)(int32_t)v_head_stride + GALE_HEAD_VALUE;
   if (!attention_sizes_ok(n_tok, n_req, n_heads) || n_kv < 0 || q_stride < ql || out_stride < ol ||
       k_head_stride < GALE_HEAD_NOPE || v_head_stride < GALE_HEAD_VALUE || k_head_stride > INT32_MAX ||
-      v_head_stride > INT32_MAX || k_stride < kl || v_stride < vl || k_rope_stride < GALE_LATENT_ROPE) {
+      v_head_stride > INT32_MAX || k_stride < kl || v_stride < vl || k_rope_stride < GALE_LATENT_ROPE ||
+      std::max({k_stride, v_stride, k_rope_stride}) > GALE_MAX_KEY_STRIDE) {
     set_error("%s: n_tok=%d n_kv=%d n_req=%d n_heads=%d strides %lld (q), %lld, %lld (k), %lld (k_rope), %lld, %lld (v), %lld (out)",
               fn, n_tok, n_kv, n_req, n_heads, (long long)q_stride, (long long)k_stride, (long long)k_head_stride,
               (long long)k_rope_stride, (long long)v_stride, (long long)v_head_stride, (long long)out_stride);

@@ -34,4 +34,108 @@ __device__ __forceinline__ int keys_of(const int32_t* kv_lens, int r, int max_bl
   return (int)min((int64_t)max(kv_lens[r], 0), (int64_t)max_blocks << shift);
 }
 
+// ---------------------------------------------------------------------------
+// Matrix-core pieces.  Both forms compute S^T = K Q^T and O^T = V^T P^T with the 32x32x16 MFMA, 32 queries to a wavefront:
+//   first operand: lane l holds row l % 32, columns 8 (l / 32) .. + 7; second operand alike with its rows as columns;
+//   result register i of lane l: row 8 (i / 4) + 4 (l / 32) + i % 4, column l % 32 (measured with one-hot operands).
+// A query is a lane's column in both products, so its maximum, sum and scale are one register per lane, and eight
+// registers of S^T become an operand of the second product as they are: the order of the keys inside a product of 16 is free
+// as long as V^T has the same one (0-3 and 8-11 for the lower lanes, 4-7 and 12-15 for the upper).  V lies in LDS as rows of keys;
+// ds_read_b64_tr_b16 gives each lane four keys of one column: lane i of 16 addresses 8 bytes, (key i / 4, columns 4 (i % 4) ..),
+// and receives column i of the four keys.
+// ---------------------------------------------------------------------------
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+template <typename T>
+struct Mma;
+template <>
+struct Mma<F16> {
+  typedef _Float16 v8 __attribute__((ext_vector_type(8)));
+  // weights are 2^(s - m + kLift) for a score s and the maximum m that is in use, at most kSlack below the true one; 2^7 puts the
+  // smallest subnormal of fp16 at 2^-31 of the largest weight, and the largest at 2^15
+  static constexpr float kLift = 7.f;
+  static __device__ __forceinline__ f32x16 mma(s16x8 a, s16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ s16x8 pack(const float* v) {
+    v8 r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = (_Float16)v[i];
+    return __builtin_bit_cast(s16x8, r);
+  }
+};
+template <>
+struct Mma<BF16> {
+  typedef __bf16 v8 __attribute__((ext_vector_type(8)));
+  static constexpr float kLift = -8.f;      // weights of at most 1: sums reach no further than the values
+  static __device__ __forceinline__ f32x16 mma(s16x8 a, s16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ s16x8 pack(const float* v) {
+    v8 r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = (__bf16)v[i];
+    return __builtin_bit_cast(s16x8, r);
+  }
+};
+constexpr float kSlack = 8.f;     // sums are rescaled when the maximum has risen by more than 2^8
+
+// Where a row's 16-byte chunk lies: chunk ^ swizzle(row).  Rows are multiples of 256 bytes, so eight rows of one chunk (an
+// operand of K) and four rows of two or four chunks (an operand of V^T) have to part by the swizzle: bits 0-2 differ over eight
+// rows, bits 0-3 over 16, bits 1-2 and 2-3 over four.
+__device__ __forceinline__ int swizzle(int row) {
+  return ((row >> 2) & 1) | (row & 2) | ((row & 1) << 2) | ((((row >> 1) ^ (row >> 3)) & 1) << 3);
+}
+// The same for rows of 128 bytes (eight chunks): eight rows differ, and 16 with the row's place in 256 bytes.
+__device__ __forceinline__ int swizzle8(int row) {
+  return ((row >> 2) & 1) | (row & 2) | (((row ^ (row >> 3)) & 1) << 2);
+}
+
+__device__ __forceinline__ s16x8 lds_operand(const lds_u8* p) { return *(const __attribute__((address_space(3))) s16x8*)p; }
+__device__ __forceinline__ s16x4 lds_transposed(const lds_u8* p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
+}
+
+// The other half's value of a lane's column.
+__device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32); }
+
+// Copies into LDS that a wavefront has issued have landed, its reads are done, and so are the others'.
+__device__ __forceinline__ void tiles_ready() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// Bits that are set where one of a word's two 16-bit numbers is an infinity or a NaN.
+template <typename T>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+  constexpr uint32_t kExp = __is_same(T, F16) ? 0x7C007C00u : 0x7F807F80u, kOne = __is_same(T, F16) ? 0x04000400u : 0x00800080u;
+  return ((w & kExp) + kOne) & 0x80008000u;
+}
+// The same numbers with zeros in those places.
+template <typename T>
+__device__ __forceinline__ s16x8 finite_only(s16x8 v) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  u32x4 w = __builtin_bit_cast(u32x4, v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t b = not_finite<T>(w[i]);
+    w[i] &= ~((b - (b >> 15)) | b);            // 0x8000 -> 0xFFFF in each half
+  }
+  return __builtin_bit_cast(s16x8, w);
+}
+
+// Eight 16-bit numbers times the sign of a scale, or times 0: with it, scores are scaled by |scale| (1 for 0).
+template <typename T>
+__device__ __forceinline__ s16x8 signed_query(s16x8 v, float scale) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  u32x4 w = __builtin_bit_cast(u32x4, v);
+  const uint32_t sign = scale < 0.f ? 0x80008000u : 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t odd = not_finite<T>(w[i]);
+    w[i] = scale == 0.f ? odd - (odd >> 15) : w[i] ^ sign;      // 0 times infinity or NaN: 0x7FFF, a NaN
+  }
+  return __builtin_bit_cast(s16x8, w);
+}
+
 }  // namespace gale

@@ -1,68 +1,265 @@
 // Latent attention of prompts, expanded form.
+#include <type_traits>
+
 #include "gale_latent.h"
 
 namespace gale {
 
-constexpr int kNope = GALE_HEAD_NOPE, kValue = GALE_HEAD_VALUE;
+constexpr int kNope = GALE_HEAD_NOPE, kValue = GALE_HEAD_VALUE, kQuery = kNope + kRope;
 
-// A workgroup per query (token and head): scores of 256 keys at a time, one thread each, then the 128 sums over those keys.
-template <typename T>
-__global__ void __launch_bounds__(256) prompt_simple_kernel(const PromptParams p) {
-  __shared__ int part[4];
-  __shared__ float fpart[4], x[(kNope + kRope)], w[256];
-  const int tid = threadIdx.x, t = (int)(blockIdx.x / (unsigned)p.n_heads), h = (int)(blockIdx.x % (unsigned)p.n_heads);
-  const int r = request_of(p.q_starts, p.n_req, p.n_tok, t, part);
-  if (r == p.n_req) return;
-  const int q0 = start_at(p.q_starts, r, p.n_tok), n = start_at(p.q_starts, r + 1, p.n_tok) - q0;
-  const int k0 = start_at(p.kv_starts, r, p.n_kv), keys = max(0, start_at(p.kv_starts, r + 1, p.n_kv) - k0);
-  const int seen = p.causal ? max(0, min(keys, keys - n + (t - q0) + 1)) : keys;
-  for (int d = tid; d < (kNope + kRope); d += 256) x[d] = T::to_f32(p.q[t * p.q_stride + (int64_t)h * (kNope + kRope) + d]);
-  float m = -INFINITY, l = 0.f, o[kValue / 128] = {};
-  __syncthreads();
-  for (int j0 = 0; j0 < seen; j0 += 256) {
-    const int j = j0 + tid;
-    float s = -INFINITY;
-    if (j < seen) {
-      const uint16_t* k = p.k + (k0 + j) * p.k_stride + h * p.k_head;
-      const uint16_t* kr = p.kr + (k0 + j) * p.kr_stride;
-      float sum = 0.f;
-      for (int d = 0; d < kNope; ++d) sum += x[d] * T::to_f32(k[d]);
-      for (int d = 0; d < kRope; ++d) sum += x[kNope + d] * T::to_f32(kr[d]);
-      s = sum * p.scale;
-    }
-    float top = s;
-    for (int d = 32; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-    if ((tid & 63) == 0) fpart[tid >> 6] = top;
-    __syncthreads();
-    top = fmaxf(m, fmaxf(fmaxf(fpart[0], fpart[1]), fmaxf(fpart[2], fpart[3])));
-    const float ref = top == -INFINITY ? 0.f : top, back = m == -INFINITY ? 0.f : expf(m - ref);
-    const float e = s == -INFINITY ? 0.f : expf(s - ref);
-    w[tid] = e;
-    float sum = e;
-    for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
-    __syncthreads();
-    if ((tid & 63) == 0) fpart[tid >> 6] = sum;
-    __syncthreads();
-    l = l * back + fpart[0] + fpart[1] + fpart[2] + fpart[3];
-    m = top;
-    for (int i = 0; i < kValue / 128; ++i) o[i] *= back;
-    for (int i = 0; i < min(256, seen - j0); ++i) {
-      const float e2 = w[i];
-      if (e2 == 0.f) continue;
-      if (tid < kValue) o[0] += e2 * T::to_f32(p.v[(k0 + j0 + i) * p.v_stride + h * p.v_head + tid]);
+// A workgroup takes 128 queries of one head, 32 to each wavefront, and walks the keys in tiles of 64 with a running maximum
+// and sum.  The tiles (keys' own parts, rope rows, values: 40 KB) come by direct copies into two LDS buffers, the next one's
+// during the products of this one, so two workgroups share a CU and one's softmax runs beside the other's products.
+constexpr int kBq = 128, kBk = 64;
+constexpr int kTileK = kBk * 256, kTileR = kBk * 128, kTileV = kBk * 256, kTile = kTileK + kTileR + kTileV;
+
+// (request, its first block) of block number `idx` of the batch's blocks of kBq queries; n_req if there is none.
+__device__ __forceinline__ void find_block(const int32_t* starts, int n_req, int n_tok, int idx, int* part, int& req, int& first) {
+  req = n_req;
+  first = 0;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int r0 = 0; r0 < n_req; r0 += 256) {
+    const int r = r0 + (int)threadIdx.x;
+    int n = 0;
+    if (r < n_req) n = (max(0, start_at(starts, r + 1, n_tok) - start_at(starts, r, n_tok)) + kBq - 1) / kBq;
+    int sum = n;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int u = __shfl_up(sum, d);
+      if (lane >= d) sum += u;
     }
     __syncthreads();
+    if (lane == 63) part[wave] = sum;
+    if (threadIdx.x == 0) part[4] = -1;
+    __syncthreads();
+    sum += first;
+    for (int w = 0; w < wave; ++w) sum += part[w];
+    if (n > 0 && sum - n <= idx && idx < sum) {
+      part[4] = r;
+      part[5] = sum - n;
+    }
+    __syncthreads();
+    if (part[4] >= 0) {
+      req = part[4];
+      first = part[5];
+      return;
+    }
+    first += part[0] + part[1] + part[2] + part[3];
   }
-  if (tid < kValue) p.out[t * p.out_stride + (int64_t)h * kValue + tid] = T::from_f32(l == 0.f ? 0.f : o[0] / l);
-  if (tid == 0 && p.lse) p.lse[(int64_t)t * p.n_heads + h] = l == 0.f ? -INFINITY : m + logf(l);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256, 2) prompt_kernel(const PromptParams p, int n_blocks) {
+#if defined(__HIP_DEVICE_COMPILE__)   // buffer resources are a device type: the host pass needs the kernel's name only
+  __shared__ __attribute__((aligned(1024))) uint8_t tiles[2 * kTile];
+  const int tid = threadIdx.x, lane = tid & 63, col = lane & 31, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+  // Workgroups go round robin over the 8 XCDs: each XCD gets a contiguous run of (head, block), so the blocks that read
+  // one head's keys share an L2; within a head the blocks with the most keys come first.
+  const int total = n_blocks * p.n_heads, per = total >> 3, rest = total & 7;
+  const int xcd = blockIdx.x & 7, item = xcd * per + min(xcd, rest) + (int)(blockIdx.x >> 3);
+  const int head = item / n_blocks, idx = n_blocks - 1 - (item - head * n_blocks);
+  int req, first;
+  find_block(p.q_starts, p.n_req, p.n_tok, idx, (int*)tiles, req, first);     // two buffers are all of half a CU's LDS
+  if (req == p.n_req) return;
+  __syncthreads();
+  req = __builtin_amdgcn_readfirstlane(req);
+  const int q0 = start_at(p.q_starts, req, p.n_tok), n = start_at(p.q_starts, req + 1, p.n_tok) - q0;
+  const int k0 = start_at(p.kv_starts, req, p.n_kv), keys = max(0, start_at(p.kv_starts, req + 1, p.n_kv) - k0);
+  const int b0 = __builtin_amdgcn_readfirstlane((idx - first) * kBq);
+  const int qi = b0 + 32 * wave + col;                        // this lane's query
+  const int gap = keys - n;
+  const int seen = qi >= n ? 0 : p.causal ? max(0, min(keys, gap + qi + 1)) : keys;
+  // keys that the workgroup, and this wavefront, look at; keys that all of the wavefront's queries see
+  const int last = min(n, b0 + kBq) - 1, wlast = min(n, b0 + 32 * wave + 32) - 1, wfirst = b0 + 32 * wave;
+  const int wg_keys = __builtin_amdgcn_readfirstlane(p.causal ? max(0, min(keys, gap + last + 1)) : keys);
+  const int w_keys = __builtin_amdgcn_readfirstlane(wfirst >= n ? 0 : p.causal ? max(0, min(keys, gap + wlast + 1)) : keys);
+  const int w_all = __builtin_amdgcn_readfirstlane(wfirst >= n ? 0 : p.causal ? max(0, min(keys, gap + wfirst + 1)) : keys);
+
+  // copies: 1 KB of consecutive LDS places, lane l the place 16 l; wavefront w takes the copies 4 j + w
+  lds_u8* smem = (lds_u8*)tiles;
+  const int kr = 4 * wave + (lane >> 4), rr = 8 * wave + (lane >> 3);      // first row of this lane: + 16 j, + 32 j
+  const int kb = (int)(2 * p.k_stride), vb = (int)(2 * p.v_stride), rb = (int)(2 * p.kr_stride);   // the host keeps 64 rows in 32 bits
+  const int vk = kr * kb + 16 * ((lane & 15) ^ swizzle(kr)), vv = kr * vb + 16 * ((lane & 15) ^ swizzle(kr));
+  const int vr = rr * rb + 16 * ((lane & 7) ^ swizzle8(rr));
+  auto copy = [&](int j0, lds_u8* to) {
+    const int rows = min(kBk, keys - j0);      // rows behind the last key come as zeros
+    const auto rk = __builtin_amdgcn_make_buffer_rsrc((void*)(p.k + (int64_t)(k0 + j0) * p.k_stride + head * p.k_head), 0,
+                                                      (rows - 1) * kb + 256, 0x00020000);
+    const auto rv = __builtin_amdgcn_make_buffer_rsrc((void*)(p.v + (int64_t)(k0 + j0) * p.v_stride + head * p.v_head), 0,
+                                                      (rows - 1) * vb + 256, 0x00020000);
+    const auto rp = __builtin_amdgcn_make_buffer_rsrc((void*)(p.kr + (int64_t)(k0 + j0) * p.kr_stride), 0,
+                                                      (rows - 1) * rb + 128, 0x00020000);
+    typedef __attribute__((address_space(3))) void* lds_ptr;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rk, (lds_ptr)(to + 1024 * (4 * j + wave)), 16, vk, 16 * j * kb, 0, 0);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rp, (lds_ptr)(to + kTileK + 1024 * (4 * j + wave)), 16, vr, 32 * j * rb, 0, 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (lds_ptr)(to + kTileK + kTileR + 1024 * (4 * j + wave)), 16, vv, 16 * j * vb, 0, 0);
+  };
+
+  // this lane's query: 12 operands of 16 columns
+  s16x8 xq[12];
+  {
+    const int64_t t = q0 + min(qi, n - 1);
+    const uint16_t* src = p.q + t * p.q_stride + (int64_t)head * kQuery + 8 * half;
+#pragma unroll
+    for (int s = 0; s < 12; ++s) xq[s] = signed_query<T>(*reinterpret_cast<const s16x8*>(src + 16 * s), p.scale);
+  }
+  const float c = p.scale == 0.f ? 1.f : fabsf(p.scale) * 1.44269504088896341f;
+  if (wg_keys > 0) copy(0, smem);
+
+  // LDS places of operands
+  const int zk = swizzle(col), zr = swizzle8(col);
+  int ak[8], ar[4], av[2][4];
+#pragma unroll
+  for (int s = 0; s < 8; ++s) ak[s] = col * 256 + (((2 * s + half) ^ zk) << 4);
+#pragma unroll
+  for (int s = 0; s < 4; ++s) ar[s] = kTileK + col * 128 + (((2 * s + half) ^ zr) << 4);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int row = 8 * u + 4 * half + ((lane & 15) >> 2);
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+      av[u][b] = kTileK + kTileR + row * 256 + (((4 * b + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ swizzle(row)) << 4) + 8 * (lane & 1);
+  }
+
+  int next = kTile;        // where the next tile goes; this one is at kTile - next, and the operands' places move with it
+  f32x16 o[4] = {};
+  float m = -INFINITY, l = 0.f;
+
+  auto tile = [&](int j0, const lds_u8* at) __attribute__((always_inline)) {
+    f32x16 s[2] = {};
+#pragma unroll
+    for (int k = 0; k < 12; ++k)
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const s16x8 a = k < 8 ? lds_operand(at + ak[k & 7] + g * 32 * 256) : lds_operand(at + ar[k & 3] + g * 32 * 128);
+        s[g] = Mma<T>::mma(a, xq[k], s[g]);
+      }
+    const bool masked = j0 + kBk > w_all;
+    if (masked) {
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (j0 + 32 * g + 8 * (i >> 2) + 4 * half + (i & 3) >= seen) s[g][i] = -INFINITY;
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, s[g][i]);
+    top = fmaxf(top, other_half(top)) * c;
+    if (__any(top > m + kSlack)) {
+      const float up = fmaxf(m, top), back = m == up ? 1.f : __builtin_amdgcn_exp2f(m - up);
+#pragma unroll
+      for (int b = 0; b < 4; ++b) o[b] *= back;
+      l *= back;
+      m = up;
+    }
+    const float ref = (m == -INFINITY ? 0.f : m) - Mma<T>::kLift;
+    s16x8 pt[4];
+    float sum = 0.f;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      float w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        w[i] = __builtin_amdgcn_exp2f(fmaf(s[t >> 1][8 * (t & 1) + i], c, -ref));
+        sum += w[i];
+      }
+      pt[t] = Mma<T>::pack(w);
+    }
+    l += sum;
+    auto values = [&](auto clean) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const s16x4 lo = lds_transposed(at + av[0][b] + t * 16 * 256), hi = lds_transposed(at + av[1][b] + t * 16 * 256);
+          s16x8 a = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+          if constexpr (clean.value) a = finite_only<T>(a);
+          o[b] = Mma<T>::mma(a, pt[t], o[b]);
+          if constexpr (clean.value) __builtin_amdgcn_sched_barrier(0);      // the rare way takes no more registers
+        }
+      }
+    };
+    // A product takes the weight 0 of a key that a query does not see times its value, and NaN times 0 is NaN.  So where only some
+    // of the queries see a key, values that are not finite stay out of the product and are added to those that do.
+    uint32_t odd = 0;
+    if (masked && w_all < w_keys) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const mx_u32x4 v = *(const __attribute__((address_space(3))) mx_u32x4*)(at + (kTile - next) + kTileK + kTileR + 1024 * i + 16 * lane);
+        odd |= not_finite<T>(v.x) | not_finite<T>(v.y) | not_finite<T>(v.z) | not_finite<T>(v.w);
+      }
+    }
+    if (__builtin_expect(__any(odd != 0), 0)) {
+      values(std::true_type{});
+      for (int j = 0; j < kBk; ++j) {
+        if (j0 + j >= w_keys) break;
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {          // columns 8 u + 4 half ..
+          const s16x4 v = *(const __attribute__((address_space(3))) s16x4*)(at + (kTile - next) + kTileK + kTileR + j * 256 + ((u ^ swizzle(j)) << 4) + 8 * half);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float f = T::to_f32((uint16_t)v[i]);
+            if (!(fabsf(f) < INFINITY) && j0 + j < seen) o[u >> 2][4 * (u & 3) + i] += f;
+          }
+        }
+      }
+    } else {
+      values(std::false_type{});
+    }
+  };
+
+  for (int j0 = 0; j0 < wg_keys; j0 += kBk) {
+    tiles_ready();
+    if (j0 + kBk < wg_keys) copy(j0 + kBk, smem + next);
+    if (j0 < w_keys) tile(j0, smem);
+    const int move = 2 * next - kTile;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      ak[i] += move;
+      av[i & 1][i >> 1] += move;
+      if (i < 4) ar[i] += move;
+    }
+    next = kTile - next;
+  }
+
+  l += other_half(l);
+  if (qi < n) {
+    const int64_t t = q0 + qi;
+    const float r = l == 0.f ? 0.f : 1.f / l;
+    uint16_t* out = p.out + t * p.out_stride + (int64_t)head * kValue + 4 * half;
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        mx_u32x2 v;
+        v.x = (uint32_t)T::from_f32(o[b][4 * i] * r) | ((uint32_t)T::from_f32(o[b][4 * i + 1] * r) << 16);
+        v.y = (uint32_t)T::from_f32(o[b][4 * i + 2] * r) | ((uint32_t)T::from_f32(o[b][4 * i + 3] * r) << 16);
+        *reinterpret_cast<mx_u32x2*>(out + 32 * b + 8 * i) = v;
+      }
+    if (half == 0 && p.lse)
+      p.lse[t * p.n_heads + head] = l == 0.f ? -INFINITY : (m - Mma<T>::kLift + __builtin_amdgcn_logf(l)) * 0.693147180559945309f;
+  }
+#endif
 }
 
 hipError_t launch_prompt_attention(const PromptParams& p, int dtype, hipStream_t s) {
-  auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)(p.n_tok * p.n_heads)), dim3(256), 0, s, p);
-    return hipGetLastError();
-  };
-  return dtype == GALE_F16 ? go(prompt_simple_kernel<F16>) : go(prompt_simple_kernel<BF16>);
+  // every request has at most one block more than its share of the tokens
+  const int64_t blocks = std::min<int64_t>(((int64_t)p.n_tok + kBq - 1) / kBq + p.n_req - 1, p.n_tok);
+  const dim3 grid((unsigned)(blocks * p.n_heads));
+  if (dtype == GALE_F16) hipLaunchKernelGGL(prompt_kernel<F16>, grid, dim3(256), 0, s, p, (int)blocks);
+  else hipLaunchKernelGGL(prompt_kernel<BF16>, grid, dim3(256), 0, s, p, (int)blocks);
+  return hipGetLastError();
 }
 
 }  // namespace gale

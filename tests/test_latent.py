@@ -167,7 +167,7 @@ def test_expanded_refusals():
         (DTYPE, {10: 2}), (DTYPE, {10: 0}), (SHAPE, {1: 16 * 192 - 1}), (SHAPE, {3: 15 * 256 + 127}), (SHAPE, {4: 127}),
         (SHAPE, {4: 1 << 31}), (SHAPE, {6: 63}), (SHAPE, {8: 15 * 256 + 127}), (SHAPE, {9: 120}), (SHAPE, {9: 1 << 33}), (SHAPE, {11: -1}),
         (SHAPE, {12: -1}), (SHAPE, {13: 0}), (SHAPE, {13: 1025}), (SHAPE, {11: 1 << 28}), (SHAPE, {16: -1}), (SHAPE, {16: 65537}),
-        (SHAPE, {17: float("nan")}), (SHAPE, {20: 16 * 128 - 1}),
+        (SHAPE, {17: float("nan")}), (SHAPE, {20: 16 * 128 - 1}), (SHAPE, {3: 1 << 24}), (SHAPE, {6: 1 << 24}), (SHAPE, {8: 1 << 24}),
         (NULL, {0: None}), (NULL, {2: None}), (NULL, {5: None}), (NULL, {7: None}), (NULL, {14: None}), (NULL, {15: None}),
         (NULL, {19: None}),
         (ALIGN, {0: F + 8}), (ALIGN, {1: 16 * 192 + 4}), (ALIGN, {2: F + MB + 2}), (ALIGN, {3: 4100}), (ALIGN, {4: 257}), (ALIGN, {5: F + 2 * MB + 8}),
