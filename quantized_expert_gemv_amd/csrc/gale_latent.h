@@ -1,5 +1,6 @@
 // Device pieces shared by the kernels of latent attention.
 #pragma once
+#include "gale_lanes.h"
 #include "gale_mx.h"
 
 namespace gale {
@@ -60,6 +61,9 @@ struct Mma<F16> {
   static __device__ __forceinline__ f32x16 mma(s16x8 a, s16x8 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
   }
+  static __device__ __forceinline__ f32x4 mma(s16x8 a, s16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+  }
   static __device__ __forceinline__ s16x8 pack(const float* v) {
     v8 r;
 #pragma unroll
@@ -73,6 +77,9 @@ struct Mma<BF16> {
   static constexpr float kLift = -8.f;      // weights of at most 1: sums reach no further than the values
   static __device__ __forceinline__ f32x16 mma(s16x8 a, s16x8 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ f32x4 mma(s16x8 a, s16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
   }
   static __device__ __forceinline__ s16x8 pack(const float* v) {
     v8 r;
@@ -100,7 +107,14 @@ __device__ __forceinline__ s16x4 lds_transposed(const lds_u8* p) {
 }
 
 // The other half's value of a lane's column.
-__device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32); }
+__device__ __forceinline__ float other_half(float v) { return lane_xor<32>(v); }
+
+// f over the four lanes of a column that the 16x16 MFMA's result has, in every one of them.
+template <typename F>
+__device__ __forceinline__ float over_groups(float v, F f) {
+  v = f(v, lane_xor<16>(v));
+  return f(v, lane_xor<32>(v));
+}
 
 // Copies into LDS that a wavefront has issued have landed, its reads are done, and so are the others'.
 __device__ __forceinline__ void tiles_ready() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
@@ -136,6 +150,24 @@ __device__ __forceinline__ s16x8 signed_query(s16x8 v, float scale) {
     w[i] = scale == 0.f ? odd - (odd >> 15) : w[i] ^ sign;      // 0 times infinity or NaN: 0x7FFF, a NaN
   }
   return __builtin_bit_cast(s16x8, w);
+}
+
+// Eight 4-bit elements (the low nibble of the low byte first) times a scale, as 16-bit numbers.
+template <typename T>
+__device__ __forceinline__ mx_u32x4 mx_values8(uint32_t w, float scale) {
+  mx_u32x4 v;
+  if constexpr (__is_same(T, F16)) {
+    v.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 0));
+    v.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 1));
+    v.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 2));
+    v.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, 3));
+  } else {
+    v.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0));
+    v.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1));
+    v.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2));
+    v.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3));
+  }
+  return v;
 }
 
 }  // namespace gale
