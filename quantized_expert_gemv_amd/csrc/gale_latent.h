@@ -5,6 +5,12 @@
 
 namespace gale {
 
+// A value that the compiler takes as new here: what is made of it is not kept in registers over a loop.
+__device__ __forceinline__ int here(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 constexpr int kLat = GALE_LATENT_DIM, kRope = GALE_LATENT_ROPE, kQk = kLat + kRope;
 
 // Entry r of an ascending array of starts, within [0, n].
@@ -55,6 +61,7 @@ struct Mma;
 template <>
 struct Mma<F16> {
   typedef _Float16 v8 __attribute__((ext_vector_type(8)));
+  typedef _Float16 v4 __attribute__((ext_vector_type(4)));
   // weights are 2^(s - m + kLift) for a score s and the maximum m that is in use, at most kSlack below the true one; 2^7 puts the
   // smallest subnormal of fp16 at 2^-31 of the largest weight, and the largest at 2^15
   static constexpr float kLift = 7.f;
@@ -63,6 +70,15 @@ struct Mma<F16> {
   }
   static __device__ __forceinline__ f32x4 mma(s16x8 a, s16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ f32x4 mma4(s16x4 a, s16x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x16f16(__builtin_bit_cast(v4, a), __builtin_bit_cast(v4, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ s16x4 pack4(const float* v) {
+    v4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = (_Float16)v[i];
+    return __builtin_bit_cast(s16x4, r);
   }
   static __device__ __forceinline__ s16x8 pack(const float* v) {
     v8 r;
@@ -74,12 +90,22 @@ struct Mma<F16> {
 template <>
 struct Mma<BF16> {
   typedef __bf16 v8 __attribute__((ext_vector_type(8)));
+  typedef __bf16 v4 __attribute__((ext_vector_type(4)));
   static constexpr float kLift = -8.f;      // weights of at most 1: sums reach no further than the values
   static __device__ __forceinline__ f32x16 mma(s16x8 a, s16x8 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
   }
   static __device__ __forceinline__ f32x4 mma(s16x8 a, s16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ f32x4 mma4(s16x4 a, s16x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ s16x4 pack4(const float* v) {
+    v4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = (__bf16)v[i];
+    return __builtin_bit_cast(s16x4, r);
   }
   static __device__ __forceinline__ s16x8 pack(const float* v) {
     v8 r;
@@ -101,6 +127,7 @@ __device__ __forceinline__ int swizzle8(int row) {
   return ((row >> 2) & 1) | (row & 2) | (((row ^ (row >> 3)) & 1) << 2);
 }
 
+__device__ __forceinline__ const lds_u8* lds_at(uint32_t place) { return (const lds_u8*)place; }
 __device__ __forceinline__ s16x8 lds_operand(const lds_u8* p) { return *(const __attribute__((address_space(3))) s16x8*)p; }
 __device__ __forceinline__ s16x4 lds_transposed(const lds_u8* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
@@ -108,13 +135,6 @@ __device__ __forceinline__ s16x4 lds_transposed(const lds_u8* p) {
 
 // The other half's value of a lane's column.
 __device__ __forceinline__ float other_half(float v) { return lane_xor<32>(v); }
-
-// f over the four lanes of a column that the 16x16 MFMA's result has, in every one of them.
-template <typename F>
-__device__ __forceinline__ float over_groups(float v, F f) {
-  v = f(v, lane_xor<16>(v));
-  return f(v, lane_xor<32>(v));
-}
 
 // Copies into LDS that a wavefront has issued have landed, its reads are done, and so are the others'.
 __device__ __forceinline__ void tiles_ready() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }

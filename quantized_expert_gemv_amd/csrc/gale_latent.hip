@@ -6,174 +6,219 @@
 
 namespace gale {
 
-// The queries of a request are its tokens' heads, token by token; a run is 16 RG of them against all of the request's keys.
-// A workgroup of W wavefronts has RG row groups of 16 queries and KG = W / RG key groups: wavefront (rg, kg) walks every KG-th
-// tile of 32 keys with its own running maximum and sums, which are joined at the end of the run.  A wavefront keeps its
-// queries (72 registers) and its sums (128) to itself, and a tile (32 KB of latents, 4 KB of rope rows) is read from LDS
-// twice: as K by rows and, transposed by the read, as V.  That is a 1 KB operand for each MFMA of 16 cycles: many rows
-// are bound by the LDS, few by HBM.
+// The queries of a request are its tokens' heads, token by token; a run is Q RG of them against all of the request's keys.
+// A workgroup of four wavefronts has RG row groups of Q queries and KG = 4 / RG key groups: wavefront (rg, kg) walks every KG-th
+// tile of keys with its own running maximum and sums, which are joined at the end of the run.  A wavefront keeps its queries
+// and sums to itself, and a tile is read from LDS twice: as K by rows and, transposed by the read, as V.
 //
 // S^T = K Q^T and O^T = V^T P^T with the 16x16x32 MFMA: first operand: lane l holds row l % 16, columns 8 (l / 16) .. + 7, second
-// alike; result register i of lane l: row 4 (l / 16) + i, column l % 16.  So the weights of keys 4 g .. 4 g + 3 and 16 + 4 g .. of
-// a tile's two halves are lane group g's operand of the second product as they are, and V^T takes the same keys.
+// alike; result register i of lane l: row 4 (l / 16) + i, column l % 16.  So a query is a lane's column in both, and the weights
+// are an operand of the second product as they are, where V^T takes the keys in the same order.
+//   Up to 16 rows: four key groups, tiles of 16 keys (V by the 16x16x16 MFMA), two for each wavefront, which no other one reads:
+//     no barrier; bound by HBM.
+//   Up to 32 and 64: tiles of 32 keys for two and four row groups of 16.  Each MFMA of 16 cycles takes a 1 KB operand from LDS, twice
+//     its bandwidth, so the LDS is the bound once there are more rows than HBM's.
+//   More: eight wavefronts, two to a SIMD, four row groups of 32 queries: two MFMAs for each operand.  Queries (144 registers) and sums
+//     (256) of 32 do not fit one wavefront (300 to 580 registers spilled, also with half of the queries in LDS and with 32x32x16
+//     MFMAs), so two share them: each takes one half of the latent columns in both products, and they add their halves of the
+//     scores through LDS.
 //
 // All runs' tiles form one line, cut into up to kGroups equal parts, one for each workgroup (one to a CU): a run that lies in several
 // parts leaves unnormalised sums in the workspace, two places to a workgroup (a run that began before its part, and one that goes
 // on behind it), and latent_join_kernel adds them in the order of the parts.
 constexpr int kGroups = 256;
-constexpr int kKeys = 32, kTileL = kKeys * 2 * kLat, kTileR = kKeys * 2 * kRope, kTile = kTileL + kTileR;
-constexpr int kScaleArea = 1024;                           // MX: scales of a tile's rows, for each wavefront
-constexpr int kLds = 4 * kTile + 8 * kScaleArea + 1024 + 64;      // and maxima and sums of the wavefronts, a word of each
-constexpr int kRows = 16, kSumBytes = kRows * kLat * 4;    // a row group and its sums
 
-// Wavefronts of a workgroup with RG row groups.  LDS holds four tiles: one for each of four key groups, two for each of two, or four.
-template <int RG>
-constexpr int waves_of() { return RG == 8 ? 8 : 4; }
+template <bool MX, int Q, int RG>
+struct Shape {
+  static constexpr int C = Q / 16, W = 4 * C;                        // wavefronts that share queries, and all of them
+  static constexpr int KG = 4 / RG, KEYS = Q * RG == 16 ? 16 : 32;   // keys of a tile
+  static constexpr int LATENTS = KEYS * 2 * kLat, TILE = LATENTS + KEYS * 2 * kRope;
+  static constexpr int NB = 2;                                       // tiles in LDS of a key group
+  static constexpr int F = W / KG, OWN = KEYS / F;                   // wavefronts that fetch a tile, rows of each,
+  static constexpr int PIECES = KEYS / 8 >= F ? KEYS / 8 / F : 1;    // and KB of rope rows of each, of the first ones
+  static constexpr int UNIT = KG * KEYS;
+  static constexpr int ROWS = Q * RG;
+  // MX, tiles of 16 keys: one of 16-bit numbers, and three of rows as they are in the cache: codes, rope rows, scales (64 places)
+  static constexpr int RAW = KEYS * (kLat / 2) + KEYS * 2 * kRope + 1024, RING = 3;
+  static constexpr int G = Q / 16, BLOCKS = 32 / C;                  // a wavefront's groups of 16 queries, and blocks of 16 columns
+  static constexpr int SUMS = Q * kLat * 4;
+};
+// LDS: tiles; the halves of the scores, parts of the queries, (MX) scales; (MX, tiles of 16 keys) what Shape says; maxima and sums, a word of each wavefront
+constexpr int kScores = 2 * 32 * 1152, kQueries = kScores + 32768, kScales = 4 * 32 * 1152, kStats = 155648, kWords = kStats + 1024, kLds = kWords + 64;
+static_assert(4 * 16 * 1024 + 4 * 3 * Shape<true, 16, 1>::RAW <= kStats && kQueries + 2 * 16384 <= kScales && kScales + 8192 <= kStats && kQueries + 3 * 16384 <= kStats, "what lies in LDS");
 
 struct Run {
   int32_t parts, first, req, block;      // 0 parts: nothing to join
 };
 struct Workspace {
   int32_t* count;                        // runs of the batch
-  Run* runs;                             // by run if there are at most kGroups, else by the workgroup that a run begins in
-  float* stats;                          // [2 kGroups][RG][2][16]: maxima (powers of two), sums of weights
-  float* sums;                           // [2 kGroups][RG][32 blocks of 16 columns][64 lanes] of 4: as a wavefront holds them
+  Run* runs;                             // by run if there are at most kGroups, else by the part that a run begins in
+  float* stats;                          // [2 kGroups][RG][2][Q]: maxima (powers of two), sums of weights
+  float* sums;                           // [2 kGroups][RG][2 Q][64 lanes] of 4: as a wavefront holds them
 };
 
+constexpr int min_of(int a, int b) { return a < b ? a : b; }
 __device__ __forceinline__ int64_t uniform64(int64_t v) {
   const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
   return (int64_t)((uint64_t)hi << 32 | lo);
 }
-
-// Units (KG tiles) of request r's runs: blocks of rows, and units of each.
-template <int RG>
-__device__ __forceinline__ void run_units(const LatentParams& p, int r, int64_t& blocks, int64_t& units) {
-  const int64_t n = max(0, start_at(p.q_starts, r + 1, p.n_tok) - start_at(p.q_starts, r, p.n_tok));
-  const int64_t keys = keys_of(p.kv_lens, r, p.max_blocks, p.block_shift);
-  blocks = (n * p.n_heads + kRows * RG - 1) / (kRows * RG);
-  constexpr int kUnit = kKeys * (waves_of<RG>() / RG);
-  units = max((int64_t)1, (keys + kUnit - 1) / kUnit);
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {      // of numbers that are not negative
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-template <typename T, bool MX, int RG>
-__global__ void __launch_bounds__(64 * waves_of<RG>(), waves_of<RG>() / 4) latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
+// Request r's runs: blocks of rows, and units of each.
+template <typename Sh>
+__device__ __forceinline__ void run_units(const LatentParams& p, int r, int& blocks, int& units) {
+  const int64_t n = max(0, start_at(p.q_starts, r + 1, p.n_tok) - start_at(p.q_starts, r, p.n_tok));
+  const int keys = keys_of(p.kv_lens, r, p.max_blocks, p.block_shift);
+  blocks = (int)((n * p.n_heads + Sh::ROWS - 1) / Sh::ROWS);
+  units = max(1, (int)(((int64_t)keys + Sh::UNIT - 1) / Sh::UNIT));
+}
+
+template <typename T, bool MX, int Q, int RG>
+__global__ void __launch_bounds__(16 * Q) __attribute__((amdgpu_waves_per_eu(Q / 16, Q / 16)))      // 64 W threads, C wavefronts to a SIMD
+latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
 #if defined(__HIP_DEVICE_COMPILE__)   // buffer resources are a device type: the host pass needs the kernel's name only
-  constexpr int W = waves_of<RG>(), KG = W / RG, NB = 4 / KG;
-  constexpr int OWN = kKeys / RG, PIECES = RG <= 4 ? 4 / RG : 1;      // rows, and KB of rope rows, that a wavefront fetches
+  typedef Shape<MX, Q, RG> Sh;
+  constexpr int C = Sh::C, W = Sh::W, G = Sh::G, KG = Sh::KG, KEYS = Sh::KEYS, NB = Sh::NB, F = Sh::F, OWN = Sh::OWN;
+  constexpr int PIECES = Sh::PIECES, BLOCKS = Sh::BLOCKS, QB = 18 / C, AHEAD = C == 1 ? 8 : 4, AHEAD_K = C == 1 ? 8 : 2;      // QB: blocks of 32 columns of the queries
+  constexpr int QL = C == 1 ? 0 : MX ? 2 : 3;      // of them blocks 2, 5, 8 lie in LDS: as many as there is room for
+  constexpr bool RAW = MX && KEYS == 16;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem_raw[];
   lds_u8* smem = (lds_u8*)smem_raw;
   typedef __attribute__((address_space(3))) float lds_f32;
   typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
+  typedef __attribute__((address_space(3))) mx_u32x4 lds_u32x4;
+  typedef __attribute__((address_space(3))) uint32_t lds_u32;
+  typedef __attribute__((address_space(3))) void* lds_ptr;
   const int tid = threadIdx.x, lane = tid & 63, col = lane & 15, grp = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), rg = wave % RG, kg = wave / RG;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), rg = wave % RG, kg = C == 1 ? wave / RG : 0;
+  const int ch = C == 1 ? 0 : wave / RG, f = C == 1 ? rg : wave;      // half of the columns; place among those that fetch a tile
 
   // ---- this workgroup's part of the line of units --------------------------------------------------------------------
-  int64_t u, u_end, base, total;      // base: the first unit of request req
-  int req, run_base, groups;          // run_base: runs before request req; groups: parts that the line is cut into
+  int64_t u, u_end, base, part_units;      // base: the first unit of request req
+  int req, run_base;                       // run_base: runs before request req
   {
-    __shared__ int64_t part[W], found_base;
-    __shared__ int parts_runs[W], found[2];
+    int64_t* const part = (int64_t*)smem_raw;
+    int* const runs_of = (int*)(smem_raw + 64);
+    int* const found = (int*)(smem_raw + 128);
     const int per = (p.n_req + 64 * W - 1) / (64 * W), r0 = min(tid * per, p.n_req), r1 = min(r0 + per, p.n_req);
     int64_t sum = 0;
-    int runs = 0;
+    int runs = 0, b = 0, n = 0;
     for (int r = r0; r < r1; ++r) {
-      int64_t b, n;
-      run_units<RG>(p, r, b, n);
-      sum += b * n;
-      runs += (int)b;
+      run_units<Sh>(p, r, b, n);
+      sum += (int64_t)b * n;
+      runs += b;
     }
     int64_t scan = sum;
     int rscan = runs;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-      const int64_t a = __shfl_up(scan, d);
-      const int b = __shfl_up(rscan, d);
-      if (lane >= d) scan += a, rscan += b;
+      const int64_t x = __shfl_up(scan, d);
+      const int y = __shfl_up(rscan, d);
+      if (lane >= d) scan += x, rscan += y;
     }
-    if (lane == 63) part[tid >> 6] = scan, parts_runs[tid >> 6] = rscan;
+    if (lane == 63) part[wave] = scan, runs_of[wave] = rscan;
     __syncthreads();
-    total = 0;
+    int64_t total = 0;
     int total_runs = 0;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      if (w < (tid >> 6)) scan += part[w], rscan += parts_runs[w];
+      if (w < wave) scan += part[w], rscan += runs_of[w];
       total += part[w];
-      total_runs += parts_runs[w];
+      total_runs += runs_of[w];
     }
     if (tid == 0) {
       if (!by_run) ws.runs[blockIdx.x].parts = 0;
       if (blockIdx.x == 0) *ws.count = by_run ? total_runs : kGroups;
     }
-    groups = (int)min((int64_t)kGroups, total);
-    if ((int)blockIdx.x >= groups) return;
-    u = (int64_t)blockIdx.x * total / groups;
-    u_end = (int64_t)(blockIdx.x + 1) * total / groups;
+    total = uniform64(total);
+    part_units = (total + kGroups - 1) / kGroups;
+    u = (int64_t)blockIdx.x * part_units;
+    u_end = min(total, u + part_units);
+    if (u >= u_end) return;
     scan -= sum;
     rscan -= runs;
     if (sum > 0 && scan <= u && u < scan + sum) {
       for (int r = r0; r < r1; ++r) {
-        int64_t b, n;
-        run_units<RG>(p, r, b, n);
-        if (u < scan + b * n) {
+        if (per > 1) run_units<Sh>(p, r, b, n);
+        const int64_t mine = (int64_t)b * n;
+        if (u < scan + mine) {
           found[0] = r;
           found[1] = rscan;
-          found_base = scan;
+          *(int64_t*)(found + 2) = scan;
           break;
         }
-        scan += b * n;
-        rscan += (int)b;
+        scan += mine;
+        rscan += b;
       }
     }
     __syncthreads();
     req = __builtin_amdgcn_readfirstlane(found[0]);
     run_base = __builtin_amdgcn_readfirstlane(found[1]);
-    base = uniform64(found_base);
-    total = uniform64(total);
-    u = (int64_t)blockIdx.x * total / groups;
-    u_end = (int64_t)(blockIdx.x + 1) * total / groups;
+    base = uniform64(*(int64_t*)(found + 2));
+    __syncthreads();      // the tiles take the place
   }
-  auto owner = [&](int64_t unit) { return (int)(((unit + 1) * groups - 1) / total); };      // the workgroup of a unit
 
   // ---- LDS places of operands ------------------------------------------------------------------------------------------
-  lds_u8* const tiles = smem + kg * NB * kTile;
-  lds_u8* const scale_area = smem + 4 * kTile + wave * kScaleArea;
-  lds_f32* const stats = (lds_f32*)(smem + 4 * kTile + 8 * kScaleArea);
-  // K, column block s of 32: chunk 4 s + grp of row col (+ 16); its low four bits change with s & 3
-  const int zk = swizzle(col), zr = swizzle8(col), vrow = 4 * grp + (col >> 2);
-  int ak[4], ar[2], av[8];
-#pragma unroll
-  for (int s = 0; s < 4; ++s) ak[s] = col * 1024 + (((4 * s + grp) ^ zk) << 4);
-#pragma unroll
-  for (int s = 0; s < 2; ++s) ar[s] = kTileL + col * 128 + (((4 * s + grp) ^ zr) << 4);
-  // V^T, column block b of 16: chunks 2 b, 2 b + 1 of rows vrow (+ 16)
-#pragma unroll
-  for (int b = 0; b < 8; ++b) av[b] = vrow * 1024 + (((2 * b + ((col & 3) >> 1)) ^ swizzle(vrow)) << 4) + 8 * (col & 1);
+  lds_u8* const tiles = RAW ? smem + wave * Sh::LATENTS : smem + kg * NB * Sh::TILE;
+  lds_u8* const raw = smem + 4 * Sh::LATENTS + wave * Sh::RING * Sh::RAW;      // RAW only
+  lds_u8* const scale_area = smem + kScales + wave * 1024;                      // MX without RAW
+  lds_f32* const stats = (lds_f32*)(smem + kStats);
   const float c = p.scale == 0.f ? 1.f : fabsf(p.scale) * 1.44269504088896341f;
 
-  while (u < u_end) {
+  for (;;) {
     // ---- the next run, or what of it is in this part ---------------------------------------------------------------------
-    int64_t blocks, units;
-    run_units<RG>(p, req, blocks, units);
-    if (u >= base + blocks * units) {      // also requests without queries
-      base += blocks * units;
-      run_base += (int)blocks;
+    int blocks, units;
+    run_units<Sh>(p, req, blocks, units);
+    blocks = __builtin_amdgcn_readfirstlane(blocks);
+    units = __builtin_amdgcn_readfirstlane(units);
+    if (u >= base + (int64_t)blocks * units) {      // also requests without queries
+      base += (int64_t)blocks * units;
+      run_base += blocks;
       ++req;
       continue;
     }
-    const int block = __builtin_amdgcn_readfirstlane((int)((u - base) / units));
-    const int64_t run0 = base + block * units;
-    const int a0 = __builtin_amdgcn_readfirstlane((int)(u - run0)), a1 = __builtin_amdgcn_readfirstlane((int)min(units, u_end - run0));
+    const int block = __builtin_amdgcn_readfirstlane((int)divide(u - base, units));
+    const int64_t run0 = base + (int64_t)block * units;
+    const int a0 = __builtin_amdgcn_readfirstlane((int)(u - run0)), a1 = __builtin_amdgcn_readfirstlane((int)min((int64_t)units, u_end - run0));
     const bool whole = a0 == 0 && a1 == units;
     const int q0 = start_at(p.q_starts, req, p.n_tok), n = start_at(p.q_starts, req + 1, p.n_tok) - q0;
     const int keys = __builtin_amdgcn_readfirstlane(keys_of(p.kv_lens, req, p.max_blocks, p.block_shift));
     const int32_t* const table = p.table + (int64_t)req * p.table_stride;
-    const int64_t row64 = (int64_t)block * (kRows * RG) + kRows * rg + col;
-    const bool real = row64 < (int64_t)n * p.n_heads;
-    const int row = (int)min(row64, (int64_t)n * p.n_heads - 1);
-    int token = row / p.n_heads, head = row - token * p.n_heads;
-    const int seen = !real ? 0 : p.causal ? max(0, min(keys, keys - n + token + 1)) : keys;
-    // keys that any, and that all, of this wavefront's queries see
-    int w_keys = seen, w_all = real ? seen : keys;
+
+    // Lane r of KEYS lanes knows the slot of row r of a tile, -1 where there is no key.
+    auto slots_of = [&](int i) {
+      const int pos = (i * KG + kg) * KEYS + here(lane & (KEYS - 1));
+      return pos >= 0 && pos < keys ? slot_of(table, pos, p.block_shift, p.n_blocks) : -1;
+    };
+    constexpr uint32_t ALL = KEYS == 32 ? 0xFFFFFFFFu : 0xFFFFu;
+    auto keys_in = [&](int slot) { return (uint32_t)__ballot(slot >= 0) & ALL; };
+    int slot = slots_of(a0);
+
+    // this lane's queries
+    const int64_t rows = (int64_t)n * p.n_heads, row0 = (int64_t)block * Sh::ROWS + Q * rg + col;
+    int w_keys = 0, w_all = keys;      // and the keys that any, and that all, of this wavefront's queries see
+    lds_u8* const queries = smem + kQueries + wave * (2048 * QL) + 16 * lane;
+    s16x8 xq[G][QB - QL];      // of the columns in both products, and of the rope part
+    constexpr auto in_lds = [](int s) { return s % 3 == 2 && s / 3 < QL; };
+    constexpr auto in_regs = [](int s) { return s - min_of(QL, (s + 1) / 3); };      // place of a block among those in registers
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const bool real = row0 + 16 * g < rows;
+      const int row = (int)min(row0 + 16 * g, rows - 1), token = row / p.n_heads, head = row - token * p.n_heads;
+      const int seen = p.causal ? max(0, min(keys, keys - n + token + 1)) : keys;
+      w_keys = max(w_keys, real ? seen : 0);
+      w_all = min(w_all, real ? seen : keys);
+      const uint16_t* src = p.q + (int64_t)(q0 + token) * p.q_stride + (int64_t)head * kQk + 8 * grp;
+#pragma unroll
+      for (int s = 0; s < QB; ++s) {
+        const int block = C == 1 ? s : s < 8 ? 8 * ch + s : 16 + ch;
+        const s16x8 v = signed_query<T>(*reinterpret_cast<const s16x8*>(src + 32 * block), p.scale);
+        if (in_lds(s)) *(__attribute__((address_space(3))) s16x8*)(queries + (s / 3) * 2048 + g * 1024) = v;
+        else xq[g][in_regs(s)] = v;
+      }
+    }
 #pragma unroll
     for (int d = 8; d >= 1; d >>= 1) {
       w_keys = max(w_keys, __shfl_xor(w_keys, d));
@@ -181,207 +226,355 @@ __global__ void __launch_bounds__(64 * waves_of<RG>(), waves_of<RG>() / 4) laten
     }
     w_keys = __builtin_amdgcn_readfirstlane(w_keys);
     w_all = __builtin_amdgcn_readfirstlane(w_all);
+    // C = 2: wavefronts meet within a tile, so all take the same ones
+    if (C == 2) w_keys = keys;
     // keys that all queries of the run see, where some see more
     int some = INT_MAX;
     if (p.causal) {
-      const int t0 = (int)((int64_t)block * (kRows * RG) / p.n_heads);
-      const int t1 = (int)((min((int64_t)n * p.n_heads, (int64_t)(block + 1) * (kRows * RG)) - 1) / p.n_heads);
+      const int t0 = (int)((int64_t)block * Sh::ROWS / p.n_heads);
+      const int t1 = (int)((min(rows, (int64_t)(block + 1) * Sh::ROWS) - 1) / p.n_heads);
       if (t0 < t1) some = __builtin_amdgcn_readfirstlane(max(0, keys - n + t0 + 1));
     }
 
-    s16x8 xq[18];
-    {
-      const uint16_t* src = p.q + (int64_t)(q0 + token) * p.q_stride + (int64_t)head * kQk + 8 * grp;
+    // keys that this lane's query g sees: needed in the last tiles only, so it is not kept
+    auto seen_of = [&](int g) {
+      const int64_t q_row = (int64_t)block * Sh::ROWS + Q * rg + 16 * g + here(tid & 15);
+      return q_row >= rows ? 0 : p.causal ? max(0, min(keys, keys - n + (int)q_row / p.n_heads + 1)) : keys;
+    };
+
+    f32x4 o[G][BLOCKS] = {};
+    float m[G], l[G];
 #pragma unroll
-      for (int s = 0; s < 18; ++s) xq[s] = signed_query<T>(*reinterpret_cast<const s16x8*>(src + 32 * s), p.scale);
-    }
-    f32x4 o[32] = {};
-    float m = -INFINITY, l = 0.f;
+    for (int g = 0; g < G; ++g) m[g] = -INFINITY, l[g] = 0.f;
 
     // ---- fetching a tile ---------------------------------------------------------------------------------------------
-    // Lanes r and r + 32 know the slot of row r of a tile, -1 where there is no key.
-    auto slots_of = [&](int tile) {
-      const int pos = tile * kKeys + (lane & 31);
-      return pos >= 0 && pos < keys ? slot_of(table, pos, p.block_shift, p.n_blocks) : -1;
-    };
-    uint32_t codes[MX ? OWN : 1];
-    mx_u32x4 ropes[MX ? PIECES : 1];
+    uint32_t codes[MX && !RAW ? OWN : 1];
+    mx_u32x4 ropes[MX && !RAW ? PIECES : 1];
     // 16-bit rows: straight into LDS, a row for each copy; rows without a key come as zeros (a resource of no bytes), so that
-    // 0 times them is 0.  Their rope rows do not matter: such keys' scores are replaced.
+    // 0 times them is 0.  Their rope rows do not matter: such keys' scores are replaced.  Codes wait in registers, or in LDS.
     auto fetch = [&](int slot, int buf) {
-      typedef __attribute__((address_space(3))) void* lds_ptr;
-      lds_u8* to = tiles + buf * kTile;
+      lds_u8* to = RAW ? raw + buf * Sh::RAW : tiles + buf * Sh::TILE;
+      const int lane = here(tid & 63);
+      if constexpr (RAW) {
 #pragma unroll
-      for (int i = 0; i < OWN; ++i) {
-        const int r = rg * OWN + i, at = __builtin_amdgcn_readlane(slot, r);
-        if constexpr (MX) {
-          const auto rs = __builtin_amdgcn_make_buffer_rsrc((void*)(p.latent + (int64_t)max(at, 0) * (kLat / 2)), 0,
-                                                            at < 0 ? 0 : kLat / 2, 0x00020000);
-          codes[i] = __builtin_amdgcn_raw_buffer_load_b32(rs, 4 * lane, 0, 0);
-        } else {
-          const auto rs = __builtin_amdgcn_make_buffer_rsrc((void*)(p.latent + (int64_t)max(at, 0) * p.latent_bytes), 0,
-                                                            at < 0 ? 0 : 2 * kLat, 0x00020000);
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr)(to + r * 1024), 16, (lane ^ swizzle(r)) << 4, 0, 0, 0);
+        for (int i = 0; i < 4; ++i) {
+          const uint8_t* src = p.latent + (int64_t)max(__shfl(slot, 4 * i + (lane >> 4)), 0) * (kLat / 2) + 16 * (lane & 15);
+          __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src, (lds_ptr)(to + 1024 * i), 16, 0, 0);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) {
+          const int r = f * OWN + i, at = __builtin_amdgcn_readlane(slot, r);
+          const int64_t bytes = MX ? kLat / 2 : p.latent_bytes;
+          const auto rs = __builtin_amdgcn_make_buffer_rsrc((void*)(p.latent + (int64_t)max(at, 0) * bytes), 0,
+                                                            at < 0 ? 0 : MX ? kLat / 2 : 2 * kLat, 0x00020000);
+          if constexpr (MX) codes[i] = __builtin_amdgcn_raw_buffer_load_b32(rs, 4 * lane, 0, 0);
+          else __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr)(to + r * 1024), 16, (lane ^ swizzle(r)) << 4, 0, 0, 0);
         }
       }
 #pragma unroll
       for (int i = 0; i < PIECES; ++i) {
-        if (rg * PIECES + i >= 4) break;
-        const int r = 8 * (rg * PIECES + i) + (lane >> 3);
+        if (f * PIECES + i >= KEYS / 8) break;
+        const int r = 8 * (f * PIECES + i) + (lane >> 3);
         const uint8_t* src = p.rope + (int64_t)max(__shfl(slot, r), 0) * p.rope_bytes + (((lane & 7) ^ swizzle8(r)) << 4);
-        if constexpr (MX) ropes[i] = *reinterpret_cast<const mx_u32x4*>(src);
+        if constexpr (MX && !RAW) ropes[i] = *reinterpret_cast<const mx_u32x4*>(src);
         else
           __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                           (lds_ptr)(to + kTileL + 1024 * (rg * PIECES + i)), 16, 0, 0);
+                                           (lds_ptr)(to + (RAW ? 4096 : Sh::LATENTS) + 1024 * (f * PIECES + i)), 16, 0, 0);
       }
       if constexpr (MX) {
-        const uint8_t* src = p.scales + (int64_t)max(__shfl(slot, rg * OWN + (lane & (OWN - 1))), 0) * (kLat / 32);
-        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src, (lds_ptr)scale_area, 16, 0, 0);
+        const uint8_t* src = p.scales + (int64_t)max(__shfl(slot, f * OWN + (lane & (OWN - 1))), 0) * (kLat / 32);
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                         RAW ? (lds_ptr)(to + 6144) : (lds_ptr)scale_area, 16, 0, 0);
       }
     };
-    // MX rows, a tile later: 4-bit elements to 16-bit numbers, rounded where a scale takes them out of fp16's range.
+    constexpr int COPIES = RAW ? 7 : OWN + PIECES;      // of a fetch into LDS
+    // MX rows, later: 4-bit elements to 16-bit numbers, rounded where a scale takes them out of fp16's range.
     auto store = [&](uint32_t valid, int buf) {
       if constexpr (MX) {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");      // the scales' copy
-        lds_u8* to = tiles + buf * kTile;
+        lds_u8* to = RAW ? tiles : tiles + buf * Sh::TILE;
+        const lds_u8* from = raw + buf * Sh::RAW;
+        const lds_u8* scales = RAW ? from + 6144 : scale_area;
+        const int lane = here(tid & 63);
+        if constexpr (!RAW) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");      // the scales' copy
+        uint32_t scale[OWN], word[OWN];
 #pragma unroll
         for (int i = 0; i < OWN; ++i) {
-          const int r = rg * OWN + i;
-          const uint32_t s = scale_area[16 * i + (lane >> 2)];
-          const float scale = s == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(s ? s << 23 : 0x400000u);
-          mx_u32x4 v = mx_values8<T>(codes[i], scale);
-          if (!(valid >> r & 1u)) v = mx_u32x4{0, 0, 0, 0};
-          *(__attribute__((address_space(3))) mx_u32x4*)(to + r * 1024 + ((lane ^ swizzle(r)) << 4)) = v;
+          scale[i] = scales[16 * i + (lane >> 2)];
+          word[i] = RAW ? *(const lds_u32*)(from + 256 * i + 4 * lane) : codes[RAW ? 0 : i];
         }
+        __builtin_amdgcn_sched_barrier(0);      // all reads first
 #pragma unroll
-        for (int i = 0; i < PIECES; ++i)
-          if (rg * PIECES + i < 4) *(__attribute__((address_space(3))) mx_u32x4*)(to + kTileL + 1024 * (rg * PIECES + i) + 16 * lane) = ropes[i];
+        for (int i = 0; i < OWN; ++i) {
+          const int r = f * OWN + i;
+          const uint32_t keep = 0u - (valid >> r & 1u);      // rows without a key: 0 times 2^-127
+          // 2^(s - 127): 0 is the subnormal 2^-127, 255 NaN
+          const uint32_t x = max(scale[i] << 23 | (scale[i] + 1u) >> 8 << 22, 0x400000u);
+          const mx_u32x4 v = mx_values8<T>(word[i] & keep, __uint_as_float(x & keep));
+          *(lds_u32x4*)(to + r * 1024 + ((lane ^ swizzle(r)) << 4)) = v;
+        }
+        if constexpr (!RAW) {
+#pragma unroll
+          for (int i = 0; i < PIECES; ++i)
+            if (f * PIECES + i < KEYS / 8) *(lds_u32x4*)(to + Sh::LATENTS + 1024 * (f * PIECES + i) + 16 * lane) = ropes[i];
+        }
       }
     };
 
-    // ---- the products with a tile --------------------------------------------------------------------------------------
-    auto use = [&](int j0, uint32_t valid, const lds_u8* at) __attribute__((always_inline)) {
-      f32x4 s[2] = {};
+    // ---- the products with a tile: latents at `at`, rope rows at `rope` ----------------------------------------------------
+    auto use = [&](int j0, uint32_t valid, const lds_u8* at, const lds_u8* rope) __attribute__((always_inline)) {
+      // operands are read AHEAD in front of their products; the scheduler by itself would read each right before
+      constexpr int U = KEYS / 16, NK = QB * U;
+      // LDS places of operands.  K, column block s of 32: chunk 4 s + grp of row col (+ 16); V^T, column block b of 16: chunks 2 b and
+      // 2 b + 1 of rows vrow (+ 16).  A row's swizzle and the block change the same bits 4 .. 7 of a place in a tile, which
+      // starts at a multiple of 256: a block is one exclusive or away.
+      const int lane = here(tid & 63), col = lane & 15, grp = lane >> 4, vrow = 4 * grp + (col >> 2);
+      const uint32_t at_k = (uint32_t)(at + 512 * ch) + col * 1024 + ((grp ^ swizzle(col)) << 4);
+      const uint32_t at_r = (uint32_t)rope + col * 128 + (((4 * ch + grp) ^ swizzle8(col)) << 4);
+      auto key = [&](int k) {
+        const int u = k % U, s = k / U;
+        return s < 16 / C ? lds_operand(lds_at(at_k ^ ((s & 3) << 6)) + (s >> 2) * 256 + u * 16 * 1024)
+                          : lds_operand(lds_at(at_r ^ ((s & 1) << 6)) + u * 16 * 128);
+      };
+      f32x4 s[G][2] = {};      // U = 1: two chains, an MFMA takes longer than its issue
+      {
+        s16x8 a[AHEAD_K], x[G];      // x: the queries' next block from LDS
+        const lds_u8* from = smem + kQueries + wave * (2048 * QL) + 16 * lane;
+        if constexpr (QL > 0) {
 #pragma unroll
-      for (int k = 0; k < 18; ++k)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const s16x8 a = k < 16 ? lds_operand(at + ak[k & 3] + (k >> 2) * 256 + u * 16 * 1024)
-                                 : lds_operand(at + ar[k & 1] + u * 16 * 128);
-          s[u] = Mma<T>::mma(a, xq[k], s[u]);
+          for (int g = 0; g < G; ++g) x[g] = lds_operand(from + g * 1024);
         }
-      if (valid != 0xFFFFFFFFu || j0 + kKeys > w_all) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int k = 0; k < AHEAD_K; ++k) a[k] = key(k);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = 16 * u + 4 * grp + i;
-            if (!(valid >> r & 1u) || j0 + r >= seen) s[u][i] = -INFINITY;
+        for (int k = 0; k < NK; ++k) {
+          __builtin_amdgcn_sched_barrier(0);
+          const int b = k / U;
+#pragma unroll
+          for (int g = 0; g < G; ++g) s[g][k & 1] = Mma<T>::mma(a[k % AHEAD_K], in_lds(b) ? x[g] : xq[g][in_regs(b)], s[g][k & 1]);
+          if (k + AHEAD_K < NK) a[k % AHEAD_K] = key(k + AHEAD_K);
+          if (in_lds(b) && in_lds(b + 3) && k % U == U - 1) {
+#pragma unroll
+            for (int g = 0; g < G; ++g) x[g] = lds_operand(from + (b / 3 + 1) * 2048 + g * 1024);
           }
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
-      float top = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])), fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
-      top = over_groups(top, [](float a, float b) { return fmaxf(a, b); }) * c;
-      if (__any(top > m + kSlack)) {
-        const float up = fmaxf(m, top), back = m == up ? 1.f : __builtin_amdgcn_exp2f(m - up);
+      const uint32_t at_v = (uint32_t)(at + 512 * ch) + vrow * 1024 + ((((col & 3) >> 1) ^ swizzle(vrow)) << 4) + 8 * (col & 1);
+      if constexpr (C == 2) {      // the sum of both halves is the same in both wavefronts, bit for bit
+        lds_f32x4* mine = (lds_f32x4*)(smem + kScores) + wave * 256 + lane;
 #pragma unroll
-        for (int b = 0; b < 32; ++b) o[b] *= back;
-        l *= back;
-        m = up;
-      }
-      const float ref = (m == -INFINITY ? 0.f : m) - Mma<T>::kLift;
-      float e[8], sum = 0.f;
+        for (int i = 0; i < 4; ++i) mine[64 * i] = s[i >> 1][i & 1];
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        const lds_f32x4* other = mine + (ch ? -256 * RG : 256 * RG);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        e[i] = __builtin_amdgcn_exp2f(fmaf(s[i >> 2][i & 3], c, -ref));
-        sum += e[i];
+        for (int i = 0; i < 4; ++i) s[i >> 1][i & 1] += other[64 * i];
       }
-      l += sum;
-      const s16x8 w = Mma<T>::pack(e);
+      if constexpr (U == 1) {
 #pragma unroll
-      for (int b = 0; b < 32; ++b) {
-        const s16x4 lo = lds_transposed(at + av[b & 7] + (b >> 3) * 256);
-        const s16x4 hi = lds_transposed(at + av[b & 7] + (b >> 3) * 256 + 16 * 1024);
-        o[b] = Mma<T>::mma(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), w, o[b]);
+        for (int g = 0; g < G; ++g) s[g][0] += s[g][1];
       }
+      if (valid != ALL || j0 + KEYS > w_all) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const int seen = seen_of(g);
+#pragma unroll
+          for (int i = 0; i < 4 * U; ++i) {
+            const int r = 16 * (i >> 2) + 4 * grp + (i & 3);
+            if (!(valid >> r & 1u) || j0 + r >= seen) s[g][i >> 2][i & 3] = -INFINITY;
+          }
+        }
+      }
+      float top[G];
+      bool rise = false;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        top[g] = s[g][0][0];
+#pragma unroll
+        for (int i = 1; i < 4 * U; ++i) top[g] = fmaxf(top[g], s[g][i >> 2][i & 3]);
+        top[g] = fmaxf(top[g], lane_xor<16>(top[g]));
+        top[g] = fmaxf(top[g], lane_xor<32>(top[g])) * c;
+        rise = rise || top[g] > m[g] + kSlack;
+      }
+      if (__any(rise)) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const float up = fmaxf(m[g], top[g]), back = m[g] == up ? 1.f : __builtin_amdgcn_exp2f(m[g] - up);
+#pragma unroll
+          for (int b = 0; b < BLOCKS; ++b) o[g][b] *= back;
+          l[g] *= back;
+          m[g] = up;
+        }
+      }
+      float e[G][4 * U];
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const float ref = (m[g] == -INFINITY ? 0.f : m[g]) - Mma<T>::kLift;
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4 * U; ++i) {
+          e[g][i] = __builtin_amdgcn_exp2f(fmaf(s[g][i >> 2][i & 3], c, -ref));
+          sum += e[g][i];
+        }
+        l[g] += sum;
+      }
+      if constexpr (U == 1) {
+        s16x4 w[G], a[AHEAD];
+#pragma unroll
+        for (int g = 0; g < G; ++g) w[g] = Mma<T>::pack4(e[g]);
+        auto value = [&](int b) { return lds_transposed(lds_at(at_v ^ ((b & 7) << 5)) + (b >> 3) * 256); };
+#pragma unroll
+        for (int b = 0; b < AHEAD; ++b) a[b] = value(b);
+#pragma unroll
+        for (int b = 0; b < 32; ++b) {
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int g = 0; g < G; ++g) o[g][b] = Mma<T>::mma4(a[b % AHEAD], w[g], o[g][b]);
+          if (b + AHEAD < 32) a[b % AHEAD] = value(b + AHEAD);
+        }
+      } else {
+        s16x8 w[G], a[AHEAD];
+#pragma unroll
+        for (int g = 0; g < G; ++g) w[g] = Mma<T>::pack(e[g]);
+        auto value = [&](int b) {
+          const lds_u8* from = lds_at(at_v ^ ((b & 7) << 5)) + (b >> 3) * 256;
+          return __builtin_shufflevector(lds_transposed(from), lds_transposed(from + 16 * 1024), 0, 1, 2, 3, 4, 5, 6, 7);
+        };
+#pragma unroll
+        for (int b = 0; b < AHEAD; ++b) a[b] = value(b);
+#pragma unroll
+        for (int b = 0; b < BLOCKS; ++b) {
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int g = 0; g < G; ++g) o[g][b] = Mma<T>::mma(a[b % AHEAD], w[g], o[g][b]);
+          if (b + AHEAD < BLOCKS) a[b % AHEAD] = value(b + AHEAD);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
     };
     // A product takes the weight 0 of a key that a query does not see times its value, and NaN times 0 is NaN.  So where only some
     // of the run's queries see a key (j >= some), rows of a tile that are not finite are zeroed by the wavefront that fetched them, and
     // the queries that see such a key have NaN as their sum of weights.
     auto clear = [&](int j0, lds_u8* at) {
       uint32_t bad = 0;
-      for (int r = max(rg * OWN, some - j0); r < (rg + 1) * OWN; ++r) {
-        __attribute__((address_space(3))) mx_u32x4* row16 = (__attribute__((address_space(3))) mx_u32x4*)(at + r * 1024 + 16 * lane);
+      for (int r = max(f * OWN, some - j0); r < (f + 1) * OWN; ++r) {
+        lds_u32x4* row16 = (lds_u32x4*)(at + r * 1024 + 16 * lane);
         const mx_u32x4 v = *row16;
         if (__any((not_finite<T>(v.x) | not_finite<T>(v.y) | not_finite<T>(v.z) | not_finite<T>(v.w)) != 0)) {
           bad |= 1u << r;
           *row16 = mx_u32x4{0, 0, 0, 0};
         }
       }
-      if constexpr (RG > 1) {
-        __attribute__((address_space(3))) uint32_t* words = (__attribute__((address_space(3))) uint32_t*)(stats + 256);
+      if constexpr (F > 1) {
+        lds_u32* words = (lds_u32*)(smem + kWords);
         if (lane == 0) words[wave] = bad;
         tiles_ready();
         bad = 0;
 #pragma unroll
-        for (int g = 0; g < RG; ++g) bad |= words[kg * RG + g];
+        for (int g = 0; g < F; ++g) bad |= words[kg * F + g];
       }
       bad = __builtin_amdgcn_readfirstlane(bad);
       while (bad != 0) {
         const int r = __builtin_ctz(bad);
         bad &= bad - 1;
-        if (j0 + r < seen) l = NAN;
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+          if (j0 + r < seen_of(g)) l[g] = NAN;
       }
     };
 
     // ---- the tiles -----------------------------------------------------------------------------------------------------
-    // valid: which rows of a tile hold keys.  A ballot's two halves are alike.
-    int slot = slots_of(a0 * KG + kg);
-    if constexpr (NB == 1) {
-      if constexpr (MX) fetch(slot, 0);
+    if constexpr (RAW) {
+      // every wavefront by itself, three tiles' rows on the way: a fetch is 7 copies, and what is younger than a tile's is known
+      uint32_t valid[3] = {keys_in(slot), 0, 0};
+      fetch(slot, 0);
+#pragma unroll
+      for (int k = 1; k < 3; ++k)
+        if (a0 + k < a1) {
+          slot = slots_of(a0 + k);
+          valid[k] = keys_in(slot);
+          fetch(slot, k);
+        }
+      // slots are looked up two tiles before their fetch: waiting for a look-up waits for the copies in front of it too
+      slot = a0 + 3 < a1 ? slots_of(a0 + 3) : -1;
+      int slot2 = a0 + 4 < a1 ? slots_of(a0 + 4) : -1;
+      int buf = 0;
       for (int i = a0; i < a1; ++i) {
-        const uint32_t valid = (uint32_t)__ballot(slot >= 0);
+        if (i + 2 < a1) asm volatile("s_waitcnt vmcnt(14) lgkmcnt(0)" ::: "memory");
+        else if (i + 1 < a1) asm volatile("s_waitcnt vmcnt(7) lgkmcnt(0)" ::: "memory");
+        else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        const int j0 = (i * KG + kg) * KEYS;
+        if (j0 < w_keys) {
+          store(valid[0], buf);
+          if (j0 + KEYS > some) clear(j0, tiles);
+          use(j0, valid[0], tiles, raw + buf * Sh::RAW + 4096);
+        }
+        valid[0] = valid[1];
+        valid[1] = valid[2];
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");      // the tile is read
+        if (i + 3 < a1) {
+          valid[2] = keys_in(slot);
+          const int next = i + 5 < a1 ? slots_of(i + 5) : -1;
+          fetch(slot, buf);
+          slot = slot2;
+          slot2 = next;
+        }
+        buf = buf == 2 ? 0 : buf + 1;
+      }
+    } else if constexpr (KEYS == 16) {
+      // every wavefront by itself: the next tile's copies go out before this one's are waited for
+      static_assert(COPIES == 18, "the wait below");
+      uint32_t valid = keys_in(slot);
+      fetch(slot, 0);
+      slot = a0 + 1 < a1 ? slots_of(a0 + 1) : -1;
+      int buf = 0;
+      for (int i = a0; i < a1; ++i) {
+        const uint32_t next_valid = keys_in(slot);
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");      // the tile before is read
-        if constexpr (MX) store(valid, 0);
-        else fetch(slot, 0);
-        slot = i + 1 < a1 ? slots_of((i + 1) * KG + kg) : -1;
-        if constexpr (MX) {
-          if (i + 1 < a1) fetch(slot, 0);
+        if (i + 1 < a1) {
+          const int next = i + 2 < a1 ? slots_of(i + 2) : -1;
+          fetch(slot, buf ^ 1);
+          slot = next;
+          asm volatile("s_waitcnt vmcnt(18)" ::: "memory");
         } else {
           asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         }
-        const int j0 = (i * KG + kg) * kKeys;
-        if (j0 + kKeys > some) clear(j0, tiles);
-        if (j0 < w_keys) use(j0, valid, tiles);
+        const int j0 = (i * KG + kg) * KEYS;
+        lds_u8* at = tiles + buf * Sh::TILE;
+        if (j0 + KEYS > some) clear(j0, at);
+        if (j0 < w_keys) use(j0, valid, at, at + Sh::LATENTS);
+        valid = next_valid;
+        buf ^= 1;
       }
     } else {
-      uint32_t valid = (uint32_t)__ballot(slot >= 0);
+      uint32_t valid = keys_in(slot);
       fetch(slot, 0);
       if constexpr (MX) store(valid, 0);
-      slot = a0 + 1 < a1 ? slots_of((a0 + 1) * KG + kg) : -1;
+      slot = a0 + 1 < a1 ? slots_of(a0 + 1) : -1;
       if constexpr (MX) {
         if (a0 + 1 < a1) fetch(slot, 0);
       }
       int buf = 0;
       for (int i = a0; i < a1; ++i) {
         tiles_ready();
-        const uint32_t next = (uint32_t)__ballot(slot >= 0);
-        const int j0 = (i * KG + kg) * kKeys;
-        lds_u8* at = tiles + buf * kTile;
+        const uint32_t next = keys_in(slot);
+        const int j0 = (i * KG + kg) * KEYS;
+        lds_u8* at = tiles + buf * Sh::TILE;
         buf ^= 1;
-        if ((i + 1) * (KG * kKeys) > some) clear(j0, at);      // the same for all wavefronts
+        if ((i + 1) * Sh::UNIT > some) clear(j0, at);      // the same for all wavefronts
         if constexpr (MX) {
-          if (j0 < w_keys) use(j0, valid, at);
+          if (j0 < w_keys) use(j0, valid, at, at + Sh::LATENTS);
           if (i + 1 < a1) {
             store(next, buf);
-            slot = i + 2 < a1 ? slots_of((i + 2) * KG + kg) : -1;
+            slot = i + 2 < a1 ? slots_of(i + 2) : -1;
             if (i + 2 < a1) fetch(slot, 0);
           }
         } else {
           if (i + 1 < a1) {
             fetch(slot, buf);
-            slot = i + 2 < a1 ? slots_of((i + 2) * KG + kg) : -1;
+            slot = i + 2 < a1 ? slots_of(i + 2) : -1;
           }
-          if (j0 < w_keys) use(j0, valid, at);
+          if (j0 < w_keys) use(j0, valid, at, at + Sh::LATENTS);
         }
         valid = next;
       }
@@ -389,126 +582,136 @@ __global__ void __launch_bounds__(64 * waves_of<RG>(), waves_of<RG>() / 4) laten
 
     // ---- joining the key groups, and what leaves ---------------------------------------------------------------------------
     const int place = a0 == 0 ? 2 * (int)blockIdx.x + 1 : 2 * (int)blockIdx.x;
-    int q_row = row;
-    asm("" : "+v"(q_row));       // addresses of results are made here, not kept over the loop
-    token = q_row / p.n_heads;
-    head = q_row - token * p.n_heads;
-    l = over_groups(l, [](float a, float b) { return a + b; });
-    float top = m;
-    if constexpr (KG > 1) {
-      if (grp == 0) {
-        stats[wave * 32 + col] = m;
-        stats[wave * 32 + 16 + col] = l;
-      }
-      __syncthreads();
-      float lsum = 0.f;
+    const int lane = here(tid & 63), col = lane & 15, grp = lane >> 4;
+    float top[G];
 #pragma unroll
-      for (int k = 0; k < KG; ++k) top = fmaxf(top, stats[(k * RG + rg) * 32 + col]);
-#pragma unroll
-      for (int k = 0; k < KG; ++k) {
-        const float mk = stats[(k * RG + rg) * 32 + col], lk = stats[(k * RG + rg) * 32 + 16 + col];
-        lsum += mk == top ? lk : lk * __builtin_amdgcn_exp2f(mk - top);
-      }
-      l = lsum;
-      const float back = m == top ? 1.f : __builtin_amdgcn_exp2f(m - top);
-#pragma unroll
-      for (int b = 0; b < 32; ++b) o[b] *= back;
+    for (int g = 0; g < G; ++g) {
+      l[g] += lane_xor<16>(l[g]);
+      l[g] += lane_xor<32>(l[g]);
+      top[g] = m[g];
     }
-    const float r = l == 0.f ? 0.f : 1.f / l;
-    uint16_t* out = p.out + (int64_t)(q0 + token) * p.out_stride + (int64_t)head * kLat + 4 * grp;
-    float* sums = ws.sums + ((int64_t)place * RG + rg) * (kRows * kLat) + 4 * lane;
-    // columns 16 b + 4 grp .. of this lane's query
-    auto leave = [&](int b, f32x4 v) {
-      if (whole) {
-        if (real) {
-          mx_u32x2 h;
-          h.x = (uint32_t)T::from_f32(v.x * r) | ((uint32_t)T::from_f32(v.y * r) << 16);
-          h.y = (uint32_t)T::from_f32(v.z * r) | ((uint32_t)T::from_f32(v.w * r) << 16);
-          *reinterpret_cast<mx_u32x2*>(out + 16 * b) = h;
+    if constexpr (KG > 1) {
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        if (grp == 0) {
+          stats[wave * 2 * Q + 16 * g + col] = m[g];
+          stats[wave * 2 * Q + Q + 16 * g + col] = l[g];
         }
-      } else {
-        *reinterpret_cast<f32x4*>(sums + b * 256) = v;
+      __syncthreads();
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const lds_f32* st = stats + 16 * g + col;
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < KG; ++k) top[g] = fmaxf(top[g], st[(k * RG + rg) * 2 * Q]);
+#pragma unroll
+        for (int k = 0; k < KG; ++k) {
+          const float mk = st[(k * RG + rg) * 2 * Q], lk = st[(k * RG + rg) * 2 * Q + Q];
+          sum += mk == top[g] ? lk : lk * __builtin_amdgcn_exp2f(mk - top[g]);
+        }
+        l[g] = sum;
+        const float back = m[g] == top[g] ? 1.f : __builtin_amdgcn_exp2f(m[g] - top[g]);
+#pragma unroll
+        for (int b = 0; b < BLOCKS; ++b) o[g][b] *= back;
       }
-    };
-    if constexpr (KG == 1) {
+    }
+    float* sums = ws.sums + ((int64_t)place * RG + rg) * (Q * kLat) + 4 * lane;
+    float* st = ws.stats + ((int64_t)place * RG + rg) * 2 * Q + col;
 #pragma unroll
-      for (int b = 0; b < 32; ++b) leave(b, o[b]);
-    } else {
-      // 128 KB at a time: all columns of four wavefronts or half of eight; each adds its share of its row group's blocks
-      constexpr int STEP = 128 / W, MINE = STEP / KG;
+    for (int g = 0; g < G; ++g) {
+      const int64_t q_row = here(Q * rg + 16 * g + col) + (int64_t)block * Sh::ROWS;
+      const bool real = q_row < rows;
+      const int row = (int)min(q_row, rows - 1), token = row / p.n_heads, head = row - token * p.n_heads;
+      const float r = l[g] == 0.f ? 0.f : 1.f / l[g];
+      uint16_t* out = p.out + (int64_t)(q0 + token) * p.out_stride + (int64_t)head * kLat + 4 * grp;
+      auto leave = [&](int b, f32x4 v) {      // columns 16 b + 4 grp ..
+        if (whole) {
+          if (real) {
+            mx_u32x2 h;
+            h.x = (uint32_t)T::from_f32(v.x * r) | ((uint32_t)T::from_f32(v.y * r) << 16);
+            h.y = (uint32_t)T::from_f32(v.z * r) | ((uint32_t)T::from_f32(v.w * r) << 16);
+            *reinterpret_cast<mx_u32x2*>(out + 16 * b) = h;
+          }
+        } else {
+          *reinterpret_cast<f32x4*>(sums + (32 * g + b) * 256) = v;
+        }
+      };
+      if constexpr (KG == 1) {
 #pragma unroll
-      for (int t = 0; t < 32 / STEP; ++t) {
+        for (int b = 0; b < BLOCKS; ++b) leave(16 * ch + b, o[g][b]);
+      } else {
+        // 32 KB of every wavefront; each adds its share of its row group's
+        constexpr int MINE = 32 / KG;
         __syncthreads();
 #pragma unroll
-        for (int b = 0; b < STEP; ++b) ((lds_f32x4*)smem)[(wave * STEP + b) * 64 + lane] = o[STEP * t + b];
+        for (int b = 0; b < 32; ++b) ((lds_f32x4*)smem)[(wave * 32 + b) * 64 + lane] = o[g][b % BLOCKS];
         __syncthreads();
 #pragma unroll
         for (int b = 0; b < MINE; ++b) {
           f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int k = 0; k < KG; ++k) v += ((const lds_f32x4*)smem)[((k * RG + rg) * STEP + kg * MINE + b) * 64 + lane];
-          leave(STEP * t + kg * MINE + b, v);
+          for (int k = 0; k < KG; ++k) v += ((const lds_f32x4*)smem)[((k * RG + rg) * 32 + kg * MINE + b) * 64 + lane];
+          leave(kg * MINE + b, v);
+        }
+      }
+      if (kg == 0 && ch == 0 && grp == 0) {
+        if (!whole) {
+          st[16 * g] = top[g];
+          st[Q + 16 * g] = l[g];
+        } else if (real && p.lse) {
+          p.lse[(int64_t)(q0 + token) * p.n_heads + head] =
+              l[g] == 0.f ? -INFINITY : (top[g] - Mma<T>::kLift + __builtin_amdgcn_logf(l[g])) * 0.693147180559945309f;
         }
       }
     }
-    if (kg == 0 && grp == 0) {
-      if (whole) {
-        if (real && p.lse)
-          p.lse[(int64_t)(q0 + token) * p.n_heads + head] =
-              l == 0.f ? -INFINITY : (top - Mma<T>::kLift + __builtin_amdgcn_logf(l)) * 0.693147180559945309f;
-      } else {
-        float* st = ws.stats + ((int64_t)place * RG + rg) * 32;
-        st[col] = top;
-        st[16 + col] = l;
-      }
-    }
     if (a0 == 0 && tid == 0) {
-      const int first = (int)blockIdx.x;
-      const int at = by_run ? run_base + block : first;
+      const int first = (int)blockIdx.x, at = by_run ? run_base + block : first;
       if (at < kGroups)       // always, where q_starts ascends
-        ws.runs[at] = Run{whole ? 0 : owner(run0 + units - 1) - first + 1, first, req, block};
+        ws.runs[at] = Run{whole ? 0 : (int)divide(run0 + units - 1, part_units) - first + 1, first, req, block};
     }
     u = run0 + a1;
+    if (u >= u_end) break;
     __syncthreads();          // the next run writes the tiles
   }
 #endif
 }
 
-// The sums of a run that lies in several parts: a workgroup per row group and 64 columns, four quarters of the parts side by
+// The sums of a run that lies in several parts: a workgroup per row group and four KB of sums, four quarters of the parts side by
 // side.  Every sum goes in the order of the parts, so equal calls give equal bits.
-template <typename T, int RG>
+template <typename T, int Q, int RG>
 __global__ void __launch_bounds__(1024) latent_join_kernel(const LatentParams p, const Workspace ws) {
-  __shared__ float weight[kGroups][kRows], most[64][kRows], sum[64][kRows];
+  constexpr int K0 = 1024 / Q;
+  __shared__ float weight[kGroups][Q], most[K0][Q], sum[K0][Q];
   __shared__ f32x4 part[3][256];
   if ((int)blockIdx.x >= *ws.count) return;
   const Run run = ws.runs[blockIdx.x];
   if (run.parts <= 1) return;
-  const int tid = threadIdx.x, rg = (int)blockIdx.y >> 3;
+  const int tid = threadIdx.x, rg = (int)blockIdx.y / (Q / 2);
   auto place = [&](int k) { return (int64_t)(2 * (run.first + k) + (k == 0)) * RG + rg; };
   float top = -INFINITY;
   {
-    const int row = tid & 15, k0 = tid >> 4;
+    const int row = tid & (Q - 1), k0 = tid / Q;
     float l = 0.f;
-    for (int k = k0; k < run.parts; k += 64) top = fmaxf(top, ws.stats[place(k) * 32 + row]);
+    for (int k = k0; k < run.parts; k += K0) top = fmaxf(top, ws.stats[place(k) * 2 * Q + row]);
     most[k0][row] = top;
     __syncthreads();
 #pragma unroll 8
-    for (int k = 0; k < 64; ++k) top = fmaxf(top, most[k][row]);
-    for (int k = k0; k < run.parts; k += 64) {
-      const float mk = ws.stats[place(k) * 32 + row], e = mk == top ? 1.f : __builtin_amdgcn_exp2f(mk - top);
+    for (int k = 0; k < K0; ++k) top = fmaxf(top, most[k][row]);
+    for (int k = k0; k < run.parts; k += K0) {
+      const float mk = ws.stats[place(k) * 2 * Q + row], e = mk == top ? 1.f : __builtin_amdgcn_exp2f(mk - top);
       weight[k][row] = e;
-      l += e * ws.stats[place(k) * 32 + 16 + row];
+      l += e * ws.stats[place(k) * 2 * Q + Q + row];
     }
     sum[k0][row] = l;
     __syncthreads();
   }
-  // row tid % 16 is also the row of the lane's query
-  const int lane = tid & 63, b = ((int)blockIdx.y & 7) * 4 + ((tid >> 6) & 3), quarter = tid >> 8, col = lane & 15, grp = lane >> 4;
+  const int lane = tid & 63, k1 = (int)blockIdx.y % (Q / 2) * 4 + ((tid >> 6) & 3), quarter = tid >> 8;
+  const int b = k1 & 31, col = 16 * (k1 >> 5) + (lane & 15), grp = lane >> 4;      // part k1: columns 16 b + 4 grp .. of query col
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  const float* src = ws.sums + (b * 64 + lane) * 4;
+  const float* src = ws.sums + (k1 * 64 + lane) * 4;
 #pragma unroll 4
   for (int k = quarter; k < run.parts; k += 4) {
-    const f32x4 v = *reinterpret_cast<const f32x4*>(src + place(k) * (kRows * kLat));
+    const f32x4 v = *reinterpret_cast<const f32x4*>(src + place(k) * (Q * kLat));
     acc += weight[k][col] * v;
   }
   if (quarter > 0) part[quarter - 1][tid & 255] = acc;
@@ -518,9 +721,9 @@ __global__ void __launch_bounds__(1024) latent_join_kernel(const LatentParams p,
   for (int k = 0; k < 3; ++k) acc += part[k][tid];
   float l = 0.f;
 #pragma unroll 8
-  for (int k = 0; k < 64; ++k) l += sum[k][col];
+  for (int k = 0; k < K0; ++k) l += sum[k][col];
   const int q0 = start_at(p.q_starts, run.req, p.n_tok), n = start_at(p.q_starts, run.req + 1, p.n_tok) - q0;
-  const int64_t row = (int64_t)run.block * (kRows * RG) + kRows * rg + col;
+  const int64_t row = (int64_t)run.block * (Q * RG) + Q * rg + col;
   if (row >= (int64_t)n * p.n_heads) return;
   const int token = (int)row / p.n_heads, head = (int)row - token * p.n_heads;
   const float r = l == 0.f ? 0.f : 1.f / l;
@@ -528,48 +731,54 @@ __global__ void __launch_bounds__(1024) latent_join_kernel(const LatentParams p,
   h.x = (uint32_t)T::from_f32(acc.x * r) | ((uint32_t)T::from_f32(acc.y * r) << 16);
   h.y = (uint32_t)T::from_f32(acc.z * r) | ((uint32_t)T::from_f32(acc.w * r) << 16);
   *reinterpret_cast<mx_u32x2*>(p.out + (int64_t)(q0 + token) * p.out_stride + (int64_t)head * kLat + 16 * b + 4 * grp) = h;
-  if (b == 0 && grp == 0 && p.lse)
+  if (b == 0 && grp == 0 && p.lse) {
+    float top = -INFINITY;
+    for (int k = 0; k < K0; ++k) top = fmaxf(top, most[k][col]);
     p.lse[(int64_t)(q0 + token) * p.n_heads + head] =
         l == 0.f ? -INFINITY : (top - Mma<T>::kLift + __builtin_amdgcn_logf(l)) * 0.693147180559945309f;
+  }
 }
 
-// Row groups of a workgroup: few rows leave key groups to the other wavefronts, many share each tile.
-static int row_groups(int n_tok, int n_req, int n_heads) {
+// Queries of a wavefront and row groups of a workgroup, by the rows of an average request: few rows leave key groups to the other
+// wavefronts, many share each tile.
+static int run_rows(int n_tok, int n_req, int n_heads) {
   const int64_t rows = ((int64_t)n_tok * n_heads + std::max(n_req, 1) - 1) / std::max(n_req, 1);
-  return rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 64 ? 4 : 8;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
 }
 
 constexpr size_t kHead = 256, kRunBytes = (kGroups * sizeof(Run) + 255) & ~(size_t)255;
+static size_t stats_bytes(int rows) { return (size_t)2 * kGroups * rows * 2 * 4; }
 
 size_t latent_workspace_bytes(int n_tok, int n_req, int n_heads) {
-  return kHead + kRunBytes + (size_t)2 * kGroups * row_groups(n_tok, n_req, n_heads) * (128 + kSumBytes);
+  const int rows = run_rows(n_tok, n_req, n_heads);
+  return kHead + kRunBytes + stats_bytes(rows) + (size_t)2 * kGroups * rows * kLat * 4;
 }
 
-template <typename T, bool MX, int RG>
+template <typename T, bool MX, int Q, int RG>
 static hipError_t launch_latent(const LatentParams& p, void* mem, hipStream_t s) {
   uint8_t* at = (uint8_t*)mem;
   const Workspace ws = {(int32_t*)at, (Run*)(at + kHead), (float*)(at + kHead + kRunBytes),
-                        (float*)(at + kHead + kRunBytes + (size_t)2 * kGroups * RG * 128)};
+                        (float*)(at + kHead + kRunBytes + stats_bytes(Q * RG))};
   // every request has at most one run more than its share of the rows
-  const int64_t rows = (int64_t)p.n_tok * p.n_heads, runs = std::min(rows / (kRows * RG) + p.n_req, rows);
+  const int64_t rows = (int64_t)p.n_tok * p.n_heads, runs = std::min(rows / (Q * RG) + p.n_req, rows);
   const bool by_run = runs <= kGroups;
-  hipError_t e = hipFuncSetAttribute((const void*)latent_kernel<T, MX, RG>, hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+  hipError_t e = hipFuncSetAttribute((const void*)latent_kernel<T, MX, Q, RG>, hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(HIP_KERNEL_NAME(latent_kernel<T, MX, RG>), dim3(kGroups), dim3(64 * waves_of<RG>()), kLds, s, p, ws, by_run);
+  hipLaunchKernelGGL(HIP_KERNEL_NAME(latent_kernel<T, MX, Q, RG>), dim3(kGroups), dim3(64 * Shape<MX, Q, RG>::W), kLds, s, p, ws, by_run);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(HIP_KERNEL_NAME(latent_join_kernel<T, RG>), dim3((unsigned)std::min<int64_t>(runs, kGroups), 8 * RG), dim3(1024), 0, s,
-                     p, ws);
+  hipLaunchKernelGGL(HIP_KERNEL_NAME(latent_join_kernel<T, Q, RG>), dim3((unsigned)std::min<int64_t>(runs, kGroups), Q / 2 * RG), dim3(1024),
+                     0, s, p, ws);
   return hipGetLastError();
 }
 
 template <typename T, bool MX>
 static hipError_t launch_rows(const LatentParams& p, void* ws, hipStream_t s) {
-  const int rg = row_groups(p.n_tok, p.n_req, p.n_heads);
-  return rg == 1   ? launch_latent<T, MX, 1>(p, ws, s)
-         : rg == 2 ? launch_latent<T, MX, 2>(p, ws, s)
-         : rg == 4 ? launch_latent<T, MX, 4>(p, ws, s)
-                   : launch_latent<T, MX, 8>(p, ws, s);
+  const int rows = run_rows(p.n_tok, p.n_req, p.n_heads);
+  return rows == 16   ? launch_latent<T, MX, 16, 1>(p, ws, s)
+         : rows == 32 ? launch_latent<T, MX, 16, 2>(p, ws, s)
+         : rows == 64 ? launch_latent<T, MX, 16, 4>(p, ws, s)
+                      : launch_latent<T, MX, 32, 4>(p, ws, s);
 }
 
 hipError_t launch_latent_attention(const LatentParams& p, int dtype, int fmt, void* ws, hipStream_t s) {
