@@ -26,7 +26,7 @@ namespace gale {
 // All runs' tiles form one line, cut into up to kGroups equal parts, one for each workgroup (one to a CU): a run that lies in several
 // parts leaves unnormalised sums in the workspace, two places to a workgroup (a run that began before its part, and one that goes
 // on behind it), and latent_join_kernel adds them in the order of the parts.
-constexpr int kGroups = 256;
+constexpr int kGroups = 256, kLead = 4;
 
 template <bool MX, int Q, int RG>
 struct Shape {
@@ -75,6 +75,17 @@ __device__ __forceinline__ void run_units(const LatentParams& p, int r, int& blo
   units = max(1, (int)(((int64_t)keys + Sh::UNIT - 1) / Sh::UNIT));
 }
 
+__device__ uint32_t zero_row[2 * kLat / 4];      // never written
+
+// Which 32 columns a product with K takes together is free: four chunks of 8, one for each lane group.  The groups that the LDS serves
+// at once, 0 and 1 or 2 and 3 with eight rows of each (all even and odd rows of four), must not meet where a chunk's bits
+// and the row's swizzle cancel, so they differ in bit 2 of the chunk (bit 1 of the rope's), which the swizzle changes with bit 0 (1) of
+// the row.  With consecutive chunks every read of K took twice as long (counters: a conflict cycle for each).
+__device__ __forceinline__ int block_chunk(int s, int grp) {
+  return (s & 3) | (grp & 1) << 2 | (s & 4) << 1 | (grp >> 1) << 4 | (s >> 3) << 5;
+}
+__device__ __forceinline__ int rope_chunk(int s, int grp) { return (grp & 1) << 1 | grp >> 1 | s << 2; }
+
 template <typename T, bool MX, int Q, int RG>
 __global__ void __launch_bounds__(16 * Q) __attribute__((amdgpu_waves_per_eu(Q / 16, Q / 16)))      // 64 W threads, C wavefronts to a SIMD
 latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
@@ -97,7 +108,7 @@ latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
 
   // ---- this workgroup's part of the line of units --------------------------------------------------------------------
   int64_t u, u_end, base, part_units;      // base: the first unit of request req
-  int req, run_base;                       // run_base: runs before request req
+  int req, run_base, lead;                 // run_base: runs before request req
   {
     int64_t* const part = (int64_t*)smem_raw;
     int* const runs_of = (int*)(smem_raw + 64);
@@ -133,16 +144,21 @@ latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
       if (blockIdx.x == 0) *ws.count = by_run ? total_runs : kGroups;
     }
     total = uniform64(total);
+    // a run costs as much as `lead` units beside its own (its queries, the first tiles' latency, its sums): they stand in front of
+    // it in the line, but where there are few units a workgroup takes one
+    lead = total <= kGroups ? 0 : kLead;
+    total += (int64_t)lead * total_runs;
     part_units = (total + kGroups - 1) / kGroups;
     u = (int64_t)blockIdx.x * part_units;
     u_end = min(total, u + part_units);
     if (u >= u_end) return;
-    scan -= sum;
+    sum += (int64_t)lead * runs;
+    scan += (int64_t)lead * rscan - sum;
     rscan -= runs;
     if (sum > 0 && scan <= u && u < scan + sum) {
       for (int r = r0; r < r1; ++r) {
         if (per > 1) run_units<Sh>(p, r, b, n);
-        const int64_t mine = (int64_t)b * n;
+        const int64_t mine = (int64_t)b * (n + lead);
         if (u < scan + mine) {
           found[0] = r;
           found[1] = rscan;
@@ -172,7 +188,7 @@ latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
     int blocks, units;
     run_units<Sh>(p, req, blocks, units);
     blocks = __builtin_amdgcn_readfirstlane(blocks);
-    units = __builtin_amdgcn_readfirstlane(units);
+    units = __builtin_amdgcn_readfirstlane(units) + lead;
     if (u >= base + (int64_t)blocks * units) {      // also requests without queries
       base += (int64_t)blocks * units;
       run_base += blocks;
@@ -181,20 +197,34 @@ latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
     }
     const int block = __builtin_amdgcn_readfirstlane((int)divide(u - base, units));
     const int64_t run0 = base + (int64_t)block * units;
-    const int a0 = __builtin_amdgcn_readfirstlane((int)(u - run0)), a1 = __builtin_amdgcn_readfirstlane((int)min((int64_t)units, u_end - run0));
-    const bool whole = a0 == 0 && a1 == units;
+    const int a0 = max(0, __builtin_amdgcn_readfirstlane((int)(u - run0)) - lead);
+    const int a1 = __builtin_amdgcn_readfirstlane((int)min((int64_t)units, u_end - run0)) - lead;
+    if (a1 <= 0) break;      // the part ends in front of the run's first unit
+    const bool whole = a0 == 0 && a1 == units - lead;
     const int q0 = start_at(p.q_starts, req, p.n_tok), n = start_at(p.q_starts, req + 1, p.n_tok) - q0;
     const int keys = __builtin_amdgcn_readfirstlane(keys_of(p.kv_lens, req, p.max_blocks, p.block_shift));
     const int32_t* const table = p.table + (int64_t)req * p.table_stride;
 
-    // Lane r of KEYS lanes knows the slot of row r of a tile, -1 where there is no key.
-    auto slots_of = [&](int i) {
-      const int pos = (i * KG + kg) * KEYS + here(lane & (KEYS - 1));
-      return pos >= 0 && pos < keys ? slot_of(table, pos, p.block_shift, p.n_blocks) : -1;
+    // The blocks of the halves of unit i's tile (past the last key: the last key's; without a key: any number), each in one block where
+    // those are large enough: scalar loads, ahead of their use, which no copy is waited for with.  In smaller blocks lane r of
+    // KEYS lanes looks up row r's when it is needed.  slot_of_row: lane r's row of the cache, -1 where there is no key.
+    const bool large = (2 << p.block_shift) >= KEYS;
+    const int64_t blocks_of = uniform64((int64_t)(keys > 0 ? table : p.kv_lens));
+    const uint32_t last_key = (uint32_t)max(keys, 1) - 1u;
+    auto position = [&](int i) { return (i * KG + kg) * KEYS + here(lane & (KEYS - 1)); };
+    auto look = [&](int i, int half) {
+      const uint32_t pos = min((uint32_t)((i * KG + kg) * KEYS + half * (KEYS / 2)), last_key);
+      return __builtin_amdgcn_readfirstlane(((const __attribute__((address_space(4))) int32_t*)blocks_of)[pos >> p.block_shift]);
+    };
+    auto slot_of_row = [&](int lower, int upper, int i) {
+      const int pos = position(i);
+      int id = pos & (KEYS / 2) ? upper : lower;
+      if (!large) id = here(((const __attribute__((address_space(1))) int32_t*)blocks_of)[min((uint32_t)pos, last_key) >> p.block_shift]);
+      return id >= 0 && id < p.n_blocks && (uint32_t)pos < (uint32_t)keys ? (id << p.block_shift) + (pos & ((1 << p.block_shift) - 1)) : -1;
     };
     constexpr uint32_t ALL = KEYS == 32 ? 0xFFFFFFFFu : 0xFFFFu;
     auto keys_in = [&](int slot) { return (uint32_t)__ballot(slot >= 0) & ALL; };
-    int slot = slots_of(a0);
+    int lower = look(a0, 0), upper = look(a0, 1), lower1 = look(a0 + 1, 0), upper1 = look(a0 + 1, 1);      // of the next tile, of the one behind
 
     // this lane's queries
     const int64_t rows = (int64_t)n * p.n_heads, row0 = (int64_t)block * Sh::ROWS + Q * rg + col;
@@ -210,11 +240,11 @@ latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
       const int seen = p.causal ? max(0, min(keys, keys - n + token + 1)) : keys;
       w_keys = max(w_keys, real ? seen : 0);
       w_all = min(w_all, real ? seen : keys);
-      const uint16_t* src = p.q + (int64_t)(q0 + token) * p.q_stride + (int64_t)head * kQk + 8 * grp;
+      const uint16_t* src = p.q + (int64_t)(q0 + token) * p.q_stride + (int64_t)head * kQk;
 #pragma unroll
       for (int s = 0; s < QB; ++s) {
-        const int block = C == 1 ? s : s < 8 ? 8 * ch + s : 16 + ch;
-        const s16x8 v = signed_query<T>(*reinterpret_cast<const s16x8*>(src + 32 * block), p.scale);
+        const int at = s < 16 / C ? 8 * block_chunk(C == 1 ? s : 8 * ch + s, grp) : kLat + 8 * rope_chunk(C == 1 ? s - 16 : ch, grp);
+        const s16x8 v = signed_query<T>(*reinterpret_cast<const s16x8*>(src + at), p.scale);
         if (in_lds(s)) *(__attribute__((address_space(3))) s16x8*)(queries + (s / 3) * 2048 + g * 1024) = v;
         else xq[g][in_regs(s)] = v;
       }
@@ -250,50 +280,53 @@ latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
     // ---- fetching a tile ---------------------------------------------------------------------------------------------
     uint32_t codes[MX && !RAW ? OWN : 1];
     mx_u32x4 ropes[MX && !RAW ? PIECES : 1];
-    // 16-bit rows: straight into LDS, a row for each copy; rows without a key come as zeros (a resource of no bytes), so that
-    // 0 times them is 0.  Their rope rows do not matter: such keys' scores are replaced.  Codes wait in registers, or in LDS.
-    auto fetch = [&](int slot, int buf) {
-      lds_u8* to = RAW ? raw + buf * Sh::RAW : tiles + buf * Sh::TILE;
+    // 16-bit rows: straight into LDS, a row for each copy; rows without a key come from a row of zeros, so that 0 times them is 0.
+    // Their rope rows do not matter: such keys' scores are replaced.  Codes wait in registers, or in LDS.
+    auto fetch = [&](int slot, lds_u8* to) __attribute__((always_inline)) {
       const int lane = here(tid & 63);
+      typedef const __attribute__((address_space(1))) void* global_ptr;
+      int at_codes[4], at_rope[PIECES], at_scale = 0;      // all exchanges first
       if constexpr (RAW) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint8_t* src = p.latent + (int64_t)max(__shfl(slot, 4 * i + (lane >> 4)), 0) * (kLat / 2) + 16 * (lane & 15);
-          __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src, (lds_ptr)(to + 1024 * i), 16, 0, 0);
-        }
+        for (int i = 0; i < 4; ++i) at_codes[i] = max(__shfl(slot, 4 * i + (lane >> 4)), 0);
+      }
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) at_rope[i] = max(__shfl(slot, 8 * ((f * PIECES + i) % (KEYS / 8)) + (lane >> 3)), 0);
+      if constexpr (MX) at_scale = max(__shfl(slot, f * OWN + (lane & (OWN - 1))), 0);
+      if constexpr (RAW) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          __builtin_amdgcn_global_load_lds((global_ptr)(p.latent + (int64_t)at_codes[i] * (kLat / 2) + 16 * (lane & 15)),
+                                           (lds_ptr)(to + 1024 * i), 16, 0, 0);
       } else {
 #pragma unroll
         for (int i = 0; i < OWN; ++i) {
           const int r = f * OWN + i, at = __builtin_amdgcn_readlane(slot, r);
-          const int64_t bytes = MX ? kLat / 2 : p.latent_bytes;
-          const auto rs = __builtin_amdgcn_make_buffer_rsrc((void*)(p.latent + (int64_t)max(at, 0) * bytes), 0,
-                                                            at < 0 ? 0 : MX ? kLat / 2 : 2 * kLat, 0x00020000);
-          if constexpr (MX) codes[i] = __builtin_amdgcn_raw_buffer_load_b32(rs, 4 * lane, 0, 0);
-          else __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr)(to + r * 1024), 16, (lane ^ swizzle(r)) << 4, 0, 0, 0);
+          if constexpr (MX) {
+            codes[i] = *reinterpret_cast<const uint32_t*>(p.latent + (int64_t)max(at, 0) * (kLat / 2) + 4 * lane);
+          } else {
+            const uint8_t* row = at < 0 ? reinterpret_cast<const uint8_t*>(zero_row) : p.latent + (int64_t)at * p.latent_bytes;
+            __builtin_amdgcn_global_load_lds((global_ptr)(row + ((lane ^ swizzle(r)) << 4)), (lds_ptr)(to + r * 1024), 16, 0, 0);
+          }
         }
       }
 #pragma unroll
       for (int i = 0; i < PIECES; ++i) {
         if (f * PIECES + i >= KEYS / 8) break;
         const int r = 8 * (f * PIECES + i) + (lane >> 3);
-        const uint8_t* src = p.rope + (int64_t)max(__shfl(slot, r), 0) * p.rope_bytes + (((lane & 7) ^ swizzle8(r)) << 4);
+        const uint8_t* src = p.rope + (int64_t)at_rope[i] * p.rope_bytes + (((lane & 7) ^ swizzle8(r)) << 4);
         if constexpr (MX && !RAW) ropes[i] = *reinterpret_cast<const mx_u32x4*>(src);
         else
-          __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                           (lds_ptr)(to + (RAW ? 4096 : Sh::LATENTS) + 1024 * (f * PIECES + i)), 16, 0, 0);
+          __builtin_amdgcn_global_load_lds((global_ptr)src, (lds_ptr)(to + (RAW ? 4096 : Sh::LATENTS) + 1024 * (f * PIECES + i)), 16, 0, 0);
       }
-      if constexpr (MX) {
-        const uint8_t* src = p.scales + (int64_t)max(__shfl(slot, f * OWN + (lane & (OWN - 1))), 0) * (kLat / 32);
-        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+      if constexpr (MX)
+        __builtin_amdgcn_global_load_lds((global_ptr)(p.scales + (int64_t)at_scale * (kLat / 32)),
                                          RAW ? (lds_ptr)(to + 6144) : (lds_ptr)scale_area, 16, 0, 0);
-      }
     };
     constexpr int COPIES = RAW ? 7 : OWN + PIECES;      // of a fetch into LDS
     // MX rows, later: 4-bit elements to 16-bit numbers, rounded where a scale takes them out of fp16's range.
-    auto store = [&](uint32_t valid, int buf) {
+    auto store = [&](uint32_t valid, const lds_u8* from, lds_u8* to) __attribute__((always_inline)) {
       if constexpr (MX) {
-        lds_u8* to = RAW ? tiles : tiles + buf * Sh::TILE;
-        const lds_u8* from = raw + buf * Sh::RAW;
         const lds_u8* scales = RAW ? from + 6144 : scale_area;
         const int lane = here(tid & 63);
         if constexpr (!RAW) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");      // the scales' copy
@@ -323,18 +356,19 @@ latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
 
     // ---- the products with a tile: latents at `at`, rope rows at `rope` ----------------------------------------------------
     auto use = [&](int j0, uint32_t valid, const lds_u8* at, const lds_u8* rope) __attribute__((always_inline)) {
+      at += 512 * ch;
       // operands are read AHEAD in front of their products; the scheduler by itself would read each right before
       constexpr int U = KEYS / 16, NK = QB * U;
-      // LDS places of operands.  K, column block s of 32: chunk 4 s + grp of row col (+ 16); V^T, column block b of 16: chunks 2 b and
-      // 2 b + 1 of rows vrow (+ 16).  A row's swizzle and the block change the same bits 4 .. 7 of a place in a tile, which
-      // starts at a multiple of 256: a block is one exclusive or away.
+      // LDS places of operands.  K, block s: the lane group's chunk (block_chunk) of row col (+ 16); V^T, column block b of 16: chunks
+      // 2 b and 2 b + 1 of rows vrow (+ 16).  A row's swizzle and the block change the same bits 4 .. 7 of a place in a tile,
+      // which starts at a multiple of 256: a block is one exclusive or away.
       const int lane = here(tid & 63), col = lane & 15, grp = lane >> 4, vrow = 4 * grp + (col >> 2);
-      const uint32_t at_k = (uint32_t)(at + 512 * ch) + col * 1024 + ((grp ^ swizzle(col)) << 4);
-      const uint32_t at_r = (uint32_t)rope + col * 128 + (((4 * ch + grp) ^ swizzle8(col)) << 4);
+      const int at_k = col * 1024 + (grp >> 1) * 256 + (((grp & 1) * 4 ^ swizzle(col)) << 4);
+      const int at_r = col * 128 + ((rope_chunk(ch, grp) ^ swizzle8(col)) << 4);
       auto key = [&](int k) {
         const int u = k % U, s = k / U;
-        return s < 16 / C ? lds_operand(lds_at(at_k ^ ((s & 3) << 6)) + (s >> 2) * 256 + u * 16 * 1024)
-                          : lds_operand(lds_at(at_r ^ ((s & 1) << 6)) + u * 16 * 128);
+        return s < 16 / C ? lds_operand(at + (at_k ^ (((s & 3) | (s & 4) << 1) << 4)) + (s >> 3) * 512 + u * 16 * 1024)
+                          : lds_operand(rope + (at_r ^ ((s & 1) << 6)) + u * 16 * 128);
       };
       f32x4 s[G][2] = {};      // U = 1: two chains, an MFMA takes longer than its issue
       {
@@ -360,7 +394,7 @@ latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
         }
         __builtin_amdgcn_sched_barrier(0);
       }
-      const uint32_t at_v = (uint32_t)(at + 512 * ch) + vrow * 1024 + ((((col & 3) >> 1) ^ swizzle(vrow)) << 4) + 8 * (col & 1);
+      const int at_v = vrow * 1024 + ((((col & 3) >> 1) ^ swizzle(vrow)) << 4) + 8 * (col & 1);
       if constexpr (C == 2) {      // the sum of both halves is the same in both wavefronts, bit for bit
         lds_f32x4* mine = (lds_f32x4*)(smem + kScores) + wave * 256 + lane;
 #pragma unroll
@@ -422,7 +456,7 @@ latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
         s16x4 w[G], a[AHEAD];
 #pragma unroll
         for (int g = 0; g < G; ++g) w[g] = Mma<T>::pack4(e[g]);
-        auto value = [&](int b) { return lds_transposed(lds_at(at_v ^ ((b & 7) << 5)) + (b >> 3) * 256); };
+        auto value = [&](int b) { return lds_transposed(at + (at_v ^ ((b & 7) << 5)) + (b >> 3) * 256); };
 #pragma unroll
         for (int b = 0; b < AHEAD; ++b) a[b] = value(b);
 #pragma unroll
@@ -437,7 +471,7 @@ latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
 #pragma unroll
         for (int g = 0; g < G; ++g) w[g] = Mma<T>::pack(e[g]);
         auto value = [&](int b) {
-          const lds_u8* from = lds_at(at_v ^ ((b & 7) << 5)) + (b >> 3) * 256;
+          const lds_u8* from = at + (at_v ^ ((b & 7) << 5)) + (b >> 3) * 256;
           return __builtin_shufflevector(lds_transposed(from), lds_transposed(from + 16 * 1024), 0, 1, 2, 3, 4, 5, 6, 7);
         };
 #pragma unroll
@@ -455,7 +489,7 @@ latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
     // A product takes the weight 0 of a key that a query does not see times its value, and NaN times 0 is NaN.  So where only some
     // of the run's queries see a key (j >= some), rows of a tile that are not finite are zeroed by the wavefront that fetched them, and
     // the queries that see such a key have NaN as their sum of weights.
-    auto clear = [&](int j0, lds_u8* at) {
+    auto clear = [&](int j0, lds_u8* at) __attribute__((always_inline)) {
       uint32_t bad = 0;
       for (int r = max(f * OWN, some - j0); r < (f + 1) * OWN; ++r) {
         lds_u32x4* row16 = (lds_u32x4*)(at + r * 1024 + 16 * lane);
@@ -484,99 +518,115 @@ latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
     };
 
     // ---- the tiles -----------------------------------------------------------------------------------------------------
+    // A fetch and the use of another tile stand in one function with pointers that do not meet: the compiler, which does not see
+    // how the places alternate, would otherwise wait for all copies in front of every transposing read.
+    int slot = slot_of_row(lower, upper, a0);
+    lower = lower1, upper = upper1;
     if constexpr (RAW) {
       // every wavefront by itself, three tiles' rows on the way: a fetch is 7 copies, and what is younger than a tile's is known
+      lower1 = look(a0 + 2, 0), upper1 = look(a0 + 2, 1);
       uint32_t valid[3] = {keys_in(slot), 0, 0};
-      fetch(slot, 0);
-#pragma unroll
-      for (int k = 1; k < 3; ++k)
-        if (a0 + k < a1) {
-          slot = slots_of(a0 + k);
-          valid[k] = keys_in(slot);
-          fetch(slot, k);
+      fetch(slot, raw);
+      if (a0 + 1 < a1) {
+        slot = slot_of_row(lower, upper, a0 + 1);
+        valid[1] = keys_in(slot);
+        fetch(slot, raw + Sh::RAW);
+      }
+      lower = look(a0 + 3, 0), upper = look(a0 + 3, 1);
+      if (a0 + 2 < a1) {
+        slot = slot_of_row(lower1, upper1, a0 + 2);
+        valid[2] = keys_in(slot);
+        fetch(slot, raw + 2 * Sh::RAW);
+      }
+      auto step = [&](int i, lds_u8* __restrict rows, lds_u8* __restrict at) __attribute__((always_inline)) {
+        const int j0 = (i * KG + kg) * KEYS;
+        if (j0 < w_keys) {
+          store(valid[0], rows, at);
+          if (j0 + KEYS > some) clear(j0, at);
+          use(j0, valid[0], at, rows + 4096);
         }
-      // slots are looked up two tiles before their fetch: waiting for a look-up waits for the copies in front of it too
-      slot = a0 + 3 < a1 ? slots_of(a0 + 3) : -1;
-      int slot2 = a0 + 4 < a1 ? slots_of(a0 + 4) : -1;
+        valid[0] = valid[1];
+        valid[1] = valid[2];
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");      // the tile is read
+        slot = slot_of_row(lower, upper, i + 3);
+        lower = look(i + 4, 0), upper = look(i + 4, 1);
+        if (i + 3 < a1) {
+          valid[2] = keys_in(slot);
+          fetch(slot, rows);
+        }
+      };
       int buf = 0;
       for (int i = a0; i < a1; ++i) {
         if (i + 2 < a1) asm volatile("s_waitcnt vmcnt(14) lgkmcnt(0)" ::: "memory");
         else if (i + 1 < a1) asm volatile("s_waitcnt vmcnt(7) lgkmcnt(0)" ::: "memory");
         else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-        const int j0 = (i * KG + kg) * KEYS;
-        if (j0 < w_keys) {
-          store(valid[0], buf);
-          if (j0 + KEYS > some) clear(j0, tiles);
-          use(j0, valid[0], tiles, raw + buf * Sh::RAW + 4096);
-        }
-        valid[0] = valid[1];
-        valid[1] = valid[2];
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");      // the tile is read
-        if (i + 3 < a1) {
-          valid[2] = keys_in(slot);
-          const int next = i + 5 < a1 ? slots_of(i + 5) : -1;
-          fetch(slot, buf);
-          slot = slot2;
-          slot2 = next;
-        }
+        step(i, raw + buf * Sh::RAW, tiles);
         buf = buf == 2 ? 0 : buf + 1;
       }
     } else if constexpr (KEYS == 16) {
       // every wavefront by itself: the next tile's copies go out before this one's are waited for
       static_assert(COPIES == 18, "the wait below");
       uint32_t valid = keys_in(slot);
-      fetch(slot, 0);
-      slot = a0 + 1 < a1 ? slots_of(a0 + 1) : -1;
-      int buf = 0;
-      for (int i = a0; i < a1; ++i) {
-        const uint32_t next_valid = keys_in(slot);
+      fetch(slot, tiles);
+      auto step = [&](int i, lds_u8* __restrict to, lds_u8* __restrict at) __attribute__((always_inline)) {
+        uint32_t next = 0;
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");      // the tile before is read
+        slot = slot_of_row(lower, upper, i + 1);
+        lower = look(i + 2, 0), upper = look(i + 2, 1);
         if (i + 1 < a1) {
-          const int next = i + 2 < a1 ? slots_of(i + 2) : -1;
-          fetch(slot, buf ^ 1);
-          slot = next;
+          next = keys_in(slot);
+          fetch(slot, to);
           asm volatile("s_waitcnt vmcnt(18)" ::: "memory");
         } else {
           asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         }
         const int j0 = (i * KG + kg) * KEYS;
-        lds_u8* at = tiles + buf * Sh::TILE;
         if (j0 + KEYS > some) clear(j0, at);
         if (j0 < w_keys) use(j0, valid, at, at + Sh::LATENTS);
-        valid = next_valid;
-        buf ^= 1;
-      }
-    } else {
-      uint32_t valid = keys_in(slot);
-      fetch(slot, 0);
-      if constexpr (MX) store(valid, 0);
-      slot = a0 + 1 < a1 ? slots_of(a0 + 1) : -1;
-      if constexpr (MX) {
-        if (a0 + 1 < a1) fetch(slot, 0);
-      }
+        valid = next;
+      };
       int buf = 0;
-      for (int i = a0; i < a1; ++i) {
-        tiles_ready();
-        const uint32_t next = keys_in(slot);
+      for (int i = a0; i < a1; ++i, buf ^= 1) step(i, tiles + (buf ^ 1) * Sh::TILE, tiles + buf * Sh::TILE);
+    } else {
+      uint32_t valid = keys_in(slot), next = 0;
+      fetch(slot, tiles);
+      if constexpr (MX) {
+        store(valid, nullptr, tiles);
+        slot = slot_of_row(lower, upper, a0 + 1);
+        lower = look(a0 + 2, 0), upper = look(a0 + 2, 1);
+        if (a0 + 1 < a1) {
+          next = keys_in(slot);
+          fetch(slot, nullptr);
+        }
+      }
+      auto step = [&](int i, lds_u8* __restrict to, lds_u8* __restrict at) __attribute__((always_inline)) {
         const int j0 = (i * KG + kg) * KEYS;
-        lds_u8* at = tiles + buf * Sh::TILE;
-        buf ^= 1;
         if ((i + 1) * Sh::UNIT > some) clear(j0, at);      // the same for all wavefronts
         if constexpr (MX) {
           if (j0 < w_keys) use(j0, valid, at, at + Sh::LATENTS);
-          if (i + 1 < a1) {
-            store(next, buf);
-            slot = i + 2 < a1 ? slots_of(i + 2) : -1;
-            if (i + 2 < a1) fetch(slot, 0);
+          valid = next;
+          if (i + 1 < a1) store(next, nullptr, to);
+          slot = slot_of_row(lower, upper, i + 2);
+          lower = look(i + 3, 0), upper = look(i + 3, 1);
+          if (i + 2 < a1) {
+            next = keys_in(slot);
+            fetch(slot, nullptr);
           }
         } else {
+          slot = slot_of_row(lower, upper, i + 1);
+          lower = look(i + 2, 0), upper = look(i + 2, 1);
           if (i + 1 < a1) {
-            fetch(slot, buf);
-            slot = i + 2 < a1 ? slots_of(i + 2) : -1;
+            next = keys_in(slot);
+            fetch(slot, to);
           }
           if (j0 < w_keys) use(j0, valid, at, at + Sh::LATENTS);
+          valid = next;
         }
-        valid = next;
+      };
+      int buf = 0;
+      for (int i = a0; i < a1; ++i, buf ^= 1) {
+        tiles_ready();
+        step(i, tiles + (buf ^ 1) * Sh::TILE, tiles + buf * Sh::TILE);
       }
     }
 
@@ -669,7 +719,7 @@ latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
       if (at < kGroups)       // always, where q_starts ascends
         ws.runs[at] = Run{whole ? 0 : (int)divide(run0 + units - 1, part_units) - first + 1, first, req, block};
     }
-    u = run0 + a1;
+    u = run0 + lead + a1;
     if (u >= u_end) break;
     __syncthreads();          // the next run writes the tiles
   }
