@@ -114,32 +114,29 @@ __global__ void __launch_bounds__(256, 2) prompt_kernel(const PromptParams p, in
   const float c = p.scale == 0.f ? 1.f : fabsf(p.scale) * 1.44269504088896341f;
   if (wg_keys > 0) copy(0, smem);
 
-  // LDS places of operands
-  const int zk = swizzle(col), zr = swizzle8(col);
-  int ak[8], ar[4], av[2][4];
-#pragma unroll
-  for (int s = 0; s < 8; ++s) ak[s] = col * 256 + (((2 * s + half) ^ zk) << 4);
-#pragma unroll
-  for (int s = 0; s < 4; ++s) ar[s] = kTileK + col * 128 + (((2 * s + half) ^ zr) << 4);
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int row = 8 * u + 4 * half + ((lane & 15) >> 2);
-#pragma unroll
-    for (int b = 0; b < 4; ++b)
-      av[u][b] = kTileK + kTileR + row * 256 + (((4 * b + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1)) ^ swizzle(row)) << 4) + 8 * (lane & 1);
-  }
-
-  int next = kTile;        // where the next tile goes; this one is at kTile - next, and the operands' places move with it
   f32x16 o[4] = {};
   float m = -INFINITY, l = 0.f;
 
-  auto tile = [&](int j0, const lds_u8* at) __attribute__((always_inline)) {
+  // The next tile's copies and the use of this one stand in one function with pointers that do not meet: the compiler, which does not
+  // see how the places alternate, would otherwise wait for all copies in front of every transposing read.
+  auto step = [&](int j0, lds_u8* __restrict to, const lds_u8* __restrict at) __attribute__((always_inline)) {
+    if (j0 + kBk < wg_keys) copy(j0 + kBk, to);
+    if (j0 >= w_keys) return;
+    // LDS places of operands: K, block k of 16 columns: chunk 2 k + half of row col (+ 32); V^T, column block b of 32: chunks 4 b .. of
+    // rows vrow, vrow + 8 (+ 16 t).  Blocks change the same bits of a place as a row's swizzle: by exclusive or.
+    const int lane = here(tid & 63), col = lane & 31, half = lane >> 5, vrow = 4 * half + ((lane & 15) >> 2);
+    const int ak = col * 256 + ((half ^ swizzle(col)) << 4), ar = col * 128 + ((half ^ swizzle8(col)) << 4);
+    const int chunk = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+    const int av0 = vrow * 256 + ((chunk ^ swizzle(vrow)) << 4) + 8 * (lane & 1);
+    const int av1 = (vrow + 8) * 256 + ((chunk ^ swizzle(vrow + 8)) << 4) + 8 * (lane & 1);
+    const lds_u8* const rows = at + kTileK;
+    const lds_u8* const vals = rows + kTileR;
     f32x16 s[2] = {};
 #pragma unroll
     for (int k = 0; k < 12; ++k)
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        const s16x8 a = k < 8 ? lds_operand(at + ak[k & 7] + g * 32 * 256) : lds_operand(at + ar[k & 3] + g * 32 * 128);
+        const s16x8 a = k < 8 ? lds_operand(at + (ak ^ (k << 5)) + g * 32 * 256) : lds_operand(rows + (ar ^ ((k & 3) << 5)) + g * 32 * 128);
         s[g] = Mma<T>::mma(a, xq[k], s[g]);
       }
     const bool masked = j0 + kBk > w_all;
@@ -182,7 +179,7 @@ __global__ void __launch_bounds__(256, 2) prompt_kernel(const PromptParams p, in
       for (int t = 0; t < 4; ++t) {
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          const s16x4 lo = lds_transposed(at + av[0][b] + t * 16 * 256), hi = lds_transposed(at + av[1][b] + t * 16 * 256);
+          const s16x4 lo = lds_transposed(vals + (av0 ^ (b << 6)) + t * 16 * 256), hi = lds_transposed(vals + (av1 ^ (b << 6)) + t * 16 * 256);
           s16x8 a = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
           if constexpr (clean.value) a = finite_only<T>(a);
           o[b] = Mma<T>::mma(a, pt[t], o[b]);
@@ -196,7 +193,7 @@ __global__ void __launch_bounds__(256, 2) prompt_kernel(const PromptParams p, in
     if (masked && w_all < w_keys) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const mx_u32x4 v = *(const __attribute__((address_space(3))) mx_u32x4*)(at + (kTile - next) + kTileK + kTileR + 1024 * i + 16 * lane);
+        const mx_u32x4 v = *(const __attribute__((address_space(3))) mx_u32x4*)(vals + 1024 * i + 16 * lane);
         odd |= not_finite<T>(v.x) | not_finite<T>(v.y) | not_finite<T>(v.z) | not_finite<T>(v.w);
       }
     }
@@ -206,7 +203,7 @@ __global__ void __launch_bounds__(256, 2) prompt_kernel(const PromptParams p, in
         if (j0 + j >= w_keys) break;
 #pragma unroll
         for (int u = 0; u < 16; ++u) {          // columns 8 u + 4 half ..
-          const s16x4 v = *(const __attribute__((address_space(3))) s16x4*)(at + (kTile - next) + kTileK + kTileR + j * 256 + ((u ^ swizzle(j)) << 4) + 8 * half);
+          const s16x4 v = *(const __attribute__((address_space(3))) s16x4*)(vals + j * 256 + ((u ^ swizzle(j)) << 4) + 8 * half);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float f = T::to_f32((uint16_t)v[i]);
@@ -219,18 +216,10 @@ __global__ void __launch_bounds__(256, 2) prompt_kernel(const PromptParams p, in
     }
   };
 
-  for (int j0 = 0; j0 < wg_keys; j0 += kBk) {
+  int buf = 0;
+  for (int j0 = 0; j0 < wg_keys; j0 += kBk, buf ^= 1) {
     tiles_ready();
-    if (j0 + kBk < wg_keys) copy(j0 + kBk, smem + next);
-    if (j0 < w_keys) tile(j0, smem);
-    const int move = 2 * next - kTile;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      ak[i] += move;
-      av[i & 1][i >> 1] += move;
-      if (i < 4) ar[i] += move;
-    }
-    next = kTile - next;
+    step(j0, smem + (buf ^ 1) * kTile, smem + buf * kTile);
   }
 
   l += other_half(l);
