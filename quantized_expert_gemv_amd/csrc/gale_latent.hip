@@ -244,8 +244,8 @@ latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
 #pragma unroll
       for (int s = 0; s < QB; ++s) {
         const int at = s < 16 / C ? 8 * block_chunk(C == 1 ? s : 8 * ch + s, grp) : kLat + 8 * rope_chunk(C == 1 ? s - 16 : ch, grp);
-        const s16x8 v = signed_query<T>(*reinterpret_cast<const s16x8*>(src + at), p.scale);
-        if (in_lds(s)) *(__attribute__((address_space(3))) s16x8*)(queries + (s / 3) * 2048 + g * 1024) = v;
+        const s16x8 v = *reinterpret_cast<const s16x8*>(src + at);
+        if (in_lds(s)) *(__attribute__((address_space(3))) s16x8*)(queries + (s / 3) * 2048 + g * 1024) = signed_query<T>(v, p.scale);
         else xq[g][in_regs(s)] = v;
       }
     }
@@ -538,6 +538,10 @@ latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
         valid[2] = keys_in(slot);
         fetch(slot, raw + 2 * Sh::RAW);
       }
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int s = 0; s < QB - QL; ++s) xq[g][s] = signed_query<T>(xq[g][s], p.scale);      // waited for behind the first copies
       auto step = [&](int i, lds_u8* __restrict rows, lds_u8* __restrict at) __attribute__((always_inline)) {
         const int j0 = (i * KG + kg) * KEYS;
         if (j0 < w_keys) {
@@ -568,6 +572,10 @@ latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
       static_assert(COPIES == 18, "the wait below");
       uint32_t valid = keys_in(slot);
       fetch(slot, tiles);
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int s = 0; s < QB - QL; ++s) xq[g][s] = signed_query<T>(xq[g][s], p.scale);      // waited for behind the first copies
       auto step = [&](int i, lds_u8* __restrict to, lds_u8* __restrict at) __attribute__((always_inline)) {
         uint32_t next = 0;
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");      // the tile before is read
@@ -599,6 +607,10 @@ latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
           fetch(slot, nullptr);
         }
       }
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int s = 0; s < QB - QL; ++s) xq[g][s] = signed_query<T>(xq[g][s], p.scale);      // waited for behind the first copies
       auto step = [&](int i, lds_u8* __restrict to, lds_u8* __restrict at) __attribute__((always_inline)) {
         const int j0 = (i * KG + kg) * KEYS;
         if ((i + 1) * Sh::UNIT > some) clear(j0, at);      // the same for all wavefronts
@@ -727,51 +739,42 @@ latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
 }
 
 // The sums of a run that lies in several parts: a workgroup per row group and four KB of sums, four quarters of the parts side by
-// side.  Every sum goes in the order of the parts, so equal calls give equal bits.
+// side, each in one pass with a running maximum, as the parts themselves are made: nothing is loaded twice, and the loads hang on
+// the run's record only (latency: 16 parts of one query group in 4 us where maxima, weights and sums were three passes: 5).
+// Every sum goes in the order of the parts, so equal calls give equal bits.
 template <typename T, int Q, int RG>
 __global__ void __launch_bounds__(1024) latent_join_kernel(const LatentParams p, const Workspace ws) {
-  constexpr int K0 = 1024 / Q;
-  __shared__ float weight[kGroups][Q], most[K0][Q], sum[K0][Q];
   __shared__ f32x4 part[3][256];
-  if ((int)blockIdx.x >= *ws.count) return;
+  __shared__ float stats[3][256][2];
+  const int count = *ws.count;
   const Run run = ws.runs[blockIdx.x];
-  if (run.parts <= 1) return;
+  if ((int)blockIdx.x >= count || run.parts <= 1) return;      // past count the record is of an earlier call
   const int tid = threadIdx.x, rg = (int)blockIdx.y / (Q / 2);
   auto place = [&](int k) { return (int64_t)(2 * (run.first + k) + (k == 0)) * RG + rg; };
-  float top = -INFINITY;
-  {
-    const int row = tid & (Q - 1), k0 = tid / Q;
-    float l = 0.f;
-    for (int k = k0; k < run.parts; k += K0) top = fmaxf(top, ws.stats[place(k) * 2 * Q + row]);
-    most[k0][row] = top;
-    __syncthreads();
-#pragma unroll 8
-    for (int k = 0; k < K0; ++k) top = fmaxf(top, most[k][row]);
-    for (int k = k0; k < run.parts; k += K0) {
-      const float mk = ws.stats[place(k) * 2 * Q + row], e = mk == top ? 1.f : __builtin_amdgcn_exp2f(mk - top);
-      weight[k][row] = e;
-      l += e * ws.stats[place(k) * 2 * Q + Q + row];
-    }
-    sum[k0][row] = l;
-    __syncthreads();
-  }
   const int lane = tid & 63, k1 = (int)blockIdx.y % (Q / 2) * 4 + ((tid >> 6) & 3), quarter = tid >> 8;
   const int b = k1 & 31, col = 16 * (k1 >> 5) + (lane & 15), grp = lane >> 4;      // part k1: columns 16 b + 4 grp .. of query col
+  const float* const src = ws.sums + (k1 * 64 + lane) * 4;
+  const float* const st = ws.stats + col;
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  const float* src = ws.sums + (k1 * 64 + lane) * 4;
+  float m = -INFINITY, l = 0.f;
+  auto add = [&](float mk, float lk, f32x4 v) {
+    const float up = fmaxf(m, mk), x = m == up ? 1.f : __builtin_amdgcn_exp2f(m - up), y = mk == up ? 1.f : __builtin_amdgcn_exp2f(mk - up);
+    acc = x * acc + y * v;
+    l = x * l + y * lk;
+    m = up;
+  };
 #pragma unroll 4
-  for (int k = quarter; k < run.parts; k += 4) {
-    const f32x4 v = *reinterpret_cast<const f32x4*>(src + place(k) * (Q * kLat));
-    acc += weight[k][col] * v;
+  for (int k = quarter; k < run.parts; k += 4)
+    add(st[place(k) * 2 * Q], st[place(k) * 2 * Q + Q], *reinterpret_cast<const f32x4*>(src + place(k) * (Q * kLat)));
+  if (quarter > 0) {
+    part[quarter - 1][tid & 255] = acc;
+    stats[quarter - 1][tid & 255][0] = m;
+    stats[quarter - 1][tid & 255][1] = l;
   }
-  if (quarter > 0) part[quarter - 1][tid & 255] = acc;
   __syncthreads();
   if (quarter > 0) return;
 #pragma unroll
-  for (int k = 0; k < 3; ++k) acc += part[k][tid];
-  float l = 0.f;
-#pragma unroll 8
-  for (int k = 0; k < K0; ++k) l += sum[k][col];
+  for (int k = 0; k < 3; ++k) add(stats[k][tid][0], stats[k][tid][1], part[k][tid]);
   const int q0 = start_at(p.q_starts, run.req, p.n_tok), n = start_at(p.q_starts, run.req + 1, p.n_tok) - q0;
   const int64_t row = (int64_t)run.block * (Q * RG) + Q * rg + col;
   if (row >= (int64_t)n * p.n_heads) return;
@@ -781,12 +784,9 @@ __global__ void __launch_bounds__(1024) latent_join_kernel(const LatentParams p,
   h.x = (uint32_t)T::from_f32(acc.x * r) | ((uint32_t)T::from_f32(acc.y * r) << 16);
   h.y = (uint32_t)T::from_f32(acc.z * r) | ((uint32_t)T::from_f32(acc.w * r) << 16);
   *reinterpret_cast<mx_u32x2*>(p.out + (int64_t)(q0 + token) * p.out_stride + (int64_t)head * kLat + 16 * b + 4 * grp) = h;
-  if (b == 0 && grp == 0 && p.lse) {
-    float top = -INFINITY;
-    for (int k = 0; k < K0; ++k) top = fmaxf(top, most[k][col]);
+  if (b == 0 && grp == 0 && p.lse)
     p.lse[(int64_t)(q0 + token) * p.n_heads + head] =
-        l == 0.f ? -INFINITY : (top - Mma<T>::kLift + __builtin_amdgcn_logf(l)) * 0.693147180559945309f;
-  }
+        l == 0.f ? -INFINITY : (m - Mma<T>::kLift + __builtin_amdgcn_logf(l)) * 0.693147180559945309f;
 }
 
 // Queries of a wavefront and row groups of a workgroup, by the rows of an average request: few rows leave key groups to the other
