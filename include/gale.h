@@ -515,6 +515,7 @@ int gale_add_rms_norm(const void* x, int64_t x_stride, const void* residual, int
 #define GALE_MAX_BLOCK_SIZE 1024
 #define GALE_MAX_REQUESTS  65536
 #define GALE_MAX_HEADS      1024
+#define GALE_MAX_KEYS 2147482624 /* positions that a row of a block table spans: 2^31 - 1024 */
 #define GALE_MAX_KEY_STRIDE 16777208 /* elements between tokens of k, k_rope and v in the expanded form */
 
 typedef struct {
@@ -564,16 +565,19 @@ size_t gale_latent_workspace_bytes(int32_t n_tok, int32_t n_req, int32_t n_heads
  *   s_j = scale * (a . c_j + b . r_j),   w = softmax(s),   out = sum_j w_j c_j,   lse = log(sum_j exp(s_j)).
  * Query i of a request's n sees keys j <= kv_len - n + i when causal != 0, else all kv_len.  A key whose block id is outside
  * [0, n_blocks) is not seen.  What a query does not see has no influence on it, NaN included; a query that sees no key
- * gets out = 0 and lse = -infinity.  kv_lens outside [0, max_blocks * block_size] are clamped to it.  Products are exact and
- * summed in fp32; the weights are rounded to the queries' type for the second product, relative to a running maximum,
- * and normalised in fp32 (sums of weights times values past fp32's range, values above 2^90, are infinite); 4-bit latents are
- * read as numbers of the queries' type, gale_mx_dequantize's rounding.
+ * gets out = 0 and lse = -infinity; one that sees a latent, or has a score, that is not finite gets NaN, or what the formula
+ * gives.  kv_lens outside [0, max_blocks * block_size] are clamped to it, and max_blocks * block_size <= GALE_MAX_KEYS.
+ * Products are exact and summed in fp32; the weights are rounded to the queries' type for the second product, relative to a
+ * running maximum that is at most 2^8 below the true one, and normalised in fp32: their sums with bf16 values pass fp32's
+ * range, and are infinite, where a value times the number of keys does.  4-bit latents are read as numbers of the queries'
+ * type, gale_mx_dequantize's rounding.
  * q: [n_tok] tokens, q_stride elements apart, of n_heads rows of GALE_LATENT_DIM + GALE_LATENT_ROPE values of the cache's
  * dtype; out: [n_tok] tokens, out_stride elements apart, of n_heads rows of GALE_LATENT_DIM; both 16-byte aligned with
  * strides of whole 16 bytes.  lse: fp32 [n_tok][n_heads], or NULL.  block_table: as gale_paged_plan's; q_starts: int32
  * [n_req + 1], ascending from 0, values outside [0, n_tok] are clamped; tokens from q_starts[n_req] on are left as they
  * were.  n_heads <= GALE_MAX_HEADS, n_tok * n_heads < 2^31, n_req <= GALE_MAX_REQUESTS; n_req and n_tok may be 0.  ws: 256-byte
- * aligned; nothing in it lives from call to call.  Equal calls give equal bits. */
+ * aligned; nothing in it lives from call to call, and calls that may run at the same time need one each.  Equal calls give
+ * equal bits. */
 int gale_latent_attention(const gale_latent_cache* cache, const int32_t* block_table, int64_t table_stride,
                           int32_t max_blocks, const int32_t* kv_lens, const int32_t* q_starts, int32_t n_req,
                           const void* q, int64_t q_stride, int32_t n_tok, int32_t n_heads, float scale, int32_t causal,
@@ -587,8 +591,9 @@ int gale_latent_attention(const gale_latent_cache* cache, const int32_t* block_t
  * k_stride and v_stride apart, of n_heads rows of GALE_HEAD_NOPE and GALE_HEAD_VALUE values, k_head_stride and v_head_stride apart
  * (both may lie in one product's output); k_rope: [n_kv] rows of GALE_LATENT_ROPE; out: [n_tok] tokens of
  * n_heads rows of GALE_HEAD_VALUE; all of dtype (GALE_F16 or GALE_BF16), strides in elements, 16-byte aligned with strides of
- * whole 16 bytes, those between tokens of k, k_rope and v at most GALE_MAX_KEY_STRIDE.  lse: fp32 [n_tok][n_heads], or NULL.  q_starts, kv_starts: int32 [n_req + 1], ascending from 0, clamped
- * to [0, n_tok] and [0, n_kv]; tokens from q_starts[n_req] on are left as they were. */
+ * whole 16 bytes, those between tokens of k, k_rope and v at most GALE_MAX_KEY_STRIDE.  lse: fp32 [n_tok][n_heads], or NULL.
+ * q_starts, kv_starts: int32 [n_req + 1], ascending from 0, clamped to [0, n_tok] and [0, n_kv]; tokens from q_starts[n_req] on
+ * are left as they were. */
 int gale_latent_attention_expanded(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                                    int64_t k_head_stride, const void* k_rope, int64_t k_rope_stride, const void* v,
                                    int64_t v_stride, int64_t v_head_stride, int32_t dtype, int32_t n_tok, int32_t n_kv,

@@ -16,7 +16,7 @@ from .binding import (  # noqa: F401
     GALE_BF16, GALE_MX_E2M1, GALE_MX_E4M3, GALE_MX_BLOCK, GALE_MX_GROUP, GALE_SCORE_SOFTMAX, GALE_SCORE_SIGMOID,
     GALE_GROUP_MAX, GALE_GROUP_TOP2, MXTensor, mx_quantize, mx_swiglu_quantize, mx_dequantize, mx_gemm, add_rms_norm,
     route_scored, moe_layer_fwd_given,
-    GALE_LATENT_DIM, GALE_LATENT_ROPE, GALE_HEAD_NOPE, GALE_HEAD_VALUE, GALE_MAX_BLOCK_SIZE, LatentCache, paged_plan,
+    GALE_LATENT_DIM, GALE_LATENT_ROPE, GALE_HEAD_NOPE, GALE_HEAD_VALUE, GALE_MAX_BLOCK_SIZE, GALE_MAX_KEYS, LatentCache, paged_plan,
     latent_append, latent_workspace_bytes, latent_attention, latent_attention_expanded,
 )
 from .pack_files import Pack, PackWriter, LoadedStack, load_stack, read_manifest  # noqa: F401,E402

@@ -25,6 +25,7 @@ GALE_SCORE_SOFTMAX, GALE_SCORE_SIGMOID = 1, 2
 GALE_GROUP_MAX, GALE_GROUP_TOP2 = 1, 2
 GALE_LATENT_DIM, GALE_LATENT_ROPE, GALE_HEAD_NOPE, GALE_HEAD_VALUE = 512, 64, 128, 128
 GALE_MAX_BLOCK_SIZE = 1024
+GALE_MAX_KEYS = 2147482624
 GALE_X_ROTATED = 0x1
 GALE_X_PREPARED = 0x2
 GALE_PATH_DECODE = 0x10

@@ -1196,8 +1196,8 @@ extern "C" int gale_latent_attention(const gale_latent_cache* cache, const int32
   const int st = check_cache(fn, cache, c);
   if (st) return st;
   const int64_t ql = (int64_t)n_heads * (GALE_LATENT_DIM + GALE_LATENT_ROPE), ol = (int64_t)n_heads * GALE_LATENT_DIM;
-  if (!attention_sizes_ok(n_tok, n_req, n_heads) || max_blocks < 0 || table_stride < max_blocks || q_stride < ql ||
-      out_stride < ol) {
+  if (!attention_sizes_ok(n_tok, n_req, n_heads) || max_blocks < 0 || (int64_t)max_blocks * cache->block_size > GALE_MAX_KEYS ||
+      table_stride < max_blocks || q_stride < ql || out_stride < ol) {
     set_error("%s: n_tok=%d n_req=%d n_heads=%d max_blocks=%d strides %lld (table), %lld (q), %lld (out)", fn, n_tok, n_req,
               n_heads, max_blocks, (long long)table_stride, (long long)q_stride, (long long)out_stride);
     return GALE_ERR_SHAPE;

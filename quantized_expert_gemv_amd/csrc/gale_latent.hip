@@ -130,6 +130,7 @@ latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
       if (lane >= d) scan += x, rscan += y;
     }
     if (lane == 63) part[wave] = scan, runs_of[wave] = rscan;
+    if (tid == 0) found[0] = -1;
     __syncthreads();
     int64_t total = 0;
     int total_runs = 0;
@@ -171,6 +172,7 @@ latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
     }
     __syncthreads();
     req = __builtin_amdgcn_readfirstlane(found[0]);
+    if (req < 0) return;      // only where q_starts does not ascend
     run_base = __builtin_amdgcn_readfirstlane(found[1]);
     base = uniform64(*(int64_t*)(found + 2));
     __syncthreads();      // the tiles take the place
@@ -192,7 +194,7 @@ latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
     if (u >= base + (int64_t)blocks * units) {      // also requests without queries
       base += (int64_t)blocks * units;
       run_base += blocks;
-      ++req;
+      if (++req == p.n_req) return;      // likewise
       continue;
     }
     const int block = __builtin_amdgcn_readfirstlane((int)divide(u - base, units));
@@ -728,7 +730,7 @@ latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
     }
     if (a0 == 0 && tid == 0) {
       const int first = (int)blockIdx.x, at = by_run ? run_base + block : first;
-      if (at < kGroups)       // always, where q_starts ascends
+      if ((unsigned)at < kGroups)       // always, where q_starts ascends
         ws.runs[at] = Run{whole ? 0 : (int)divide(run0 + units - 1, part_units) - first + 1, first, req, block};
     }
     u = run0 + lead + a1;

@@ -13,38 +13,32 @@ constexpr int kNope = GALE_HEAD_NOPE, kValue = GALE_HEAD_VALUE, kQuery = kNope +
 constexpr int kBq = 128, kBk = 64;
 constexpr int kTileK = kBk * 256, kTileR = kBk * 128, kTileV = kBk * 256, kTile = kTileK + kTileR + kTileV;
 
-// (request, its first block) of block number `idx` of the batch's blocks of kBq queries; n_req if there is none.
-__device__ __forceinline__ void find_block(const int32_t* starts, int n_req, int n_tok, int idx, int* part, int& req, int& first) {
-  req = n_req;
-  first = 0;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int r0 = 0; r0 < n_req; r0 += 256) {
-    const int r = r0 + (int)threadIdx.x;
-    int n = 0;
-    if (r < n_req) n = (max(0, start_at(starts, r + 1, n_tok) - start_at(starts, r, n_tok)) + kBq - 1) / kBq;
-    int sum = n;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int u = __shfl_up(sum, d);
-      if (lane >= d) sum += u;
+// Blocks of a batch: request r's begin at number start_r / kBq + r, which is at most one number more than its blocks behind the
+// request before it, so a block's request is found by a search in the starts alone: 64 places at a time, one round of loads
+// for up to 64 requests and three for the most.  Every wavefront does it by itself.
+struct Found {
+  int q0, n, k0, keys, block;
+};
+__device__ __forceinline__ bool find_block(const PromptParams& p, int idx, Found& f) {
+  const int lane = threadIdx.x & 63;
+  for (int lo = 0, hi = p.n_req;;) {
+    const int step = (hi - lo + 63) >> 6, r = lo + lane * step, at = min(r, p.n_req - 1);
+    const int q = start_at(p.q_starts, at, p.n_tok), q1 = start_at(p.q_starts, at + 1, p.n_tok);
+    const int k = start_at(p.kv_starts, at, p.n_kv), k1 = start_at(p.kv_starts, at + 1, p.n_kv);
+    const uint64_t ahead = __ballot(r < hi && q / kBq + r <= idx);
+    if (ahead == 0) return false;
+    const int last = 63 - __builtin_clzll(ahead);
+    if (step > 1) {
+      lo += last * step;
+      hi = min(hi, lo + step);
+      continue;
     }
-    __syncthreads();
-    if (lane == 63) part[wave] = sum;
-    if (threadIdx.x == 0) part[4] = -1;
-    __syncthreads();
-    sum += first;
-    for (int w = 0; w < wave; ++w) sum += part[w];
-    if (n > 0 && sum - n <= idx && idx < sum) {
-      part[4] = r;
-      part[5] = sum - n;
-    }
-    __syncthreads();
-    if (part[4] >= 0) {
-      req = part[4];
-      first = part[5];
-      return;
-    }
-    first += part[0] + part[1] + part[2] + part[3];
+    f.q0 = __builtin_amdgcn_readlane(q, last);
+    f.n = __builtin_amdgcn_readlane(q1, last) - f.q0;
+    f.k0 = __builtin_amdgcn_readlane(k, last);
+    f.keys = max(0, __builtin_amdgcn_readlane(k1, last) - f.k0);
+    f.block = idx - (f.q0 / kBq + lo + last);
+    return (int64_t)f.block * kBq < f.n;
   }
 }
 
@@ -58,16 +52,13 @@ __global__ void __launch_bounds__(256, 2) prompt_kernel(const PromptParams p, in
   // Workgroups go round robin over the 8 XCDs: each XCD gets a contiguous run of (head, block), so the blocks that read
   // one head's keys share an L2; within a head the blocks with the most keys come first.
   const int total = n_blocks * p.n_heads, per = total >> 3, rest = total & 7;
-  const int xcd = blockIdx.x & 7, item = xcd * per + min(xcd, rest) + (int)(blockIdx.x >> 3);
-  const int head = item / n_blocks, idx = n_blocks - 1 - (item - head * n_blocks);
-  int req, first;
-  find_block(p.q_starts, p.n_req, p.n_tok, idx, (int*)tiles, req, first);     // two buffers are all of half a CU's LDS
-  if (req == p.n_req) return;
-  __syncthreads();
-  req = __builtin_amdgcn_readfirstlane(req);
-  const int q0 = start_at(p.q_starts, req, p.n_tok), n = start_at(p.q_starts, req + 1, p.n_tok) - q0;
-  const int k0 = start_at(p.kv_starts, req, p.n_kv), keys = max(0, start_at(p.kv_starts, req + 1, p.n_kv) - k0);
-  const int b0 = __builtin_amdgcn_readfirstlane((idx - first) * kBq);
+  const int64_t place = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  if (place >= total) return;
+  const int xcd = (int)place & 7, item = xcd * per + min(xcd, rest) + (int)(place >> 3);
+  const int head = item / n_blocks;
+  Found f;
+  if (!find_block(p, n_blocks - 1 - (item - head * n_blocks), f)) return;
+  const int q0 = f.q0, n = f.n, k0 = f.k0, keys = f.keys, b0 = f.block * kBq;
   const int qi = b0 + 32 * wave + col;                        // this lane's query
   const int gap = keys - n;
   const int seen = qi >= n ? 0 : p.causal ? max(0, min(keys, gap + qi + 1)) : keys;
@@ -243,9 +234,10 @@ __global__ void __launch_bounds__(256, 2) prompt_kernel(const PromptParams p, in
 }
 
 hipError_t launch_prompt_attention(const PromptParams& p, int dtype, hipStream_t s) {
-  // every request has at most one block more than its share of the tokens
-  const int64_t blocks = std::min<int64_t>(((int64_t)p.n_tok + kBq - 1) / kBq + p.n_req - 1, p.n_tok);
-  const dim3 grid((unsigned)(blocks * p.n_heads));
+  const int64_t blocks = (int64_t)p.n_tok / kBq + p.n_req, total = blocks * p.n_heads;
+  // a dimension of a grid is less than 2^32 threads
+  const unsigned x = (unsigned)std::min<int64_t>(total, 1 << 23);
+  const dim3 grid(x, (unsigned)((total + x - 1) / x));
   if (dtype == GALE_F16) hipLaunchKernelGGL(prompt_kernel<F16>, grid, dim3(256), 0, s, p, (int)blocks);
   else hipLaunchKernelGGL(prompt_kernel<BF16>, grid, dim3(256), 0, s, p, (int)blocks);
   return hipGetLastError();

@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(256) paged_plan_kernel(
     __syncthreads();
     // the workgroup's own tokens among this turn's
     const int lo = (int)max((int64_t)t0, min(turn_first, (int64_t)n_tok)), hi = (int)min((int64_t)t1, tok0);
-    for (int t = lo + (int)threadIdx.x; t < hi; t += 256) {
+    for (int64_t t = lo + (int64_t)threadIdx.x; t < hi; t += 256) {
       int a = 0, b = kPlanTurn - 1;                           // the first request that ends behind t
       while (a < b) {
         const int m = (a + b) >> 1;
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(256) paged_plan_kernel(
       const int begin = a ? s_end[a - 1] : (int)turn_first;
       int64_t slot = -1;
       if (s_base[a] >= 0) {
-        const int64_t pos = (int64_t)s_past[a] + (t - begin);
+        const int64_t pos = s_past[a] + (t - begin);
         const int64_t blk = pos >> shift, have = ((int64_t)s_past[a] + mask) >> shift;
         int32_t* entry = table + (int64_t)(r0 + a) * table_stride + blk;
         int32_t id;
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(256) paged_plan_kernel(
     const int grid = (int)gridDim.x, next = turn + 1 + ((int)blockIdx.x - (turn + 1) % grid + grid) % grid;
     if (tok0 >= t1 && !last_group && (int64_t)next * kPlanTurn >= n_req) return;
   }
-  for (int t = (int)max((int64_t)t0, min(tok0, (int64_t)n_tok)) + (int)threadIdx.x; t < t1; t += 256) slots[t] = -1;
+  for (int64_t t = max((int64_t)t0, min(tok0, (int64_t)n_tok)) + threadIdx.x; t < t1; t += 256) slots[t] = -1;
   if (last_group) {
     (void)block_scan(used, part, total);
     if (threadIdx.x == 0) {
@@ -150,34 +150,35 @@ __global__ void __launch_bounds__(256) latent_append_kernel(const uint16_t* __re
                                                             uint8_t* __restrict__ scales, uint8_t* __restrict__ r,
                                                             int64_t r_bytes) {
   const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (t >= n_tok) return;
-  const uint16_t* src = latent + t * latent_stride;
-  const mx_u32x4 a = *reinterpret_cast<const mx_u32x4*>(src + 8 * lane);
-  mx_u32x4 b = {0, 0, 0, 0};
-  if (lane < 8) b = *reinterpret_cast<const mx_u32x4*>(rope + t * rope_stride + 8 * lane);
-  const int64_t slot = slots[t];
-  if (slot < 0 || slot >= n_slots) return;
-  if constexpr (MX) {
-    float v[8];
+  for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < n_tok; t += (int64_t)gridDim.x * 4) {
+    const uint16_t* src = latent + t * latent_stride;
+    const mx_u32x4 a = *reinterpret_cast<const mx_u32x4*>(src + 8 * lane);
+    mx_u32x4 b = {0, 0, 0, 0};
+    if (lane < 8) b = *reinterpret_cast<const mx_u32x4*>(rope + t * rope_stride + 8 * lane);
+    const int64_t slot = slots[t];
+    if (slot < 0 || slot >= n_slots) continue;
+    if constexpr (MX) {
+      float v[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = T::to_f32((uint16_t)(a[i] & 0xFFFFu));
-      v[2 * i + 1] = T::to_f32((uint16_t)(a[i] >> 16));
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = T::to_f32((uint16_t)(a[i] & 0xFFFFu));
+        v[2 * i + 1] = T::to_f32((uint16_t)(a[i] >> 16));
+      }
+      uint32_t words[2];
+      const uint32_t s = mx_encode8<GALE_MX_E2M1>(v, words);
+      mx_store8<GALE_MX_E2M1>(c + slot * (GALE_LATENT_DIM / 2), scales + slot * (GALE_LATENT_DIM / 32), lane, s, words);
+    } else {
+      *reinterpret_cast<mx_u32x4*>(c + slot * c_bytes + 16 * lane) = a;
     }
-    uint32_t words[2];
-    const uint32_t s = mx_encode8<GALE_MX_E2M1>(v, words);
-    mx_store8<GALE_MX_E2M1>(c + slot * (GALE_LATENT_DIM / 2), scales + slot * (GALE_LATENT_DIM / 32), lane, s, words);
-  } else {
-    *reinterpret_cast<mx_u32x4*>(c + slot * c_bytes + 16 * lane) = a;
+    if (lane < 8) *reinterpret_cast<mx_u32x4*>(r + slot * r_bytes + 16 * lane) = b;
   }
-  if (lane < 8) *reinterpret_cast<mx_u32x4*>(r + slot * r_bytes + 16 * lane) = b;
 }
 
 hipError_t launch_latent_append(const gale_latent_cache& c, const void* latent, int64_t latent_stride, const void* rope,
                                 int64_t rope_stride, const int64_t* slots, int n_tok, hipStream_t s) {
+  const unsigned grid = (unsigned)std::min<int64_t>(((int64_t)n_tok + 3) / 4, 1 << 23);      // a grid has less than 2^32 threads
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)(((int64_t)n_tok + 3) / 4)), dim3(256), 0, s, (const uint16_t*)latent, latent_stride,
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), 0, s, (const uint16_t*)latent, latent_stride,
                        (const uint16_t*)rope, rope_stride, slots, n_tok, c.n_blocks * c.block_size, (uint8_t*)c.latent,
                        2 * c.latent_stride, c.scales, (uint8_t*)c.rope, 2 * c.rope_stride);
     return hipGetLastError();

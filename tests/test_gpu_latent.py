@@ -676,3 +676,82 @@ def test_a_layer_runs_together(q):
     assert taken.item() == 1 and keys.tolist() == [38, 65, 2]
     q.latent_append(cache, c1, kr1, slots)
     check_latent(q, cache, x1, table.cpu().numpy(), [0, 1, 2, 3], [38, 65, 2])
+
+
+# ---- the largest calls: sizes at which a grid dimension, or a 32-bit place, would pass its range -----------------------------
+def room(gib):
+    if torch.cuda.mem_get_info()[0] < gib * 2 ** 30:
+        pytest.skip(f"{gib} GiB of device memory are not free")
+
+
+@pytest.mark.parametrize("R", [63, 64, 65, 4096, 4097, 20000])
+def test_prompts_of_thousands_of_requests(q, R):
+    rng = np.random.default_rng(R)
+    lens = rng.choice([0, 0, 0, 1, 2, 3, 128, 129] if R < 1000 else [0, 0, 1, 1, 2, 3, 5, 129], R).tolist()
+    keys = [n + int(rng.integers(0, 3)) for n in lens]
+    args = prompts(lens, keys, 1, torch.bfloat16, R)
+    T = args[4][-1]
+    check_prompt(q, *args, tokens={0, T - 1, *map(int, rng.integers(0, T, 100))})
+
+
+def test_prompts_of_more_workgroups_than_a_grid_dimension_holds(q):
+    room(40)
+    R, H = 16400, 1024                                                   # 2^24 workgroups of 256 threads are 2^32 threads
+    x = torch.zeros((R, H, 192), dtype=torch.float16, device=DEV)
+    k, v, kr = rand((3, H, 128), 1, torch.float16), rand((3, H, 128), 2, torch.float16), rand((3, 64), 3, torch.float16)
+    starts = torch.arange(R + 1, dtype=torch.int32, device=DEV)
+    kstarts = torch.zeros(R + 1, dtype=torch.int32, device=DEV)
+    kstarts[R // 2 + 1:] = 1                                             # one key for the request in the middle, two for the last
+    kstarts[R] = 3
+    out, lse = q.latent_attention_expanded(x, k, kr, v, starts, kstarts, SCALE, causal=False)
+    some = torch.ones(R, dtype=torch.bool, device=DEV)
+    some[R // 2] = some[R - 1] = False
+    assert (lse[some] == -math.inf).all() and not out[some].any()
+    assert torch.equal(out[R // 2], v[0]) and lse[R // 2].abs().max() <= 2 ** -18
+    # equal scores: the mean of two values, rounded once (their sum is exact in fp32)
+    assert torch.equal(out[R - 1], (v[1:].float().sum(0) / 2).half()) and torch.allclose(lse[R - 1], torch.tensor(math.log(2.0)).to(DEV))
+
+
+def test_append_of_more_tokens_than_a_grid_dimension_holds(q):
+    room(100)
+    n = 2 ** 26 + 5                                                      # a wavefront of 64 each: past 2^32 threads
+    cache = filled(q, 2, 16, torch.bfloat16, False, 1)
+    x = torch.empty((n, 576), dtype=torch.bfloat16, device=DEV)
+    slots = torch.full((n,), -1, dtype=torch.int64, device=DEV)
+    want = [cache.latent.clone(), cache.rope.clone()]
+    for i, (t, slot) in enumerate([(0, 3), (n // 2, 30), (n - 1, 17)]):
+        x[t] = rand((576,), 7 + i, torch.bfloat16)
+        slots[t] = slot
+        want[0][slot], want[1][slot] = x[t, :512], x[t, 512:]
+    q.latent_append(cache, x[:, :512], x[:, 512:], slots)
+    assert torch.equal(cache.latent, want[0]) and torch.equal(cache.rope, want[1])
+
+
+def test_plan_of_the_most_places(q):
+    room(40)
+    n = 2 ** 31 - 1
+    table = torch.full((2, 3), -1, dtype=torch.int32, device=DEV)
+    slots, starts, keys, taken = q.paged_plan(i32([0, 5]), i32([3, 70]), i32([9, 4, 6]), i32([3]), table, 64, n)
+    assert slots[:3].tolist() == [576, 577, 578] and starts.tolist() == [0, 3, 73] and keys.tolist() == [3, 75]
+    assert taken.tolist() == [2] and table.tolist() == [[9, -1, -1], [-1, 4, -1]]
+    assert slots.numel() == n and all((slots[a: a + 2 ** 28] == -1).all() for a in range(73, n, 2 ** 28))
+
+
+def test_the_longest_row_of_a_block_table(q):
+    """2^31 - 1024 positions: all in one block of zeros but for the last block, whose last key has score 40."""
+    n, bs = q.GALE_MAX_KEYS, 1024
+    latent = torch.zeros((2 * bs, 512), dtype=torch.bfloat16, device=DEV)
+    rope = torch.zeros((2 * bs, 64), dtype=torch.bfloat16, device=DEV)
+    latent[-1] = rand((512,), 1, torch.bfloat16)
+    rope[-1, 0] = 5
+    cache = q.LatentCache(latent, rope, bs)
+    table = torch.zeros((1, n // bs), dtype=torch.int32, device=DEV)
+    table[0, -1] = 1
+    x = torch.zeros((1, 1, 576), dtype=torch.bfloat16, device=DEV)
+    x[0, 0, 512] = 8
+    out, lse = q.latent_attention(x, cache, table, i32([0, 1]), i32([n]), 1.0)
+    # the others' share is 2^31 exp(-40) < 2^-26 of the sum: below half a step of bf16 and of lse
+    assert torch.equal(out[0, 0], latent[-1]) and abs(lse.item() - 40) <= 2 ** -18 * 41
+    out, lse = q.latent_attention(x, cache, table, i32([0, 1]), i32([n - 1]), 1.0)
+    # a lane adds fours, 2^-8 of them, up to 2^17 times: exact; what joins them and the logarithm: the bound above
+    assert not out.any() and abs(lse.item() - math.log(n - 1)) <= 2 ** -18 * (1 + math.log(n - 1))

@@ -219,3 +219,11 @@ def test_binding_refusals():
                 lambda: q.latent_attention_expanded(x[..., :192], x[..., :128], rope[:3], x[..., :127], i32(2), i32(2), 1.0)):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_attention_refuses_tables_past_the_last_position():
+    need = q.latent_workspace_bytes(1, 1, 16)
+    wide = q.GALE_MAX_KEYS // 64 + 1
+    good = [_cache(), F + 40 * MB, 8, 8, F + 41 * MB, F + 42 * MB, 1, F + 43 * MB, 16 * 576, 1, 16, 0.1, 1, F + 44 * MB, 16 * 512,
+            None, F + 46 * MB, need, None]
+    _refused("gale_latent_attention", good, [(SHAPE, {2: wide, 3: wide})])
