@@ -1,4 +1,5 @@
 // Latent attention of prompts, expanded form.
+#include <climits>
 #include <type_traits>
 
 #include "gale_latent.h"
@@ -10,15 +11,69 @@ constexpr int kNope = GALE_HEAD_NOPE, kValue = GALE_HEAD_VALUE, kQuery = kNope +
 // A workgroup takes 128 queries of one head, 32 to each wavefront, and walks the keys in tiles of 64 with a running maximum
 // and sum.  The tiles (keys' own parts, rope rows, values: 40 KB) come by direct copies into two LDS buffers, the next one's
 // during the products of this one, so two workgroups share a CU and one's softmax runs beside the other's products.
-constexpr int kBq = 128, kBk = 64;
+constexpr int kBq = 128, kBk = 64, kHeads = 8;
 constexpr int kTileK = kBk * 256, kTileR = kBk * 128, kTileV = kBk * 256, kTile = kTileK + kTileR + kTileV;
 
-// Blocks of a batch: request r's begin at number start_r / kBq + r, which is at most one number more than its blocks behind the
-// request before it, so a block's request is found by a search in the starts alone: 64 places at a time, one round of loads
-// for up to 64 requests and three for the most.  Every wavefront does it by itself.
 struct Found {
   int q0, n, k0, keys, block;
 };
+__device__ __forceinline__ int wave_sum(int v) {
+  v += lane_xor<1>(v);
+  v += lane_xor<2>(v);
+  v += lane_xor<4>(v);
+  v += lane_xor<8>(v);
+  v += lane_xor<16>(v);
+  v += lane_xor<32>(v);
+  return __builtin_amdgcn_readfirstlane(v);
+}
+
+// Up to 64 requests, a lane for each: blocks go by the number of keys that they look at, in steps of kBq, most first, so that the
+// grid ends with short ones (12 prompts of 20 to 2000 tokens, 32 heads: 352 us; in the order of the batch 371).  Of a request whose
+// last block has level ceil(keys / kBq), blocks of level `at` and more are as many as the last of them: N(at) over the
+// requests falls with `at`, and a binary search finds the level that the rank lies in.
+__device__ __forceinline__ bool find_by_length(const PromptParams& p, int rank, Found& f) {
+  const int lane = threadIdx.x & 63, r = min(lane, p.n_req - 1);
+  const int q0 = start_at(p.q_starts, r, p.n_tok), q1 = start_at(p.q_starts, r + 1, p.n_tok);
+  const int k0 = start_at(p.kv_starts, r, p.n_kv), k1 = start_at(p.kv_starts, r + 1, p.n_kv);
+  const int n = lane < p.n_req ? max(0, q1 - q0) : 0, keys = max(0, k1 - k0);
+  const int blocks = n / kBq + (n % kBq != 0), top = keys / kBq + (keys % kBq != 0);
+  const int back = p.causal ? (n - keys) >> 7 : INT_MIN / 2;      // floor: block j's level is more than j - back, where it has keys
+  auto from = [&](int at) { return at <= 0 ? blocks : top < at ? 0 : blocks - min(max(at - 1 + back, 0), blocks); };
+  if (rank >= wave_sum(blocks)) return false;
+  int lo = 0, hi = n > 0 ? top : 0, behind = 0;      // N(lo) > rank >= N(hi) = behind
+  hi = max(hi, lane_xor<1>(hi));
+  hi = max(hi, lane_xor<2>(hi));
+  hi = max(hi, lane_xor<4>(hi));
+  hi = max(hi, lane_xor<8>(hi));
+  hi = max(hi, lane_xor<16>(hi));
+  hi = __builtin_amdgcn_readfirstlane(max(hi, lane_xor<32>(hi))) + 1;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1, count = wave_sum(from(mid));
+    if (count > rank) lo = mid;
+    else hi = mid, behind = count;
+  }
+  const int mine = from(lo) - from(hi);
+  int sum = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int u = __shfl_up(sum, d);
+    if (lane >= d) sum += u;
+  }
+  const int at = rank - behind, place = at - (sum - mine);
+  const uint64_t here = __ballot(place >= 0 && place < mine);
+  if (here == 0) return false;
+  const int it = __builtin_ctzll(here);
+  f.q0 = __builtin_amdgcn_readlane(q0, it);
+  f.n = __builtin_amdgcn_readlane(n, it);
+  f.k0 = __builtin_amdgcn_readlane(k0, it);
+  f.keys = __builtin_amdgcn_readlane(keys, it);
+  f.block = __builtin_amdgcn_readlane(blocks - from(lo) + place, it);
+  return true;
+}
+
+// More requests: request r's blocks begin at number start_r / kBq + r, which is at most one number more than its blocks behind the
+// request before it, so a block's request is found by a search in the starts alone: 64 places at a time, two rounds of loads
+// for up to 4096 requests and three for the most.  Every wavefront does it by itself.
 __device__ __forceinline__ bool find_block(const PromptParams& p, int idx, Found& f) {
   const int lane = threadIdx.x & 63;
   for (int lo = 0, hi = p.n_req;;) {
@@ -49,15 +104,15 @@ __global__ void __launch_bounds__(256, 2) prompt_kernel(const PromptParams p, in
   const int tid = threadIdx.x, lane = tid & 63, col = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
-  // Workgroups go round robin over the 8 XCDs: each XCD gets a contiguous run of (head, block), so the blocks that read
-  // one head's keys share an L2; within a head the blocks with the most keys come first.
-  const int total = n_blocks * p.n_heads, per = total >> 3, rest = total & 7;
+  // Workgroups go round robin over the 8 XCDs: of kHeads heads at a time an XCD takes one, so the blocks that read one head's keys
+  // share an L2 (those prompts: 0.94 GB from memory; 32 heads at a time 1.5 GB and 359 us, 16 362 us).
   const int64_t place = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
-  if (place >= total) return;
-  const int xcd = (int)place & 7, item = xcd * per + min(xcd, rest) + (int)(place >> 3);
-  const int head = item / n_blocks;
+  if (place >= (int64_t)n_blocks * p.n_heads) return;
+  const int group = (int)(place / ((int64_t)n_blocks * kHeads)), width = min(kHeads, p.n_heads - group * kHeads);
+  const int inside = (int)(place - (int64_t)group * n_blocks * kHeads), idx = inside / width;
+  const int head = group * kHeads + inside - idx * width;
   Found f;
-  if (!find_block(p, n_blocks - 1 - (item - head * n_blocks), f)) return;
+  if (p.n_req <= 64 ? !find_by_length(p, idx, f) : !find_block(p, n_blocks - 1 - idx, f)) return;
   const int q0 = f.q0, n = f.n, k0 = f.k0, keys = f.keys, b0 = f.block * kBq;
   const int qi = b0 + 32 * wave + col;                        // this lane's query
   const int gap = keys - n;
