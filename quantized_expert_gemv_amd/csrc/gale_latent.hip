@@ -1,6 +1,7 @@
 // Latent attention over a paged cache, absorbed form.
 #include <climits>
 #include <cmath>
+#include <cstdint>
 
 #include "gale_latent.h"
 
@@ -260,12 +261,11 @@ latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
     w_all = __builtin_amdgcn_readfirstlane(w_all);
     // C = 2: wavefronts meet within a tile, so all take the same ones
     if (C == 2) w_keys = keys;
-    // keys that all queries of the run see, where some see more
+    // keys that all queries of the run see, where there are more
     int some = INT_MAX;
     if (p.causal) {
       const int t0 = (int)((int64_t)block * Sh::ROWS / p.n_heads);
-      const int t1 = (int)((min(rows, (int64_t)(block + 1) * Sh::ROWS) - 1) / p.n_heads);
-      if (t0 < t1) some = __builtin_amdgcn_readfirstlane(max(0, keys - n + t0 + 1));
+      if (t0 < n - 1) some = __builtin_amdgcn_readfirstlane(max(0, keys - n + t0 + 1));
     }
 
     // keys that this lane's query g sees: needed in the last tiles only, so it is not kept
@@ -488,7 +488,7 @@ latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
       }
       __builtin_amdgcn_sched_barrier(0);
     };
-    // A product takes the weight 0 of a key that a query does not see times its value, and NaN times 0 is NaN.  So where only some
+    // A product takes the weight 0 of a key that a query does not see times its value, and NaN times 0 is NaN.  So where not all
     // of the run's queries see a key (j >= some), rows of a tile that are not finite are zeroed by the wavefront that fetched them, and
     // the queries that see such a key have NaN as their sum of weights.
     auto clear = [&](int j0, lds_u8* at) __attribute__((always_inline)) {
@@ -791,18 +791,31 @@ __global__ void __launch_bounds__(1024) latent_join_kernel(const LatentParams p,
         l == 0.f ? -INFINITY : (m - Mma<T>::kLift + __builtin_amdgcn_logf(l)) * 0.693147180559945309f;
 }
 
-// Queries of a wavefront and row groups of a workgroup, by the rows of an average request: few rows leave key groups to the other
-// wavefronts, many share each tile.
-static int run_rows(int n_tok, int n_req, int n_heads) {
-  const int64_t rows = ((int64_t)n_tok * n_heads + std::max(n_req, 1) - 1) / std::max(n_req, 1);
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+// Rows of a run, by those of an average request, `rows`, and by the batch's units of 16 rows and 64 positions of the block table
+// (a wider table than the lengths need counts as long contexts).  Few units: the most workgroups and the least time until the first
+// product, though a tile is fetched by many; many: tiles that all rows of a run share.  us, bf16, 16-bit rows, 64-slot blocks:
+//   units (requests x rows, positions)          runs of 16      32      64     128 rows
+//     256 (4 x 32, 2048)                            20.3    24.7    27.4    37.4
+//    1024 (4 x 128, 2048)                           26.6    26.6    26.2    44.8
+//    2048 (16 x 32, 4096)                           36.8    33.1    38.0    56.8
+//    4096 (32 x 32, 4096)                           60.7    44.7    53.2    79.8
+//    8192 (32 x 64, 4096)                           108     66.5    59.9    80.1
+//    8192 (16 x 128, 4096)                          83.7    64.0    59.3    61.9
+//   16384 (32 x 128, 4096)                          195     112     96.4    84.1
+//    2048 (32 x 16, 4096)                           38.5    41.9    53.0    80.7
+static int run_rows(int n_tok, int n_req, int n_heads, int64_t positions) {
+  const int64_t reqs = std::max(n_req, 1), rows = ((int64_t)n_tok * n_heads + reqs - 1) / reqs;
+  const int64_t units = reqs * ((rows + 15) / 16) * std::min<int64_t>((positions + 63) / 64, 8193);
+  if (rows <= 16 || units <= 1024) return 16;
+  if (rows <= 32) return 32;
+  return rows <= 64 || units <= 8192 ? 64 : 128;
 }
 
 constexpr size_t kHead = 256, kRunBytes = (kGroups * sizeof(Run) + 255) & ~(size_t)255;
 static size_t stats_bytes(int rows) { return (size_t)2 * kGroups * rows * 2 * 4; }
 
 size_t latent_workspace_bytes(int n_tok, int n_req, int n_heads) {
-  const int rows = run_rows(n_tok, n_req, n_heads);
+  const int rows = run_rows(n_tok, n_req, n_heads, INT64_MAX - 63);      // the most that a table can ask for
   return kHead + kRunBytes + stats_bytes(rows) + (size_t)2 * kGroups * rows * kLat * 4;
 }
 
@@ -826,7 +839,7 @@ static hipError_t launch_latent(const LatentParams& p, void* mem, hipStream_t s)
 
 template <typename T, bool MX>
 static hipError_t launch_rows(const LatentParams& p, void* ws, hipStream_t s) {
-  const int rows = run_rows(p.n_tok, p.n_req, p.n_heads);
+  const int rows = run_rows(p.n_tok, p.n_req, p.n_heads, (int64_t)p.max_blocks << p.block_shift);
   return rows == 16   ? launch_latent<T, MX, 16, 1>(p, ws, s)
          : rows == 32 ? launch_latent<T, MX, 16, 2>(p, ws, s)
          : rows == 64 ? launch_latent<T, MX, 16, 4>(p, ws, s)

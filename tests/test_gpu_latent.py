@@ -755,3 +755,110 @@ def test_the_longest_row_of_a_block_table(q):
     out, lse = q.latent_attention(x, cache, table, i32([0, 1]), i32([n - 1]), 1.0)
     # a lane adds fours, 2^-8 of them, up to 2^17 times: exact; what joins them and the logarithm: the bound above
     assert not out.any() and abs(lse.item() - math.log(n - 1)) <= 2 ** -18 * (1 + math.log(n - 1))
+
+
+# ---- every way to cut a batch: a table of many columns counts as long contexts, whatever the lengths are -----------------------------
+class WideTables:
+    """The library, with block tables widened to 2^19 and more positions (their new entries are no blocks)."""
+
+    def __init__(self, q):
+        self.q = q
+
+    def __getattr__(self, name):
+        return getattr(self.q, name)
+
+    def latent_attention(self, x, cache, table, *args, **kw):
+        more = 64 * 8200 // cache.block_size
+        return self.q.latent_attention(x, cache, torch.nn.functional.pad(table, (0, more), value=-1), *args, **kw)
+
+
+@pytest.fixture(scope="module")
+def wide(q):
+    return WideTables(q)
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("dtype", T16)
+@pytest.mark.parametrize("heads", [5, 17, 32, 33, 64, 65, 128])
+def test_decode_in_every_split(wide, dtype, mx, heads):
+    lens, bs = (LENS if heads < 64 else LENS[::2]), 16 if heads % 2 else 4
+    table, starts, lens, n = batch(wide, lens, [1] * len(lens), bs, heads)
+    cache = filled(wide, n, bs, dtype, mx, 3, strided=heads == 17)
+    check_latent(wide, cache, rand((len(lens), heads, 576), 4, dtype), table, starts, lens)
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("heads", [1, 3, 16, 40, 128])
+def test_drafts_in_every_split(wide, mx, causal, heads):
+    test_drafts(wide, mx, causal, heads)
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("heads", [7, 16, 31, 61])                       # two tokens a request: 14, 32, 62, 122 rows
+def test_unseen_nan_in_every_split(wide, heads, mx):
+    q, bs = wide, 16
+    table, starts, lens, n = batch(q, [70, 40, 33], [3, 1, 2], bs, 3)
+    table[1, 1], table[2, 0] = -1, n + 5
+    cache = filled(q, n, bs, torch.bfloat16, mx, 13)
+    x = rand((6, heads, 576), 14, torch.bfloat16)
+    out, l = check_latent(q, cache, x, table, starts, lens)
+    bad = torch.ones(n * bs, dtype=torch.bool, device=DEV)
+    for i, m in enumerate(lens):
+        rows = table[i][np.arange(m) // bs] * bs + np.arange(m) % bs
+        bad[torch.tensor(rows[(rows >= 0) & (rows < n * bs)], device=DEV)] = False
+    late = [table[0][p // bs] * bs + p % bs for p in (68, 69)] + [table[2][32 // bs] * bs + 32 % bs]
+    bad[torch.tensor(late, device=DEV)] = True
+    if mx:
+        cache.latent.scales[bad] = 255
+    else:
+        cache.latent[bad] = math.nan
+    cache.rope[bad] = math.inf
+    out2, l2 = q.latent_attention(x, cache, i32(table), i32(starts), i32(lens), SCALE)
+    # what a query sees is what it was: the same products in the same tiles
+    for t in (0, 3, 4):
+        assert torch.equal(out2[t], out[t]) and torch.equal(l2[t], l[t])
+    for t in (1, 2, 5):
+        assert torch.isnan(out2[t]).any() and not torch.isfinite(l2[t]).any()
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("heads", [16, 32, 64, 128])
+def test_unseen_nan_where_a_run_is_one_token(wide, heads, mx):
+    """Three requests without tokens take the average to one: a run is a token's heads, and none of them sees the last keys."""
+    q, bs = wide, 64
+    table, starts, lens, n = batch(q, [70, 64, 200, 9, 9, 9], [3, 1, 2, 0, 0, 0], bs, 5)
+    cache = filled(q, n, bs, torch.bfloat16, mx, 15)
+    x = rand((6, heads, 576), 16, torch.bfloat16)
+    out, l = check_latent(q, cache, x, table, starts, lens)
+    late = torch.tensor([int(table[r][p // bs]) * bs + p % bs for r, p in ((0, 68), (0, 69), (2, 199))], device=DEV)
+    if mx:
+        cache.latent.scales[late] = 255
+    else:
+        cache.latent[late, 40] = -math.inf
+    cache.rope[late, 3] = math.nan
+    out2, l2 = q.latent_attention(x, cache, i32(table), i32(starts), i32(lens), SCALE)
+    for t in (0, 3, 4):
+        assert torch.equal(out2[t], out[t]) and torch.equal(l2[t], l[t])
+    for t in (1, 2, 5):
+        assert torch.isnan(out2[t]).any() and not torch.isfinite(l2[t]).any()
+
+
+@pytest.mark.parametrize("dtype", T16)
+def test_scores_of_many_sizes_in_every_split(wide, dtype):
+    lens = [700, 700, 700, 700]
+    table, starts, lens, n = batch(wide, lens, [1] * 4, 32, 4)
+    cache = filled(wide, n, 32, dtype, False, 17)
+    for r, f in enumerate((lambda p: p / 20, lambda p: -p / 20, lambda p: 40 * np.sin(p), lambda p: 100.0 * (p == 650))):
+        p = np.arange(700)
+        slots = torch.tensor(table[r][p // 32] * 32 + p % 32, device=DEV)
+        cache.rope[slots, 0] = torch.tensor(f(p), device=DEV).to(dtype)
+    for heads in (32, 64, 128):
+        x = rand((4, heads, 576), 18, dtype)
+        x[:, :, 512] = 8.0
+        check_latent(wide, cache, x, table, starts, lens)
+
+
+@pytest.mark.parametrize("heads,mx", [(16, False), (32, True), (64, False), (128, False), (128, True)])
+def test_equal_calls_give_equal_bits_in_every_split(wide, heads, mx):
+    test_equal_calls_give_equal_bits(wide, heads, mx)
