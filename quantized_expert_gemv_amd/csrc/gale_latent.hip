@@ -16,13 +16,16 @@ namespace gale {
 // alike; result register i of lane l: row 4 (l / 16) + i, column l % 16.  So a query is a lane's column in both, and the weights
 // are an operand of the second product as they are, where V^T takes the keys in the same order.
 //   Up to 16 rows: four key groups, tiles of 16 keys (V by the 16x16x16 MFMA), two for each wavefront, which no other one reads:
-//     no barrier; bound by HBM.
+//     no barrier; bound by HBM (64 requests of 1 to 8192 keys, 16 heads: 70 us, 4.8 TB/s; 7.1 where it only fetches: the
+//     rest is unequal parts and a part's start and end, 15 us).  4-bit rows are bound by their conversion and the products
+//     after it (128 requests of 1 to 16384 keys: 168 us; their bytes alone take 84).
 //   Up to 32 and 64: tiles of 32 keys for two and four row groups of 16.  Each MFMA of 16 cycles takes a 1 KB operand from LDS, twice
 //     its bandwidth, so the LDS is the bound once there are more rows than HBM's.
 //   More: eight wavefronts, two to a SIMD, four row groups of 32 queries: two MFMAs for each operand.  Queries (144 registers) and sums
 //     (256) of 32 do not fit one wavefront (300 to 580 registers spilled, also with half of the queries in LDS and with 32x32x16
 //     MFMAs), so two share them: each takes one half of the latent columns in both products, and they add their halves of the
-//     scores through LDS.
+//     scores through LDS.  One request of 131072 keys and 128 heads: 73 us, 495 TFLOP/s; bound by the barriers of each tile, with
+//     two wavefronts to a SIMD, and by the sums that leave (64 MB, 18 us of join).
 //
 // All runs' tiles form one line, cut into up to kGroups equal parts, one for each workgroup (one to a CU): a run that lies in several
 // parts leaves unnormalised sums in the workspace, two places to a workgroup (a run that began before its part, and one that goes
