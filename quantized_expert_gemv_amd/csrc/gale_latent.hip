@@ -79,7 +79,8 @@ __device__ __forceinline__ void run_units(const LatentParams& p, int r, int& blo
   units = max(1, (int)(((int64_t)keys + Sh::UNIT - 1) / Sh::UNIT));
 }
 
-__device__ uint32_t zero_row[2 * kLat / 4];      // never written
+alignas(16) __device__ uint32_t zero_row[2 * kLat / 4];      // never written
+static_assert(__alignof__(zero_row) >= 16, "16-byte copies read it");
 
 // Which 32 columns a product with K takes together is free: four chunks of 8, one for each lane group.  The groups that the LDS serves
 // at once, 0 and 1 or 2 and 3 with eight rows of each (all even and odd rows of four), must not meet where a chunk's bits
