@@ -112,6 +112,11 @@ __device__ __forceinline__ s16x4 lds_transposed(const lds_u8* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
 }
 
+// A query's sum of weights: 0 where it sees no key, and kNoScore (in sums: below 0) where it sees some, but all of their scores are
+// -infinity, which the maximum does not tell apart.  Its result is 0 or the formula's 0 / 0; what its sums are multiplied by:
+constexpr float kNoScore = -1.f;
+__device__ __forceinline__ float normaliser(float l) { return l > 0.f ? 1.f / l : l == 0.f ? 0.f : NAN; }
+
 // The other half's value of a lane's column.
 __device__ __forceinline__ float other_half(float v) { return lane_xor<32>(v); }
 

@@ -280,6 +280,7 @@ latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
 
     f32x4 o[G][BLOCKS] = {};
     float m[G], l[G];
+    int first_key = INT_MAX;      // that this wavefront has met
 #pragma unroll
     for (int g = 0; g < G; ++g) m[g] = -INFINITY, l[g] = 0.f;
 
@@ -363,6 +364,7 @@ latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
     // ---- the products with a tile: latents at `at`, rope rows at `rope` ----------------------------------------------------
     auto use = [&](int j0, uint32_t valid, const lds_u8* at, const lds_u8* rope) __attribute__((always_inline)) {
       at += 512 * ch;
+      if (valid != 0) first_key = min(first_key, j0 + __builtin_ctz(valid));
       // operands are read AHEAD in front of their products; the scheduler by itself would read each right before
       constexpr int U = KEYS / 16, NK = QB * U;
       // LDS places of operands.  K, block s: the lane group's chunk (block_chunk) of row col (+ 16); V^T, column block b of 16: chunks
@@ -656,6 +658,7 @@ latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
     for (int g = 0; g < G; ++g) {
       l[g] += lane_xor<16>(l[g]);
       l[g] += lane_xor<32>(l[g]);
+      if (__any(m[g] == -INFINITY) && m[g] == -INFINITY && l[g] == 0.f && first_key < seen_of(g)) l[g] = kNoScore;
       top[g] = m[g];
     }
     if constexpr (KG > 1) {
@@ -690,7 +693,7 @@ latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
       const int64_t q_row = here(Q * rg + 16 * g + col) + (int64_t)block * Sh::ROWS;
       const bool real = q_row < rows;
       const int row = (int)min(q_row, rows - 1), token = row / p.n_heads, head = row - token * p.n_heads;
-      const float r = l[g] == 0.f ? 0.f : 1.f / l[g];
+      const float r = normaliser(l[g]);
       uint16_t* out = p.out + (int64_t)(q0 + token) * p.out_stride + (int64_t)head * kLat + 4 * grp;
       auto leave = [&](int b, f32x4 v) {      // columns 16 b + 4 grp ..
         if (whole) {
@@ -785,7 +788,7 @@ __global__ void __launch_bounds__(1024) latent_join_kernel(const LatentParams p,
   const int64_t row = (int64_t)run.block * (Q * RG) + Q * rg + col;
   if (row >= (int64_t)n * p.n_heads) return;
   const int token = (int)row / p.n_heads, head = (int)row - token * p.n_heads;
-  const float r = l == 0.f ? 0.f : 1.f / l;
+  const float r = normaliser(l);
   mx_u32x2 h;
   h.x = (uint32_t)T::from_f32(acc.x * r) | ((uint32_t)T::from_f32(acc.y * r) << 16);
   h.y = (uint32_t)T::from_f32(acc.z * r) | ((uint32_t)T::from_f32(acc.w * r) << 16);

@@ -272,9 +272,10 @@ __global__ void __launch_bounds__(256, 2) prompt_kernel(const PromptParams p, in
   }
 
   l += other_half(l);
+  if (l == 0.f && seen > 0) l = kNoScore;
   if (qi < n) {
     const int64_t t = q0 + qi;
-    const float r = l == 0.f ? 0.f : 1.f / l;
+    const float r = normaliser(l);
     uint16_t* out = p.out + t * p.out_stride + (int64_t)head * kValue + 4 * half;
 #pragma unroll
     for (int b = 0; b < 4; ++b)

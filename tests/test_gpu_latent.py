@@ -862,3 +862,70 @@ def test_scores_of_many_sizes_in_every_split(wide, dtype):
 @pytest.mark.parametrize("heads,mx", [(16, False), (32, True), (64, False), (128, False), (128, True)])
 def test_equal_calls_give_equal_bits_in_every_split(wide, heads, mx):
     test_equal_calls_give_equal_bits(wide, heads, mx)
+
+
+# ---- scores that are all minus infinity: the formula is 0 / 0, which is not the 0 of a query that sees nothing ------------------------
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("heads", [16, 32, 64, 128])
+@pytest.mark.parametrize("wider", [False, True])
+def test_scores_that_are_all_minus_infinity(q, wide, wider, heads, mx):
+    """Request 0 sees such keys only, 1 none, 2 (in many parts) such keys and from key 900 on finite ones, 3 nothing but holes, 4 (in many
+    parts) such keys only, 5 three of them behind a hole."""
+    bs, lens = 16, [3, 0, 5000, 40, 6000, 19]
+    table, starts, lens, n = batch(q, lens, [1] * 6, bs, 4)
+    table[3, :3], table[5, 0] = -1, n
+    cache = filled(q, n, bs, torch.bfloat16, mx, 51)
+    for r, m in ((0, 3), (2, 900), (4, 6000), (5, 19)):
+        pos = np.arange(16 if r == 5 else 0, m)
+        cache.rope[torch.tensor(table[r][pos // bs] * bs + pos % bs, device=DEV), 3] = math.inf
+    x = rand((6, heads, 576), 52, torch.bfloat16)
+    x[:, :, 515] = -1.0
+    out, l = (wide if wider else q).latent_attention(x, cache, i32(table), i32(starts), i32(lens), SCALE)
+    for r in (0, 4, 5):
+        assert torch.isnan(out[r]).all() and not torch.isfinite(l[r]).any() and not (l[r] == math.inf).any(), r
+    for r in (1, 3):
+        assert not out[r].any() and (l[r] == -math.inf).all(), r
+    c, kr = cache_values(q, cache)
+    pos = np.arange(900, 5000)
+    rows = table[2][pos // bs] * bs + pos % bs
+    k = np.concatenate((c[rows], kr[rows]), 1)
+    for h in range(0, heads, 5):
+        want, wl, spread = O.attend(f64(x)[2, h], k, c[rows], SCALE)
+        bo, bl = bounds(np.abs(f64(x)[2, h]), np.abs(k), SCALE, x.dtype, spread, np.abs(c[rows]).sum(0), want, wl)
+        assert (np.abs(f64(out)[2, h] - want) <= bo).all() and abs(l[2, h].item() - wl) <= bl
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_drafts_whose_scores_are_all_minus_infinity(q, wide, mx):
+    """The first of three tokens sees no key, the second one of score -infinity, the third a finite one too; 40 heads."""
+    table, starts, lens, n = batch(q, [2], [3], 16, 4)
+    cache = filled(q, n, 16, torch.float16, mx, 53)
+    cache.rope[int(table[0, 0]) * 16, 3] = math.inf
+    x = rand((3, 40, 576), 54, torch.float16)
+    x[:, :, 515] = -1.0
+    for lib in (q, wide):
+        out, l = lib.latent_attention(x, cache, i32(table), i32(starts), i32(lens), SCALE)
+        assert not out[0].any() and (l[0] == -math.inf).all()
+        assert torch.isnan(out[1]).all() and not torch.isfinite(l[1]).any()
+        c, _ = cache_values(q, cache)
+        assert (f64(out[2]) == c[int(table[0, 0]) * 16 + 1]).all()        # one weight, exactly 1 after its division by itself
+
+
+@pytest.mark.parametrize("dtype", T16)
+def test_prompt_scores_that_are_all_minus_infinity(q, dtype):
+    lens, keys = [150, 2, 3], [150, 0, 1]
+    x, k, kr, v, s, ks = prompts(lens, keys, 2, dtype, 55)
+    kr[:100, 3] = math.inf
+    kr[150, 3] = math.inf
+    x[:, :, 128 + 3] = -1.0
+    out, l = q.latent_attention_expanded(x, k, kr, v, i32(s), i32(ks), SCALE)
+    assert torch.isnan(out[:100]).all() and not torch.isfinite(l[:100]).any()
+    assert not out[150:154].any() and (l[150:154] == -math.inf).all()      # no keys; three queries of one key: the last sees it
+    assert torch.isnan(out[154]).all() and not torch.isfinite(l[154]).any()
+    for t in range(100, 150, 7):
+        for h in range(2):
+            keys64 = np.concatenate((f64(k)[100: t + 1, h], f64(kr)[100: t + 1]), 1)
+            val = f64(v)[100: t + 1, h]
+            want, wl, spread = O.attend(f64(x)[t, h], keys64, val, SCALE)
+            bo, bl = bounds(np.abs(f64(x)[t, h]), np.abs(keys64), SCALE, dtype, spread, np.abs(val).sum(0), want, wl)
+            assert (np.abs(f64(out)[t, h] - want) <= bo).all() and abs(l[t, h].item() - wl) <= bl
