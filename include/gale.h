@@ -568,9 +568,9 @@ size_t gale_latent_workspace_bytes(int32_t n_tok, int32_t n_req, int32_t n_heads
  * gets out = 0 and lse = -infinity; one that sees a latent, or has a score, that is not finite gets NaN, or what the formula
  * gives.  kv_lens outside [0, max_blocks * block_size] are clamped to it, and max_blocks * block_size <= GALE_MAX_KEYS.
  * Products are exact and summed in fp32; the weights are rounded to the queries' type for the second product, relative to a
- * running maximum that is at most 2^8 below the true one, and normalised in fp32: their sums with bf16 values pass fp32's
- * range, and are infinite, where a value times the number of keys does.  4-bit latents are read as numbers of the queries'
- * type, gale_mx_dequantize's rounding.
+ * running maximum that is at most 2^8 below the true one, and normalised in fp32; the scale of the sums goes by the number of keys,
+ * so that bf16 values of any size stay in fp32's range.  4-bit latents are read as numbers of the queries' type,
+ * gale_mx_dequantize's rounding.
  * q: [n_tok] tokens, q_stride elements apart, of n_heads rows of GALE_LATENT_DIM + GALE_LATENT_ROPE values of the cache's
  * dtype; out: [n_tok] tokens, out_stride elements apart, of n_heads rows of GALE_LATENT_DIM; both 16-byte aligned with
  * strides of whole 16 bytes.  lse: fp32 [n_tok][n_heads], or NULL.  block_table: as gale_paged_plan's; q_starts: int32

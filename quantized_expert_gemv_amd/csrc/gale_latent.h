@@ -42,9 +42,9 @@ template <>
 struct Mma<F16> {
   typedef _Float16 v8 __attribute__((ext_vector_type(8)));
   typedef _Float16 v4 __attribute__((ext_vector_type(4)));
-  // weights are 2^(s - m + kLift) for a score s and the maximum m that is in use, at most kSlack below the true one; 2^7 puts the
+  // weights are 2^(s - m + lift) for a score s and the maximum m that is in use, at most kSlack below the true one; 2^7 puts the
   // smallest subnormal of fp16 at 2^-31 of the largest weight, and the largest at 2^15
-  static constexpr float kLift = 7.f;
+  static __device__ __forceinline__ float lift(int) { return 7.f; }
   static __device__ __forceinline__ f32x16 mma(s16x8 a, s16x8 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
   }
@@ -71,7 +71,10 @@ template <>
 struct Mma<BF16> {
   typedef __bf16 v8 __attribute__((ext_vector_type(8)));
   typedef __bf16 v4 __attribute__((ext_vector_type(4)));
-  static constexpr float kLift = -8.f;      // weights of at most 1: sums reach no further than the values
+  // weights of at most 1 / (2 keys), keys taken up to a power of two: sums of values, which may lie at the end of fp32's range, reach
+  // no further than the largest one (the 2 is for what rounding adds).  The price is at the other end: with 2^17 keys, products
+  // of values below 2^-100 leave fp32's normal range.
+  static __device__ __forceinline__ float lift(int keys) { return keys > 1 ? (float)(__builtin_clz(keys - 1) - 32 - 9) : -9.f; }
   static __device__ __forceinline__ f32x16 mma(s16x8 a, s16x8 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
   }

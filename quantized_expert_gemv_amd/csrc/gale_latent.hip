@@ -211,6 +211,7 @@ latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
     const int q0 = start_at(p.q_starts, req, p.n_tok), n = start_at(p.q_starts, req + 1, p.n_tok) - q0;
     const int keys = __builtin_amdgcn_readfirstlane(keys_of(p.kv_lens, req, p.max_blocks, p.block_shift));
     const int32_t* const table = p.table + (int64_t)req * p.table_stride;
+    const float lift = Mma<T>::lift(keys);
 
     // The blocks of the halves of unit i's tile (past the last key: the last key's; without a key: any number), each in one block where
     // those are large enough: scalar loads, ahead of their use, which no copy is waited for with.  In smaller blocks lane r of
@@ -451,7 +452,7 @@ latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
       float e[G][4 * U];
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        const float ref = (m[g] == -INFINITY ? 0.f : m[g]) - Mma<T>::kLift;
+        const float ref = (m[g] == -INFINITY ? 0.f : m[g]) - lift;
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < 4 * U; ++i) {
@@ -731,7 +732,7 @@ latent_kernel(const LatentParams p, const Workspace ws, bool by_run) {
           st[Q + 16 * g] = l[g];
         } else if (real && p.lse) {
           p.lse[(int64_t)(q0 + token) * p.n_heads + head] =
-              l[g] == 0.f ? -INFINITY : (top[g] - Mma<T>::kLift + __builtin_amdgcn_logf(l[g])) * 0.693147180559945309f;
+              l[g] == 0.f ? -INFINITY : (top[g] - lift + __builtin_amdgcn_logf(l[g])) * 0.693147180559945309f;
         }
       }
     }
@@ -793,9 +794,10 @@ __global__ void __launch_bounds__(1024) latent_join_kernel(const LatentParams p,
   h.x = (uint32_t)T::from_f32(acc.x * r) | ((uint32_t)T::from_f32(acc.y * r) << 16);
   h.y = (uint32_t)T::from_f32(acc.z * r) | ((uint32_t)T::from_f32(acc.w * r) << 16);
   *reinterpret_cast<mx_u32x2*>(p.out + (int64_t)(q0 + token) * p.out_stride + (int64_t)head * kLat + 16 * b + 4 * grp) = h;
+  const float lift = Mma<T>::lift(keys_of(p.kv_lens, run.req, p.max_blocks, p.block_shift));
   if (b == 0 && grp == 0 && p.lse)
     p.lse[(int64_t)(q0 + token) * p.n_heads + head] =
-        l == 0.f ? -INFINITY : (m - Mma<T>::kLift + __builtin_amdgcn_logf(l)) * 0.693147180559945309f;
+        l == 0.f ? -INFINITY : (m - lift + __builtin_amdgcn_logf(l)) * 0.693147180559945309f;
 }
 
 // Rows of a run, by those of an average request, `rows`, and by the batch's units of 16 rows and 64 positions of the block table

@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(256, 2) prompt_kernel(const PromptParams p, in
   const float c = p.scale == 0.f ? 1.f : fabsf(p.scale) * 1.44269504088896341f;
   if (wg_keys > 0) copy(0, smem);
 
+  const float lift = Mma<T>::lift(keys);
   f32x16 o[4] = {};
   float m = -INFINITY, l = 0.f;
 
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(256, 2) prompt_kernel(const PromptParams p, in
       l *= back;
       m = up;
     }
-    const float ref = (m == -INFINITY ? 0.f : m) - Mma<T>::kLift;
+    const float ref = (m == -INFINITY ? 0.f : m) - lift;
     s16x8 pt[4];
     float sum = 0.f;
 #pragma unroll
@@ -287,7 +288,7 @@ __global__ void __launch_bounds__(256, 2) prompt_kernel(const PromptParams p, in
         *reinterpret_cast<mx_u32x2*>(out + 32 * b + 8 * i) = v;
       }
     if (half == 0 && p.lse)
-      p.lse[t * p.n_heads + head] = l == 0.f ? -INFINITY : (m - Mma<T>::kLift + __builtin_amdgcn_logf(l)) * 0.693147180559945309f;
+      p.lse[t * p.n_heads + head] = l == 0.f ? -INFINITY : (m - lift + __builtin_amdgcn_logf(l)) * 0.693147180559945309f;
   }
 #endif
 }

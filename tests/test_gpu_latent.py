@@ -929,3 +929,69 @@ def test_prompt_scores_that_are_all_minus_infinity(q, dtype):
             want, wl, spread = O.attend(f64(x)[t, h], keys64, val, SCALE)
             bo, bl = bounds(np.abs(f64(x)[t, h]), np.abs(keys64), SCALE, dtype, spread, np.abs(val).sum(0), want, wl)
             assert (np.abs(f64(out)[t, h] - want) <= bo).all() and abs(l[t, h].item() - wl) <= bl
+
+
+# ---- values near the end of bf16: a weighted mean is no larger than the largest value ---------------------------------------------------
+def check_large_mean(out, lse, keys):
+    """The values were 2^127 in even columns and -2^127 in odd ones, the scores equal: out is those, rounded weights or not."""
+    want = torch.full((out.shape[-1],), 2.0 ** 127, device=DEV)
+    want[1::2] *= -1
+    # a sum over keys in fp32 is off by 2^-16 of itself at most (the file's bound), which is less than half a step of bf16
+    assert torch.equal(out.float(), want.expand(out.shape)), out
+    assert (lse - math.log(keys)).abs().max() <= 2.0 ** -18 * (1 + math.log(keys))
+
+
+@pytest.mark.parametrize("heads", [16, 32, 64, 128])
+@pytest.mark.parametrize("n", [1, 300, 2000, 70000])
+def test_means_of_the_largest_values(q, wide, heads, n):
+    table, starts, lens, blocks = batch(q, [n, 5], [1, 1], 64, 3)
+    cache = filled(q, blocks, 64, torch.bfloat16, False, 1)
+    cache.latent[:, ::2], cache.latent[:, 1::2] = 2.0 ** 127, -2.0 ** 127
+    x = rand((2, heads, 576), 2, torch.bfloat16)
+    x[..., :512] = 0
+    cache.rope[:] = 0
+    for lib in (q, wide):
+        out, lse = lib.latent_attention(x, cache, i32(table), i32(starts), i32(lens), SCALE)
+        check_large_mean(out[0], lse[0], n)
+        check_large_mean(out[1], lse[1], 5)
+
+
+@pytest.mark.parametrize("n", [1, 300, 2000, 70000])
+def test_prompt_means_of_the_largest_values(q, n):
+    x, k, kr, v, s, ks = prompts([2, 1], [n, 3], 3, torch.bfloat16, 3)
+    x[:] = 0
+    v[..., ::2], v[..., 1::2] = 2.0 ** 127, -2.0 ** 127
+    out, lse = q.latent_attention_expanded(x, k, kr, v, i32(s), i32(ks), SCALE, causal=False)
+    check_large_mean(out[:2], lse[:2], n)
+    check_large_mean(out[2], lse[2], 3)
+
+
+@pytest.mark.parametrize("heads", [16, 128])
+def test_means_of_the_largest_values_under_rising_scores(q, heads):
+    """Scores that rise by less than what the running maximum may lag behind: 5 in powers of two over 700 keys."""
+    table, starts, lens, blocks = batch(q, [700], [1], 64, 3)
+    cache = filled(q, blocks, 64, torch.bfloat16, False, 1)
+    cache.latent[:] = 1.5 * 2.0 ** 127
+    cache.rope[:] = 0
+    pos = np.arange(700)
+    cache.rope[torch.tensor(table[0][pos // 64] * 64 + pos % 64, device=DEV), 0] = torch.tensor(np.floor(pos / 50) / 4, device=DEV).bfloat16()
+    x = torch.zeros(1, heads, 576, dtype=torch.bfloat16, device=DEV)
+    x[..., 512] = 1.0
+    out, lse = q.latent_attention(x, cache, i32(table), i32(starts), i32(lens), 1.0)
+    # weights are rounded by 2^-9 relative, then the result: both to either side
+    assert ((out.float() / 2.0 ** 127 - 1.5).abs() <= 1.5 * (2.0 ** -9 + 2.0 ** -16) + 2.0 ** -8).all() and torch.isfinite(lse).all()
+    x, k, kr, v, s, ks = prompts([200], [700], 2, torch.bfloat16, 4)
+    x[:], x[..., 128], v[:], kr[:] = 0, 1.0, 1.5 * 2.0 ** 127, 0
+    kr[:, 0] = torch.tensor(np.floor(pos / 50) / 4, device=DEV).bfloat16()
+    out, lse = q.latent_attention_expanded(x, k, kr, v, i32(s), i32(ks), 1.0)
+    assert ((out.float() / 2.0 ** 127 - 1.5).abs() <= 1.5 * (2.0 ** -9 + 2.0 ** -16) + 2.0 ** -8).all() and torch.isfinite(lse).all()
+
+
+def test_means_of_the_largest_values_in_4_bits(q):
+    """MX codes of 6 times 2^125: 1.5 times 2^127."""
+    table, starts, lens, blocks = batch(q, [3000, 5], [1, 1], 64, 3)
+    cache = filled(q, blocks, 64, torch.bfloat16, True, 1)
+    cache.latent.codes[:], cache.latent.scales[:], cache.rope[:] = 0x77, 127 + 125, 0
+    x = torch.zeros(2, 16, 576, dtype=torch.bfloat16, device=DEV)
+    out, lse = q.latent_attention(x, cache, i32(table), i32(starts), i32(lens), SCALE)
+    assert (out.float() == 1.5 * 2.0 ** 127).all()
