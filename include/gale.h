@@ -566,14 +566,14 @@ size_t gale_latent_workspace_bytes(int32_t n_tok, int32_t n_req, int32_t n_heads
  * Query i of a request's n sees keys j <= kv_len - n + i when causal != 0, else all kv_len.  A key whose block id is outside
  * [0, n_blocks) is not seen.  What a query does not see has no influence on it, NaN included; a query that sees no key
  * gets out = 0 and lse = -infinity; one that sees a latent, or has a score, that is not finite gets NaN, or what the formula
- * gives.  kv_lens outside [0, max_blocks * block_size] are clamped to it, and max_blocks * block_size <= GALE_MAX_KEYS.
+ * gives; scores past 2^127 in size, and sums of products past fp32's range, count as infinite.  kv_lens outside [0, max_blocks * block_size] are clamped to it, and max_blocks * block_size <= GALE_MAX_KEYS.
  * Products are exact and summed in fp32; the weights are rounded to the queries' type for the second product, relative to a
  * running maximum that is at most 2^8 below the true one, and normalised in fp32; the scale of the sums goes by the number of keys,
  * so that bf16 values of any size stay in fp32's range.  4-bit latents are read as numbers of the queries' type,
  * gale_mx_dequantize's rounding.
  * q: [n_tok] tokens, q_stride elements apart, of n_heads rows of GALE_LATENT_DIM + GALE_LATENT_ROPE values of the cache's
  * dtype; out: [n_tok] tokens, out_stride elements apart, of n_heads rows of GALE_LATENT_DIM; both 16-byte aligned with
- * strides of whole 16 bytes.  lse: fp32 [n_tok][n_heads], or NULL.  block_table: as gale_paged_plan's; q_starts: int32
+ * strides of whole 16 bytes.  scale: at most 2^127 in size.  lse: fp32 [n_tok][n_heads], or NULL.  block_table: as gale_paged_plan's; q_starts: int32
  * [n_req + 1], ascending from 0, values outside [0, n_tok] are clamped; tokens from q_starts[n_req] on are left as they
  * were.  n_heads <= GALE_MAX_HEADS, n_tok * n_heads < 2^31, n_req <= GALE_MAX_REQUESTS; n_req and n_tok may be 0.  ws: 256-byte
  * aligned; nothing in it lives from call to call, and calls that may run at the same time need one each.  Equal calls give

@@ -1181,6 +1181,9 @@ static bool attention_sizes_ok(int32_t n_tok, int32_t n_req, int32_t n_heads) {
          (int64_t)n_tok * n_heads <= INT32_MAX;
 }
 
+// The kernels take scores in powers of two: the scale times log2(e) is finite too.
+static bool scale_ok(float scale) { return fabsf(scale) <= 0x1p127f; }
+
 extern "C" size_t gale_latent_workspace_bytes(int32_t n_tok, int32_t n_req, int32_t n_heads) {
   if (!attention_sizes_ok(n_tok, n_req, n_heads)) return 0;
   return latent_workspace_bytes(n_tok, n_req, n_heads);
@@ -1202,7 +1205,7 @@ extern "C" int gale_latent_attention(const gale_latent_cache* cache, const int32
               n_heads, max_blocks, (long long)table_stride, (long long)q_stride, (long long)out_stride);
     return GALE_ERR_SHAPE;
   }
-  if (!(fabsf(scale) < INFINITY)) { set_error("%s: scale must be finite", fn); return GALE_ERR_SHAPE; }
+  if (!scale_ok(scale)) { set_error("%s: scale must be at most 2^127 in size", fn); return GALE_ERR_SHAPE; }
   if (n_tok == 0 || n_req == 0) return GALE_OK;
   if (!q || !out || !kv_lens || !q_starts || (max_blocks && !block_table)) { set_error("%s: NULL pointer", fn); return GALE_ERR_NULL; }
   if (!rows16(q, q_stride) || !rows16(out, out_stride) || !aligned(block_table, 4) || !aligned(kv_lens, 4) ||
@@ -1251,7 +1254,7 @@ extern "C" int gale_latent_attention_expanded(const void* q, int64_t q_stride, c
               (long long)k_rope_stride, (long long)v_stride, (long long)v_head_stride, (long long)out_stride);
     return GALE_ERR_SHAPE;
   }
-  if (!(fabsf(scale) < INFINITY)) { set_error("%s: scale must be finite", fn); return GALE_ERR_SHAPE; }
+  if (!scale_ok(scale)) { set_error("%s: scale must be at most 2^127 in size", fn); return GALE_ERR_SHAPE; }
   if (n_tok == 0 || n_req == 0) return GALE_OK;
   if (!q || !out || !q_starts || !kv_starts || (n_kv && (!k || !k_rope || !v))) { set_error("%s: NULL pointer", fn); return GALE_ERR_NULL; }
   if (!rows16(q, q_stride) || !rows16(out, out_stride) || !rows16(k, k_stride) || k_head_stride % 8 || !rows16(v, v_stride) ||

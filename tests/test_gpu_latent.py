@@ -995,3 +995,29 @@ def test_means_of_the_largest_values_in_4_bits(q):
     x = torch.zeros(2, 16, 576, dtype=torch.bfloat16, device=DEV)
     out, lse = q.latent_attention(x, cache, i32(table), i32(starts), i32(lens), SCALE)
     assert (out.float() == 1.5 * 2.0 ** 127).all()
+
+
+@pytest.mark.parametrize("heads", [16, 128])
+def test_the_largest_scale_and_scores(q, heads):
+    """Scores of 0 under a scale of 2^127 give the mean; scores of 2^126 and -2^126 the first value."""
+    table, starts, lens, n = batch(q, [2], [1], 16, 3)
+    cache = filled(q, n, 16, torch.bfloat16, False, 57)
+    rows = int(table[0, 0]) * 16 + np.arange(2)
+    cache.latent[rows] = rand((2, 512), 58).round().bfloat16()            # whole numbers: their mean is exact in fp32
+    x = torch.zeros(1, heads, 576, dtype=torch.bfloat16, device=DEV)
+    for scale in (2.0 ** 127, -2.0 ** 127):
+        out, lse = q.latent_attention(x, cache, i32(table), i32(starts), i32(lens), scale)
+        assert torch.equal(out[0], (cache.latent[rows].float().sum(0) / 2).bfloat16().expand(heads, 512))
+        assert torch.allclose(lse, torch.full_like(lse, math.log(2.0)), rtol=2.0 ** -18)
+    cache.rope[rows, 0] = torch.tensor([2.0 ** 63, -2.0 ** 63], device=DEV).bfloat16()
+    x[..., 512] = 2.0 ** 63
+    out, lse = q.latent_attention(x, cache, i32(table), i32(starts), i32(lens), 1.0)
+    assert torch.equal(out[0], cache.latent[rows[0]].expand(heads, 512)) and ((lse / 2.0 ** 126 - 1).abs() <= 2.0 ** -21).all()
+    y, k, kr, v, s, ks = prompts([1], [2], 2, torch.bfloat16, 59)
+    y[:] = 0
+    v[:] = rand((2, 2, 128), 60).round().bfloat16()
+    out, lse = q.latent_attention_expanded(y, k, kr, v, i32(s), i32(ks), 2.0 ** 127, causal=False)
+    assert torch.equal(out[0], (v.float().sum(0) / 2).bfloat16()) and torch.allclose(lse, torch.full_like(lse, math.log(2.0)), rtol=2.0 ** -18)
+    y[..., 128], kr[:, 0] = 2.0 ** 63, torch.tensor([2.0 ** 63, -2.0 ** 63], device=DEV).bfloat16()
+    out, lse = q.latent_attention_expanded(y, k, kr, v, i32(s), i32(ks), 1.0, causal=False)
+    assert torch.equal(out[0], v[0]) and ((lse / 2.0 ** 126 - 1).abs() <= 2.0 ** -21).all()

@@ -227,3 +227,14 @@ def test_attention_refuses_tables_past_the_last_position():
     good = [_cache(), F + 40 * MB, 8, 8, F + 41 * MB, F + 42 * MB, 1, F + 43 * MB, 16 * 576, 1, 16, 0.1, 1, F + 44 * MB, 16 * 512,
             None, F + 46 * MB, need, None]
     _refused("gale_latent_attention", good, [(SHAPE, {2: wide, 3: wide})])
+
+
+def test_scales_without_a_finite_logarithm_base_are_refused():
+    """Scores are taken in powers of two: a scale times log2(e) has to be finite."""
+    need = q.latent_workspace_bytes(1, 1, 16)
+    good = [_cache(), F + 40 * MB, 8, 8, F + 41 * MB, F + 42 * MB, 1, F + 43 * MB, 16 * 576, 1, 16, 0.1, 1, F + 44 * MB, 16 * 512,
+            None, F + 46 * MB, need, None]
+    _refused("gale_latent_attention", good, [(SHAPE, {11: 2.0 ** 127 * 1.01}), (SHAPE, {11: -3.4e38})])
+    good = [F, 16 * 192, F + MB, 4096, 256, F + 2 * MB, 64, F + MB + 256, 4096, 256, 3, 10, 20, 16, F + 4 * MB, F + 5 * MB, 2, 0.1, 1,
+            F + 6 * MB, 16 * 128, F + 7 * MB, None]
+    _refused("gale_latent_attention_expanded", good, [(SHAPE, {17: 2.0 ** 127 * 1.01}), (SHAPE, {17: -3.4e38})])
