@@ -133,7 +133,9 @@ __global__ void __launch_bounds__(256, 2) prompt_kernel(const PromptParams p, in
   const int vk = kr * kb + 16 * ((lane & 15) ^ swizzle(kr)), vv = kr * vb + 16 * ((lane & 15) ^ swizzle(kr));
   const int vr = rr * rb + 16 * ((lane & 7) ^ swizzle8(rr));
   auto copy = [&](int j0, lds_u8* to) {
-    const int rows = min(kBk, keys - j0);      // rows behind the last key come as zeros
+    // rows behind the last key come as zeros, also where a copy's scalar offset alone is past the end: it counts in the range check
+    // (measured for 1 to 64 rows, 256 bytes to 32 MB apart)
+    const int rows = min(kBk, keys - j0);
     const auto rk = __builtin_amdgcn_make_buffer_rsrc((void*)(p.k + (int64_t)(k0 + j0) * p.k_stride + head * p.k_head), 0,
                                                       (rows - 1) * kb + 256, 0x00020000);
     const auto rv = __builtin_amdgcn_make_buffer_rsrc((void*)(p.v + (int64_t)(k0 + j0) * p.v_stride + head * p.v_head), 0,

@@ -1021,3 +1021,52 @@ def test_the_largest_scale_and_scores(q, heads):
     y[..., 128], kr[:, 0] = 2.0 ** 63, torch.tensor([2.0 ** 63, -2.0 ** 63], device=DEV).bfloat16()
     out, lse = q.latent_attention_expanded(y, k, kr, v, i32(s), i32(ks), 1.0, causal=False)
     assert torch.equal(out[0], v[0]) and ((lse / 2.0 ** 126 - 1).abs() <= 2.0 ** -21).all()
+
+
+# ---- a request's neighbours ----------------------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("keys", [1, 15, 16, 17, 33, 49, 63, 64, 65, 100])
+@pytest.mark.parametrize("n,causal", [(3, False), (40, False), (1, True)])
+def test_rows_of_the_next_request_have_no_influence(q, keys, n, causal):
+    """The last tile of a request ends inside its 64 rows: NaN and infinity behind its last key leave every bit as it is."""
+    x, k, kr, v, s, ks = prompts([n, 2, 1], [keys, 70, 64], 2, torch.float16, keys)
+    a, la = q.latent_attention_expanded(x, k, kr, v, i32(s), i32(ks), SCALE, causal)
+    k[keys:], kr[keys:], v[keys:] = math.nan, math.inf, math.nan
+    v[keys + 1::3] = math.inf
+    b, lb = q.latent_attention_expanded(x, k, kr, v, i32(s), i32(ks), SCALE, causal)
+    assert torch.isfinite(a).all() and torch.equal(a[:n], b[:n]) and torch.equal(la[:n], lb[:n])
+
+
+# ---- more than 256 runs: records by the part that a run begins in --------------------------------------------------------------------------
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("dtype", T16)
+@pytest.mark.parametrize("heads", [16, 24, 48, 128])                      # runs of 16, 32, 64 and 128 rows under a wide table
+def test_more_runs_than_records(wide, dtype, mx, heads):
+    rng = np.random.default_rng(heads)
+    R = 300
+    lens = rng.integers(0, 40, R)
+    lens[[3, 150, 297]] = 3000, 5000, 2100                                # these are cut into parts
+    news = np.ones(R, dtype=np.int64)
+    news[[10, 20, 150]], news[[30, 40, 299]] = 2, 0
+    table, starts, lens, n = batch(wide, list(lens), list(news), 16, heads)
+    cache = filled(wide, n, 16, dtype, mx, 61)
+    T = int(starts[-1])
+    x = rand((T, heads, 576), 62, dtype)
+    need = wide.latent_workspace_bytes(T, R, heads)
+    around = torch.full((need + 512,), 0xA5, dtype=torch.uint8, device=DEV)
+    tokens = {0, 3, int(starts[150]), int(starts[150]) + 1, int(starts[297]), T - 1, *map(int, rng.integers(0, T, 12))}
+    check_latent(wide, cache, x, table, starts, lens, tokens=tokens, ws=around[256: 256 + need])
+    assert (around[:256] == 0xA5).all() and (around[256 + need:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("heads", [16, 32, 64, 128])
+def test_the_workspace_is_all_that_is_written(wide, heads):
+    """Few long runs, each in many parts."""
+    table, starts, lens, n = batch(wide, [9000, 20000], [1, 1], 64, heads)
+    cache = filled(wide, n, 64, torch.bfloat16, False, 63)
+    x = rand((2, heads, 576), 64, torch.bfloat16)
+    need = wide.latent_workspace_bytes(2, 2, heads)
+    around = torch.full((need + 512,), 0xA5, dtype=torch.uint8, device=DEV)
+    a, la = wide.latent_attention(x, cache, i32(table), i32(starts), i32(lens), SCALE, ws=around[256: 256 + need])
+    assert (around[:256] == 0xA5).all() and (around[256 + need:] == 0xA5).all()
+    b, lb = wide.latent_attention(x, cache, i32(table), i32(starts), i32(lens), SCALE)
+    assert torch.equal(a, b) and torch.equal(la, lb)

@@ -238,3 +238,12 @@ def test_scales_without_a_finite_logarithm_base_are_refused():
     good = [F, 16 * 192, F + MB, 4096, 256, F + 2 * MB, 64, F + MB + 256, 4096, 256, 3, 10, 20, 16, F + 4 * MB, F + 5 * MB, 2, 0.1, 1,
             F + 6 * MB, 16 * 128, F + 7 * MB, None]
     _refused("gale_latent_attention_expanded", good, [(SHAPE, {17: 2.0 ** 127 * 1.01}), (SHAPE, {17: -3.4e38})])
+
+
+def test_workspace_sizes_of_each_shape():
+    """Records (256 + 256 of 16 bytes), then two places for each of 256 workgroups: maxima and sums of weights, and 512 sums of 4
+    bytes, for each row of a run."""
+    for (tokens, requests, heads), rows in {(1, 1, 16): 16, (4, 4, 1): 16, (1, 1, 32): 32, (64, 64, 17): 32, (1, 1, 64): 64,
+                                            (2, 1, 32): 64, (1, 1, 33): 64, (1, 1, 128): 128, (8, 8, 128): 128, (300, 300, 128): 128,
+                                            (0, 0, 16): 16, (1, 65536, 1024): 16}.items():
+        assert q.latent_workspace_bytes(tokens, requests, heads) == 256 + 4096 + 512 * rows * (8 + 4 * 512), (tokens, requests, heads)
