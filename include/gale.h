@@ -533,8 +533,9 @@ typedef struct {
  *   q_starts[r] = the sum of the new lengths before it, at most n_tok; q_starts[n_req] = the sum of all, likewise;
  *   it is refused if its blocks ceil((past + new) / block_size) pass max_blocks, or its tokens n_tok;
  *   the others need ceil((past + new) / block_size) - ceil(past / block_size) more blocks.  They take them from free_blocks in
- *         the order of the requests; those whose need is not met by the *n_free (at most free_cap) entries are refused;
- *         a request that needs none is not;
+ *         the order of the requests, and a request is refused when its need and the needs before it, met or not, pass the *n_free
+ *         (at most free_cap) entries: from the first that is refused for them on, all that need a block are (none is overtaken
+ *         by a later, smaller one); a request that needs none is not;
  *   kv_lens[r] = past + new, or past for a refused request;  the new blocks' ids are put into its row of block_table, the
  *         table's other entries stay as they are.
  * slots[t], for each of the n_tok places of the batch, is where token t goes: -1 behind the last token, for the tokens of
@@ -566,7 +567,8 @@ size_t gale_latent_workspace_bytes(int32_t n_tok, int32_t n_req, int32_t n_heads
  * Query i of a request's n sees keys j <= kv_len - n + i when causal != 0, else all kv_len.  A key whose block id is outside
  * [0, n_blocks) is not seen.  What a query does not see has no influence on it, NaN included; a query that sees no key
  * gets out = 0 and lse = -infinity; one that sees a latent, or has a score, that is not finite gets NaN, or what the formula
- * gives; scores past 2^127 in size, and sums of products past fp32's range, count as infinite.  kv_lens outside [0, max_blocks * block_size] are clamped to it, and max_blocks * block_size <= GALE_MAX_KEYS.
+ * gives (NaN where all of its scores are -infinity); scores past 2^127 in size, and sums of products past fp32's range, count as
+ * infinite.  kv_lens outside [0, max_blocks * block_size] are clamped to it, and max_blocks * block_size <= GALE_MAX_KEYS.
  * Products are exact and summed in fp32; the weights are rounded to the queries' type for the second product, relative to a
  * running maximum that is at most 2^8 below the true one, and normalised in fp32; the scale of the sums goes by the number of keys,
  * so that bf16 values of any size stay in fp32's range.  4-bit latents are read as numbers of the queries' type,

@@ -900,8 +900,9 @@ def paged_plan(past_lens: torch.Tensor, new_lens: torch.Tensor, free_blocks: tor
     """(slots int64 [n_tok], q_starts int32 [R + 1], kv_lens int32 [R], taken int32 [1]) of a batch of R requests with
     past_lens tokens in the cache and new_lens in the batch (int32 [R]); new blocks come from the front of free_blocks
     (int32, the first n_free[0] of them) and are put into block_table (int32 [R, max_blocks]) in place.  Refused requests
-    (no room in the table, the batch or the free blocks) keep kv_lens = past_lens and get slots of -1.  out: the four
-    outputs' tensors."""
+    (no room in the table, the batch or the free blocks; once these do not last for a request, all later ones that need
+    some are refused) keep kv_lens = past_lens and get slots of -1, as do places behind the last token.  out: the four outputs'
+    tensors."""
     R, dev = past_lens.shape[0] if past_lens.dim() else 0, past_lens.get_device()
     _int32_vector("past_lens", past_lens, R)
     _int32_vector("new_lens", new_lens, R)
@@ -990,7 +991,8 @@ def latent_attention(q: torch.Tensor, cache: LatentCache, block_table: torch.Ten
                      lse: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
     """(out [T, H, 512], lse fp32 [T, H]): absorbed latent attention of q [T, H, 576] over the cached vectors of each
     request (block_table int32 [R, max_blocks]; q_starts int32 [R + 1] and kv_lens int32 [R] as paged_plan gives them).
-    Query i of a request's n sees its first kv_len - n + i + 1 keys, or all with causal=False."""
+    Query i of a request's n sees its first kv_len - n + i + 1 keys, or all with causal=False.  Rows of tokens from
+    q_starts[R] on (a padded batch) are left as they are in out and lse, and are not initialised where those are not given."""
     R, dev = kv_lens.shape[0] if kv_lens.dim() else 0, cache.device_index
     q = _head_rows("q", q, GALE_LATENT_DIM + GALE_LATENT_ROPE, cache.dtype, False)
     T, H = q.shape[:2]
@@ -1013,7 +1015,8 @@ def latent_attention_expanded(q: torch.Tensor, k: torch.Tensor, k_rope: torch.Te
     """(out [T, H, 128], lse fp32 [T, H]): latent attention of prompts with keys and values of every head, q [T, H, 192],
     k [S, H, 128], k_rope [S, 64] (shared by the heads), v [S, H, 128]; k and v may be halves of one product's output
     [S, H, 256].  Request r's queries are tokens q_starts[r] .. q_starts[r + 1] - 1, its keys kv_starts[r] .. likewise
-    (int32 [R + 1]); query i of n sees the first n_keys - n + i + 1 of them, or all with causal=False."""
+    (int32 [R + 1]); query i of n sees the first n_keys - n + i + 1 of them, or all with causal=False.  Rows of tokens from
+    q_starts[R] on are left as they are in out and lse, and are not initialised where those are not given."""
     R, dev = q_starts.numel() - 1, q.get_device()
     code = _dt3(q)
     q = _head_rows("q", q, GALE_HEAD_NOPE + GALE_LATENT_ROPE, q.dtype, False)

@@ -18,14 +18,17 @@ namespace gale {
 //   Up to 16 rows: four key groups, tiles of 16 keys (V by the 16x16x16 MFMA), two for each wavefront, which no other one reads:
 //     no barrier; bound by HBM (64 requests of 1 to 8192 keys, 16 heads: 70 us, 4.8 TB/s; 7.1 where it only fetches: the
 //     rest is unequal parts and a part's start and end, 15 us).  4-bit rows are bound by their conversion and the products
-//     after it (128 requests of 1 to 16384 keys: 168 us; their bytes alone take 84).
+//     after it (128 requests of 1 to 16384 keys: 176 us with the join; their bytes alone take 84).
 //   Up to 32 and 64: tiles of 32 keys for two and four row groups of 16.  Each MFMA of 16 cycles takes a 1 KB operand from LDS, twice
-//     its bandwidth, so the LDS is the bound once there are more rows than HBM's.
+//     its bandwidth, so the LDS is the bound once there are more rows than HBM's (32 requests of 1 to 4096 keys, 32 and 64 heads:
+//     36 and 46 us; 4-bit rows 38 and 51).
 //   More: eight wavefronts, two to a SIMD, four row groups of 32 queries: two MFMAs for each operand.  Queries (144 registers) and sums
 //     (256) of 32 do not fit one wavefront (300 to 580 registers spilled, also with half of the queries in LDS and with 32x32x16
 //     MFMAs), so two share them: each takes one half of the latent columns in both products, and they add their halves of the
 //     scores through LDS.  One request of 131072 keys and 128 heads: 73 us, 495 TFLOP/s; bound by the barriers of each tile, with
 //     two wavefronts to a SIMD, and by the sums that leave (64 MB, 18 us of join).
+// Block ids of pages below 8 slots (16 for tiles of 32 keys) are vector loads, which return behind the copies in flight: 64 requests
+// in pages of one slot take 79 us for 74, in 4 bits 68 for 61.
 //
 // All runs' tiles form one line, cut into up to kGroups equal parts, one for each workgroup (one to a CU): a run that lies in several
 // parts leaves unnormalised sums in the workspace, two places to a workgroup (a run that began before its part, and one that goes
@@ -801,7 +804,8 @@ __global__ void __launch_bounds__(1024) latent_join_kernel(const LatentParams p,
 }
 
 // Rows of a run, by those of an average request, `rows`, and by the batch's units of 16 rows and 64 positions of the block table
-// (a wider table than the lengths need counts as long contexts).  Few units: the most workgroups and the least time until the first
+// (a wider table than the lengths need counts as long contexts).  4-bit rows go by the same rule, which was not measured for
+// them.  Few units: the most workgroups and the least time until the first
 // product, though a tile is fetched by many; many: tiles that all rows of a run share.  us, bf16, 16-bit rows, 64-slot blocks:
 //   units (requests x rows, positions)          runs of 16      32      64     128 rows
 //     256 (4 x 32, 2048)                            20.3    24.7    27.4    37.4
